@@ -471,13 +471,212 @@ ssm_status_t ssm_layer_fwd(const ssm_layer_params_t *p, void *stream);
 size_t ssm_layer_workspace_size(const ssm_layer_params_t *p);
 ssm_status_t ssm_layer_check(const ssm_layer_params_t *p);
 
+/* ------------------------------------------------------------------------
+ * Gated delta rule: the multi-head linear recurrence whose input is the error
+ * of the state's own prediction.  Per sequence and value head h, state S (V, K):
+ *   S <- e^{g_t} S;  u_t = beta_t (v_t - S k_t);  S <- S + u_t k_t^T;  o_t = scale S q_t
+ *   q, k      (Bt, L, Hk, K) x_dtype, v (Bt, L, H, V) x_dtype; head h reads key
+ *             head h / (H / Hk).  *_stride: elements from one token to the next
+ *             (the same across sequences), 0 for a dense tensor: rows of a
+ *             wider projection are taken where they are
+ *   g, beta   (Bt, L, H) f32: the log of the decay (<= 0 in a model; -inf forgets
+ *             the state) and the write strength
+ *   qk_norm   nonzero: q and k rows are first divided by sqrt(|row|^2 + eps)
+ *   cu_seqlens (num_seqs + 1) int32 in DEVICE memory or NULL: packed sequences,
+ *             Bt = 1, sequence i holds the tokens [cu[i], cu[i+1]); offsets rise
+ *             from 0 to L (empty sequences allowed).  They are not read on the
+ *             host; offsets out of range are clamped, tokens outside every
+ *             sequence are not written.  NULL: num_seqs = Bt
+ *   state_in  (num_seqs, H, V, K) f32 or NULL (zeros); state_out the same or NULL;
+ *             may alias state_in exactly
+ *   o         (Bt, L, H, V) o_dtype, dense
+ * The sequence is taken in chunks of 64 tokens whose corrections u solve one
+ * triangular system each, with matrix products throughout.  bf16 operands are
+ * exact; 32-bit operands (f32 inputs, the state, u) enter the matrix cores as
+ * two or three bf16 parts, so an f32 result carries f32 accuracy.
+ * Workspace: ssm_delta_chunk_workspace_size() bytes, 256-byte aligned (about
+ * 31 KB per chunk and head and 48 KB per chunk and key head at K = 128 in bf16).
+ * Supported: K <= 128, any V, x_dtype f32 or bf16, L == 0 copies the state.
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_delta_chunk_params {
+  uint32_t struct_size; /* = sizeof(ssm_delta_chunk_params_t) */
+  int32_t batch, seqlen, num_seqs, nkheads, nheads, d_key, d_value;
+  const void *q, *k, *v;
+  int32_t x_dtype;
+  int64_t q_stride, k_stride, v_stride;
+  const float *g, *beta;
+  float scale;
+  int32_t qk_norm;
+  float eps;
+  const int32_t *cu_seqlens;
+  const float *state_in;
+  float *state_out;
+  void *o;
+  int32_t o_dtype;
+  void *workspace;
+  size_t workspace_bytes;
+} ssm_delta_chunk_params_t;
+
+ssm_status_t ssm_delta_chunk_fwd(const ssm_delta_chunk_params_t *p, void *stream);
+size_t ssm_delta_chunk_workspace_size(const ssm_delta_chunk_params_t *p);
+ssm_status_t ssm_delta_chunk_check(const ssm_delta_chunk_params_t *p);
+
+/* ------------------------------------------------------------------------
+ * Backward of ssm_delta_chunk_fwd, recomputing the states of the chunks.  Given
+ * dout = dL/do (Bt, L, H, V) x_dtype and optionally dstate_out (num_seqs, H, V, K)
+ * f32, writes dq, dk (Bt, L, Hk, K) and dv (Bt, L, H, V) in grad_dtype, dense, and
+ * dg, dbeta (Bt, L, H) and dstate_in (num_seqs, H, V, K) in f32; any may be NULL.
+ * Key heads shared by several value heads receive the sum over them, in a fixed
+ * order (no atomics: results repeat bit for bit).  The other fields are those of
+ * the forward.  Workspace: ssm_delta_chunk_bwd_workspace_size() bytes (the
+ * forward's, and two (K, V) states and two (64, V) tiles in f32 per chunk and head).
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_delta_chunk_bwd_params {
+  uint32_t struct_size; /* = sizeof(ssm_delta_chunk_bwd_params_t) */
+  int32_t batch, seqlen, num_seqs, nkheads, nheads, d_key, d_value;
+  const void *q, *k, *v;
+  int32_t x_dtype;
+  int64_t q_stride, k_stride, v_stride;
+  const float *g, *beta;
+  float scale;
+  int32_t qk_norm;
+  float eps;
+  const int32_t *cu_seqlens;
+  const float *state_in;
+  const void *dout;
+  const float *dstate_out;
+  void *dq, *dk, *dv;
+  int32_t grad_dtype;
+  float *dg, *dbeta, *dstate_in;
+  void *workspace;
+  size_t workspace_bytes;
+} ssm_delta_chunk_bwd_params_t;
+
+ssm_status_t ssm_delta_chunk_bwd(const ssm_delta_chunk_bwd_params_t *p, void *stream);
+size_t ssm_delta_chunk_bwd_workspace_size(const ssm_delta_chunk_bwd_params_t *p);
+ssm_status_t ssm_delta_chunk_bwd_check(const ssm_delta_chunk_bwd_params_t *p);
+
+/* ------------------------------------------------------------------------
+ * One token of the gated delta rule for each of Bt sequences, in place (the
+ * result equals ssm_delta_chunk_fwd with L = 1 and state_in = state_out = state):
+ *   q, k (Bt, Hk, K), v (Bt, H, V) x_dtype with *_stride elements from one
+ *   sequence to the next (0: dense); g, beta (Bt, H) f32; state (Bt, H, V, K) f32,
+ *   read then overwritten; o (Bt, H, V) o_dtype, dense.  All arithmetic is f32.
+ * Supported: K <= 128; Bt * H * V < 2^27.
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_delta_decode_params {
+  uint32_t struct_size; /* = sizeof(ssm_delta_decode_params_t) */
+  int32_t batch, nkheads, nheads, d_key, d_value;
+  const void *q, *k, *v;
+  int32_t x_dtype;
+  int64_t q_stride, k_stride, v_stride;
+  const float *g, *beta;
+  float scale;
+  int32_t qk_norm;
+  float eps;
+  float *state;
+  void *o;
+  int32_t o_dtype;
+} ssm_delta_decode_params_t;
+
+ssm_status_t ssm_delta_decode_step(const ssm_delta_decode_params_t *p, void *stream);
+ssm_status_t ssm_delta_decode_check(const ssm_delta_decode_params_t *p);
+
+/* ------------------------------------------------------------------------
+ * The norms before and after a block, fused with its gate and residual scale.
+ * On each of `rows` rows of `width` values, norm(r) = r / sqrt(mean(r^2) + eps):
+ *   y = x              (y = x SiLU(z) with gate_first)
+ *   a = norm(y) norm_w (in groups of group_size consecutive values each)
+ *   a = a SiLU(z)      (without gate_first)
+ *   t = residual + scale a,  residual_out = t
+ *   out = norm(t) out_norm_w   (out = t without out_norm_w)
+ * Every part may be left out (NULL): norm_w, z, residual, scale, out_norm_w.  The
+ * mixer's gated norm is x, z and norm_w in groups of a head; the end of a block
+ * with the next one's norm is all of it.
+ *   x, z      (rows, width) x_dtype, *_stride elements between rows (0: dense)
+ *   norm_w    f32, norm_w_len = group_size (shared by the groups) or width
+ *   residual  (rows, width) res_dtype; residual_out the same, may alias residual
+ *             exactly; NULL: not written
+ *   scale, out_norm_w (width) f32;  out (rows, width) out_dtype or NULL
+ * All arithmetic is f32; out is normalised from t before t is rounded to res_dtype.
+ * Supported: group_size <= 16384, dividing width; group_size = width where
+ * residual, scale or out_norm_w is given.
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_block_norm_params {
+  uint32_t struct_size; /* = sizeof(ssm_block_norm_params_t) */
+  int64_t rows;
+  int32_t width, group_size;
+  const void *x;
+  int32_t x_dtype;
+  int64_t x_stride;
+  const void *z;
+  int64_t z_stride;
+  int32_t gate_first;
+  const float *norm_w;
+  int32_t norm_w_len;
+  const void *residual;
+  int32_t res_dtype;
+  const float *scale;
+  void *residual_out;
+  const float *out_norm_w;
+  void *out;
+  int32_t out_dtype;
+  float eps;
+} ssm_block_norm_params_t;
+
+ssm_status_t ssm_block_norm_fwd(const ssm_block_norm_params_t *p, void *stream);
+ssm_status_t ssm_block_norm_check(const ssm_block_norm_params_t *p);
+
+/* ------------------------------------------------------------------------
+ * Backward of ssm_block_norm_fwd from its inputs (nothing is saved by the
+ * forward): dout = dL/dout and dresidual_out = dL/dresidual_out (either may be
+ * NULL), in dout_dtype and dres_dtype.  Writes dx, dz (rows, width) in grad_dtype,
+ * dresidual in res_dtype, and dnorm_w (norm_w_len), dscale, dout_norm_w (width) in
+ * f32; any may be NULL.  Column sums are taken in a fixed order (results repeat
+ * bit for bit).  The workspace holds ssm_block_norm_bwd_workspace_size(p) bytes
+ * (256-byte aligned).  The other fields are those of the forward.
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_block_norm_bwd_params {
+  uint32_t struct_size; /* = sizeof(ssm_block_norm_bwd_params_t) */
+  int64_t rows;
+  int32_t width, group_size;
+  const void *x;
+  int32_t x_dtype;
+  int64_t x_stride;
+  const void *z;
+  int64_t z_stride;
+  int32_t gate_first;
+  const float *norm_w;
+  int32_t norm_w_len;
+  const void *residual;
+  int32_t res_dtype;
+  const float *scale;
+  const float *out_norm_w;
+  float eps;
+  const void *dout;
+  int32_t dout_dtype;
+  const void *dresidual_out;
+  int32_t dres_dtype;
+  void *dx, *dz;
+  int32_t grad_dtype;
+  void *dresidual;
+  float *dnorm_w, *dscale, *dout_norm_w;
+  void *workspace;
+  size_t workspace_bytes;
+} ssm_block_norm_bwd_params_t;
+
+ssm_status_t ssm_block_norm_bwd(const ssm_block_norm_bwd_params_t *p, void *stream);
+size_t ssm_block_norm_bwd_workspace_size(const ssm_block_norm_bwd_params_t *p);
+ssm_status_t ssm_block_norm_bwd_check(const ssm_block_norm_bwd_params_t *p);
+
 /* ------------------------------------------------------------------------ */
 const char *ssm_status_string(int32_t status);
 /* Detail of the last non-OK return on the calling thread ("" if none). */
 const char *ssm_last_error(void);
 int32_t ssm_abi_version(void);
 /* sizeof of a params struct: which = 0 scan, 1 decode, 2 chunk, 3 chunk
- * decode, 4 linear, 5 layer, 6 scan backward; 0 otherwise. */
+ * decode, 4 linear, 5 layer, 6 scan backward, 8 delta chunk, 9 delta chunk
+ * backward, 10 delta decode, 11 block norm, 12 block norm backward; 0 otherwise. */
 size_t ssm_params_sizeof(int32_t which);
 
 /* Kernel timing for measurement tools.  start and stop are hipEvent_t handles

@@ -1,7 +1,8 @@
 """MI355X (gfx950) selective-scan hot path: fused prefill scan, in-place decode
-step, multi-head chunked scan and its in-place decode step, as hand-written HIP
-kernels behind the C ABI of include/ssm_mi355x.h.  This package is the thin
-Python binding."""
+step, multi-head chunked scan and its in-place decode step, the gated delta rule
+(chunked, backward, decode step) and the block norm, as hand-written HIP kernels
+behind the C ABI of include/ssm_mi355x.h.  This package is the thin Python
+binding."""
 from .binding import (  # noqa: F401
     EXPORTED,
     Call,
@@ -18,4 +19,11 @@ from .binding import (  # noqa: F401
     scan_fwd,
     scan_fwd_noalloc,
     set_timing_events,
+)
+from .delta import (  # noqa: F401
+    block_norm_bwd,
+    block_norm_fwd,
+    delta_chunk_bwd,
+    delta_chunk_fwd,
+    delta_decode_step,
 )

@@ -108,6 +108,66 @@ class ScanBwdParams(ctypes.Structure):
     ]
 
 
+_i64 = ctypes.c_int64
+_DELTA_HEAD = [
+    ("struct_size", ctypes.c_uint32), ("batch", _i32), ("seqlen", _i32), ("num_seqs", _i32), ("nkheads", _i32),
+    ("nheads", _i32), ("d_key", _i32), ("d_value", _i32), ("q", _vp), ("k", _vp), ("v", _vp), ("x_dtype", _i32),
+    ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("g", _vp), ("beta", _vp), ("scale", _f32),
+    ("qk_norm", _i32), ("eps", _f32), ("cu_seqlens", _vp), ("state_in", _vp),
+]
+
+
+class DeltaChunkParams(ctypes.Structure):
+    _fields_ = _DELTA_HEAD + [
+        ("state_out", _vp), ("o", _vp), ("o_dtype", _i32), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class DeltaChunkBwdParams(ctypes.Structure):
+    _fields_ = _DELTA_HEAD + [
+        ("dout", _vp), ("dstate_out", _vp), ("dq", _vp), ("dk", _vp), ("dv", _vp), ("grad_dtype", _i32), ("dg", _vp),
+        ("dbeta", _vp), ("dstate_in", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class DeltaDecodeParams(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("batch", _i32), ("nkheads", _i32), ("nheads", _i32), ("d_key", _i32),
+        ("d_value", _i32), ("q", _vp), ("k", _vp), ("v", _vp), ("x_dtype", _i32), ("q_stride", _i64),
+        ("k_stride", _i64), ("v_stride", _i64), ("g", _vp), ("beta", _vp), ("scale", _f32), ("qk_norm", _i32),
+        ("eps", _f32), ("state", _vp), ("o", _vp), ("o_dtype", _i32),
+    ]
+
+
+class BlockNormParams(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("rows", _i64), ("width", _i32), ("group_size", _i32), ("x", _vp),
+        ("x_dtype", _i32), ("x_stride", _i64), ("z", _vp), ("z_stride", _i64), ("gate_first", _i32), ("norm_w", _vp),
+        ("norm_w_len", _i32), ("residual", _vp), ("res_dtype", _i32), ("scale", _vp), ("residual_out", _vp),
+        ("out_norm_w", _vp), ("out", _vp), ("out_dtype", _i32), ("eps", _f32),
+    ]
+
+
+class BlockNormBwdParams(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("rows", _i64), ("width", _i32), ("group_size", _i32), ("x", _vp),
+        ("x_dtype", _i32), ("x_stride", _i64), ("z", _vp), ("z_stride", _i64), ("gate_first", _i32), ("norm_w", _vp),
+        ("norm_w_len", _i32), ("residual", _vp), ("res_dtype", _i32), ("scale", _vp), ("out_norm_w", _vp),
+        ("eps", _f32), ("dout", _vp), ("dout_dtype", _i32), ("dresidual_out", _vp), ("dres_dtype", _i32), ("dx", _vp),
+        ("dz", _vp), ("grad_dtype", _i32), ("dresidual", _vp), ("dnorm_w", _vp), ("dscale", _vp),
+        ("dout_norm_w", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+# entry points of the gated delta rule and the block norm: (name, params, has a workspace size)
+_DELTA_ENTRIES = [
+    ("ssm_delta_chunk_fwd", "ssm_delta_chunk", DeltaChunkParams, True),
+    ("ssm_delta_chunk_bwd", "ssm_delta_chunk_bwd", DeltaChunkBwdParams, True),
+    ("ssm_delta_decode_step", "ssm_delta_decode", DeltaDecodeParams, False),
+    ("ssm_block_norm_fwd", "ssm_block_norm", BlockNormParams, False),
+    ("ssm_block_norm_bwd", "ssm_block_norm_bwd", BlockNormBwdParams, True),
+]
+
 EXPORTED = [
     "ssm_scan_fwd", "ssm_scan_workspace_size", "ssm_scan_check", "ssm_scan_fwd_noalloc",
     "ssm_decode_step", "ssm_decode_check",
@@ -116,6 +176,11 @@ EXPORTED = [
     "ssm_linear_fwd", "ssm_linear_workspace_size", "ssm_linear_check",
     "ssm_layer_fwd", "ssm_layer_workspace_size", "ssm_layer_check",
     "ssm_scan_bwd", "ssm_scan_bwd_workspace_size", "ssm_scan_bwd_check",
+    "ssm_delta_chunk_fwd", "ssm_delta_chunk_workspace_size", "ssm_delta_chunk_check",
+    "ssm_delta_chunk_bwd", "ssm_delta_chunk_bwd_workspace_size", "ssm_delta_chunk_bwd_check",
+    "ssm_delta_decode_step", "ssm_delta_decode_check",
+    "ssm_block_norm_fwd", "ssm_block_norm_check",
+    "ssm_block_norm_bwd", "ssm_block_norm_bwd_workspace_size", "ssm_block_norm_bwd_check",
     "ssm_status_string", "ssm_last_error", "ssm_abi_version", "ssm_params_sizeof", "ssm_set_timing_events",
     "ssm_debug_checks", "ssm_debug_check_scan", "ssm_debug_check_chunk", "ssm_debug_check_scan_bwd",
 ]
@@ -178,6 +243,13 @@ def load(path) -> ctypes.CDLL:
     L.ssm_scan_bwd_workspace_size.restype = ctypes.c_size_t
     L.ssm_scan_bwd_check.argtypes = [ctypes.POINTER(ScanBwdParams)]
     L.ssm_scan_bwd_check.restype = _i32
+    for run, base, st, sized in _DELTA_ENTRIES:
+        ptr = ctypes.POINTER(st)
+        getattr(L, run).argtypes, getattr(L, run).restype = [ptr, _vp], _i32
+        getattr(L, base + "_check").argtypes, getattr(L, base + "_check").restype = [ptr], _i32
+        if sized:
+            size = getattr(L, base + "_workspace_size")
+            size.argtypes, size.restype = [ptr], ctypes.c_size_t
     L.ssm_status_string.argtypes = [_i32]
     L.ssm_status_string.restype = ctypes.c_char_p
     L.ssm_last_error.argtypes = []
@@ -200,6 +272,9 @@ def load(path) -> ctypes.CDLL:
                             ScanBwdParams)):
         if L.ssm_params_sizeof(i) != ctypes.sizeof(st):
             raise RuntimeError(f"ctypes mirror of params struct {i} does not match the library")
+    for i, (_, _, st, _) in enumerate(_DELTA_ENTRIES):
+        if L.ssm_params_sizeof(8 + i) != ctypes.sizeof(st):
+            raise RuntimeError(f"ctypes mirror of params struct {8 + i} does not match the library")
     return L
 
 

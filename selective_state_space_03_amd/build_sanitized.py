@@ -1,6 +1,6 @@
 """A host-sanitized build of the library for the CPU-side checks: the C-ABI
-layer (api.cpp: argument validation, workspace sizing, dispatch, and the
-SSM_DEBUG launch-plan checks) compiled with AddressSanitizer and
+layer (api.cpp and delta_api.cpp: argument validation, workspace sizing,
+dispatch, and the SSM_DEBUG launch-plan checks) compiled with AddressSanitizer and
 UndefinedBehaviorSanitizer on the host side only, linked with the kernels'
 objects of the regular build (build.py, which must have run first).  Device
 code is never built with a sanitizer.
@@ -21,6 +21,7 @@ ASAN_DIR = os.path.join(b.BUILD, "asan")
 ASAN_LIB = os.path.join(ASAN_DIR, "libssm_mi355x_hostsan.so")
 LLVM_BIN = "/opt/rocm/lib/llvm/bin"
 HOST_SAN = ["address", "undefined"]
+HOST_SOURCES = ["api.cpp", "delta_api.cpp"]
 
 
 def asan_runtime() -> str:
@@ -33,22 +34,23 @@ def asan_runtime() -> str:
 
 
 def build_host_sanitized(verbose: bool = False) -> str:
-    objs = [o for o in sorted(glob.glob(os.path.join(b.BUILD, "*.o"))) if not os.path.basename(o).startswith("api.")]
-    want = {s + ".o" for s in b.SOURCES if s != "api.cpp"}
+    skip = tuple(s.rsplit(".", 1)[0] + "." for s in HOST_SOURCES)
+    objs = [o for o in sorted(glob.glob(os.path.join(b.BUILD, "*.o"))) if not os.path.basename(o).startswith(skip)]
+    want = {s + ".o" for s in b.SOURCES if s not in HOST_SOURCES}
     if {os.path.basename(o) for o in objs} != want:
         raise RuntimeError("the kernels' objects of the regular build are missing: run build.build() first")
     os.makedirs(ASAN_DIR, exist_ok=True)
-    api_obj = os.path.join(ASAN_DIR, "api.o")
     san = []
     for s in HOST_SAN:  # host side only: each sanitizer flag behind -Xarch_host
         san += ["-Xarch_host", f"-fsanitize={s}"]
-    cmd = [b.hipcc(), "-O1", "-g", "-std=c++17", "-fPIC", f"--offload-arch={b.ARCH}", "-I", b.INCLUDE, "-I", b.CSRC,
-           *san, "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=all", "-DSSM_DEBUG",
-           "-c", os.path.join(b.CSRC, "api.cpp"), "-o", api_obj]
+    host = [os.path.join(ASAN_DIR, s + ".o") for s in HOST_SOURCES]
+    cmds = [[b.hipcc(), "-O1", "-g", "-std=c++17", "-fPIC", f"--offload-arch={b.ARCH}", "-I", b.INCLUDE, "-I", b.CSRC,
+             *san, "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-fno-sanitize-recover=all", "-DSSM_DEBUG",
+             "-c", os.path.join(b.CSRC, src), "-o", obj] for src, obj in zip(HOST_SOURCES, host)]
     link = [os.path.join(LLVM_BIN, "clang++"), "-shared", "-fPIC", "-fsanitize=" + ",".join(HOST_SAN),
-            "-shared-libasan", api_obj, *objs, "-L/opt/rocm/lib", "-Wl,-rpath,/opt/rocm/lib", "-lamdhip64",
+            "-shared-libasan", *host, *objs, "-L/opt/rocm/lib", "-Wl,-rpath,/opt/rocm/lib", "-lamdhip64",
             "-lhipblaslt", "-o", ASAN_LIB]
-    for c in (cmd, link):
+    for c in (*cmds, link):
         if verbose:
             print(" ".join(c), flush=True)
         res = subprocess.run(c, capture_output=True, text=True)

@@ -702,6 +702,10 @@ ssm_status_t hip_status(hipError_t e) {
 
 namespace ssm {
 TimingEvents timing_events() { return g_timing; }
+int32_t set_error(int32_t status, const char* detail) {
+  g_last_error = detail;
+  return status;
+}
 static_assert(kScanScratchBytes == SSM_SCAN_NOALLOC_MAX_BYTES, "scratch size in the header and the library differ");
 }  // namespace ssm
 
@@ -1297,6 +1301,11 @@ size_t ssm_params_sizeof(int32_t which) {
     case 4: return sizeof(ssm_linear_params_t);
     case 5: return sizeof(ssm_layer_params_t);
     case 6: return sizeof(ssm_scan_bwd_params_t);
+    case 8: return sizeof(ssm_delta_chunk_params_t);
+    case 9: return sizeof(ssm_delta_chunk_bwd_params_t);
+    case 10: return sizeof(ssm_delta_decode_params_t);
+    case 11: return sizeof(ssm_block_norm_params_t);
+    case 12: return sizeof(ssm_block_norm_bwd_params_t);
     default: return 0;
   }
 }

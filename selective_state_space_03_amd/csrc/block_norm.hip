@@ -1,0 +1,510 @@
+// The norms before and after a block with its gate and residual scale, forward
+// and backward, in one pass over each row.
+//
+//   y = x (SiLU(z) first, with gate_first);  a = norm(y) norm_w;  (a SiLU(z), without)
+//   t = residual + scale a;   out = norm(t) out_w;   norm(r) = r / sqrt(mean(r^2) + eps)
+// every part optional; a grouped norm is the same with each group a row.
+//
+// Bound by memory: each row is read once into registers (kChunk = 8 values per
+// lane and access), its sums taken across the TPR lanes that share it, and the
+// results written once; t is normalised from its 32-bit value, not from the
+// residual as stored.  The backward pass recomputes a and t from the inputs (it
+// needs no saved statistics) and takes the three sums of its formulas (sum y^2;
+// sum t^2 with sum dout out_w t; sum dn n) in that order.  Its weight gradients
+// are column sums: every workgroup keeps running sums in registers over the rows
+// it walks and writes one partial row, and a second kernel adds the partials in
+// a fixed order (no atomics, the same result every time).
+#include "delta.h"
+#include "ssm_device.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kChunk = 8;
+
+// 8 values from element i0 of a row of n; vec: elements per aligned access
+__device__ __forceinline__ void get8(const void* base, size_t row, int i0, int n, int dtype, int vec, float (&v)[8]) {
+  if (dtype == kBF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + row + i0;
+    if (vec == 8) {
+      const uint4 r = load16_if(p, i0 < n);
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else if (vec == 4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint2 r = make_uint2(0u, 0u);
+        if (i0 + 4 * h < n) r = *reinterpret_cast<const uint2*>(p + 4 * h);
+        v[4 * h] = __uint_as_float(r.x << 16); v[4 * h + 1] = __uint_as_float(r.x & 0xffff0000u);
+        v[4 * h + 2] = __uint_as_float(r.y << 16); v[4 * h + 3] = __uint_as_float(r.y & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i0 + i < n ? __uint_as_float(static_cast<uint32_t>(p[i]) << 16) : 0.0f;
+    }
+  } else {
+    const float* p = static_cast<const float*>(base) + row + i0;
+    if (vec >= 4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 r = load16_if(p + 4 * h, i0 + 4 * h < n);
+        v[4 * h] = __uint_as_float(r.x); v[4 * h + 1] = __uint_as_float(r.y);
+        v[4 * h + 2] = __uint_as_float(r.z); v[4 * h + 3] = __uint_as_float(r.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i0 + i < n ? p[i] : 0.0f;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ void put8(void* base, size_t row, int i0, int n, int dtype, int vec, const float (&v)[8]) {
+  if (dtype == kBF16) {
+    uint16_t* p = static_cast<uint16_t*>(base) + row + i0;
+    const uint32_t w[4] = {pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
+    if (vec == 8) {
+      if (i0 < n) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if (vec == 4) {
+      if (i0 < n) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+      if (i0 + 4 < n) *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i < n) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    }
+  } else {
+    float* p = static_cast<float*>(base) + row + i0;
+    if (vec >= 4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (i0 + 4 * h < n)
+          *reinterpret_cast<float4*>(p + 4 * h) = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i < n) p[i] = v[i];
+    }
+  }
+}
+
+// Sums of NS values over the TPR lanes of a row.  sh: NS x waves floats, one of
+// two copies used in turn, so a copy is rewritten only after a barrier has passed.
+template <int TPR, int NS>
+__device__ __forceinline__ void row_sums(float (&x)[NS], float* sh, int& turn) {
+#pragma unroll
+  for (int o = 1; o < (TPR < 64 ? TPR : 64); o <<= 1)
+#pragma unroll
+    for (int k = 0; k < NS; ++k) x[k] += __shfl_xor(x[k], o);
+  if (TPR > 64) {
+    constexpr int W = TPR / 64;
+    float* s = sh + (turn & 1) * 2 * W;
+    ++turn;
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int k = 0; k < NS; ++k) s[k * W + w] = x[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      float t = s[k * W];
+#pragma unroll
+      for (int i = 1; i < W; ++i) t += s[k * W + i];
+      x[k] = t;
+    }
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.0f + exp2_fast(-z * kLog2e)); }
+
+template <int TPR, int NCH>
+__global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
+  __shared__ float sh[4 * (TPR > 64 ? TPR / 64 : 1)];
+  int turn = 0;
+  constexpr int RPB = 256 / TPR;  // rows per workgroup
+  const int l = threadIdx.x % TPR;
+  const long row_raw = static_cast<long>(blockIdx.x) * RPB + threadIdx.x / TPR;
+  const bool act = row_raw < a.rows;  // (whole teams; with TPR 256 every row is there)
+  const long row = act ? row_raw : a.rows - 1;
+  const long call_row = row / a.groups;
+  const int grp = static_cast<int>(row - call_row * a.groups);
+  const size_t xo = call_row * a.x_stride + static_cast<size_t>(grp) * a.n;
+  const size_t zo = call_row * a.z_stride + static_cast<size_t>(grp) * a.n;
+  const size_t dense = static_cast<size_t>(row) * a.n;
+  const size_t wo = static_cast<size_t>(row % a.w_period) * a.n;
+
+  float y[NCH][8], g[NCH][8], t[NCH][8];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int i0 = (l + c * TPR) * kChunk;
+    get8(a.x, xo, i0, a.n, a.x_dtype, a.vec, y[c]);
+    if (a.z) get8(a.z, zo, i0, a.n, a.x_dtype, a.vec, g[c]);
+    if (a.res) get8(a.res, dense, i0, a.n, a.res_dtype, a.vec, t[c]);
+  }
+  float sum[1] = {0.0f};
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (a.z) {
+        g[c][i] *= sigmoid(g[c][i]);
+        if (a.gate_first) y[c][i] *= g[c][i];
+      }
+      sum[0] = fmaf(y[c][i], y[c][i], sum[0]);
+    }
+  float inv = 1.0f;
+  if (a.norm_w) {
+    row_sums<TPR, 1>(sum, sh, turn);
+    inv = 1.0f / sqrtf(sum[0] / static_cast<float>(a.n) + a.eps);
+  }
+  sum[0] = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int i0 = (l + c * TPR) * kChunk;
+    float w[8], sc[8];
+    if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, a.vec, w);
+    if (a.scale) get8(a.scale, 0, i0, a.n, kF32, a.vec, sc);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v = y[c][i];
+      if (a.norm_w) v *= inv * w[i];
+      if (a.z && !a.gate_first) v *= g[c][i];
+      if (a.scale) v *= sc[i];
+      if (a.res) v += t[c][i];
+      t[c][i] = v;
+      sum[0] = fmaf(v, v, sum[0]);
+    }
+    if (act && a.res_out) put8(a.res_out, dense, i0, a.n, a.res_dtype, a.vec, t[c]);
+  }
+  if (!a.out) return;
+  if (a.out_w) {
+    row_sums<TPR, 1>(sum, sh, turn);
+    inv = 1.0f / sqrtf(sum[0] / static_cast<float>(a.n) + a.eps);
+  }
+  if (!act) return;
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    const int i0 = (l + c * TPR) * kChunk;
+    if (a.out_w) {
+      float w[8];
+      get8(a.out_w, 0, i0, a.n, kF32, a.vec, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[c][i] *= inv * w[i];
+    }
+    put8(a.out, dense, i0, a.n, a.out_dtype, a.vec, t[c]);
+  }
+}
+
+template <int TPR, int NCH>
+__global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a) {
+  constexpr int W = TPR > 64 ? TPR / 64 : 1;
+  constexpr int TEAMS = 256 / TPR;
+  __shared__ float sh[4 * W];
+  int turn = 0;
+  const int l = threadIdx.x % TPR;
+  const long team = static_cast<long>(blockIdx.x) * TEAMS + threadIdx.x / TPR;
+  const long teams = static_cast<long>(gridDim.x) * TEAMS;  // a multiple of w_period
+  const size_t wo = static_cast<size_t>(team % a.w_period) * a.n;
+  const float rn = 1.0f / static_cast<float>(a.n);
+
+  float aw[NCH][8], as[NCH][8], ao[NCH][8];  // this team's column sums
+#pragma unroll
+  for (int c = 0; c < NCH; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) aw[c][i] = as[c][i] = ao[c][i] = 0.0f;
+
+  // every team of a workgroup walks the same number of rows (sums cross the
+  // workgroup); a row past the end is computed from row 0 and counts for nothing
+  const long first = static_cast<long>(blockIdx.x) * TEAMS;
+  for (long base = first; base < a.rows; base += teams) {
+    const long row_raw = base + threadIdx.x / TPR;
+    const bool act = row_raw < a.rows;
+    const long row = act ? row_raw : 0;
+    const long call_row = row / a.groups;
+    const int grp = static_cast<int>(row - call_row * a.groups);
+    const size_t xo = call_row * a.x_stride + static_cast<size_t>(grp) * a.n;
+    const size_t zo = call_row * a.z_stride + static_cast<size_t>(grp) * a.n;
+    const size_t dense = static_cast<size_t>(row) * a.n;
+
+    float x[NCH][8], z[NCH][8], t[NCH][8], d[NCH][8];
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int i0 = (l + c * TPR) * kChunk;
+      get8(a.x, xo, i0, a.n, a.x_dtype, a.vec, x[c]);
+      if (a.z) get8(a.z, zo, i0, a.n, a.x_dtype, a.vec, z[c]);
+      if (a.res) {
+        get8(a.res, dense, i0, a.n, a.res_dtype, a.vec, t[c]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[c][i] = 0.0f;
+      }
+      if (a.dout) get8(a.dout, dense, i0, a.n, a.dout_dtype, a.vec, d[c]);
+    }
+    float inv = 1.0f;
+    if (a.norm_w) {
+      float sum[1] = {0.0f};
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float y = a.z && a.gate_first ? x[c][i] * (z[c][i] * sigmoid(z[c][i])) : x[c][i];
+          sum[0] = fmaf(y, y, sum[0]);
+        }
+      row_sums<TPR, 1>(sum, sh, turn);
+      inv = 1.0f / sqrtf(sum[0] * rn + a.eps);
+    }
+    // the gated norm's value and, with an output norm, t and its two sums
+    float sum2[2] = {0.0f, 0.0f};
+    if (a.out_w && a.dout) {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const int i0 = (l + c * TPR) * kChunk;
+        float w[8], sc[8], ow[8];
+        if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, a.vec, w);
+        if (a.scale) get8(a.scale, 0, i0, a.n, kF32, a.vec, sc);
+        get8(a.out_w, 0, i0, a.n, kF32, a.vec, ow);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v = x[c][i] * inv;
+          if (a.norm_w) v *= w[i];
+          if (a.z) v *= z[c][i] * sigmoid(z[c][i]);
+          if (a.scale) v *= sc[i];
+          const float tv = t[c][i] + v;
+          t[c][i] = tv;
+          sum2[0] = fmaf(tv, tv, sum2[0]);
+          sum2[1] = fmaf(d[c][i] * ow[i], tv, sum2[1]);
+        }
+      }
+      row_sums<TPR, 2>(sum2, sh, turn);
+      const float oi = 1.0f / sqrtf(sum2[0] * rn + a.eps);
+      const float k = sum2[1] * rn * oi * oi * oi;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const int i0 = (l + c * TPR) * kChunk;
+        float ow[8];
+        get8(a.out_w, 0, i0, a.n, kF32, a.vec, ow);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (act) ao[c][i] = fmaf(d[c][i] * t[c][i], oi, ao[c][i]);
+          d[c][i] = fmaf(d[c][i] * ow[i], oi, -k * t[c][i]);
+        }
+      }
+    } else if (!a.dout) {
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[c][i] = 0.0f;
+    }
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int i0 = (l + c * TPR) * kChunk;
+      if (a.dres) {
+        float e[8];
+        get8(a.dres, dense, i0, a.n, a.dres_dtype, a.vec, e);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[c][i] += e[i];
+      }
+      if (act && a.dresidual) put8(a.dresidual, dense, i0, a.n, a.res_dtype, a.vec, d[c]);
+      float w[8], sc[8];
+      if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, a.vec, w);
+      if (a.scale) get8(a.scale, 0, i0, a.n, kF32, a.vec, sc);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float sg = a.z ? sigmoid(z[c][i]) : 1.0f, gate = a.z ? z[c][i] * sg : 1.0f;
+        const float n = a.gate_first ? x[c][i] * gate * inv : x[c][i] * inv;  // normalised, before its weight
+        const float wn = a.norm_w ? w[i] : 1.0f;
+        const float gated = a.gate_first ? n * wn : n * wn * gate;
+        if (a.scale) {
+          if (act) as[c][i] = fmaf(d[c][i], gated, as[c][i]);
+          d[c][i] *= sc[i];
+        }
+        const float da = a.gate_first ? d[c][i] : d[c][i] * gate;
+        if (a.norm_w && act) aw[c][i] = fmaf(da, n, aw[c][i]);
+        sum[0] = fmaf(da * wn, n, sum[0]);
+      }
+    }
+    float k = 0.0f;
+    if (a.norm_w) {
+      row_sums<TPR, 1>(sum, sh, turn);
+      k = sum[0] * rn;
+    }
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int i0 = (l + c * TPR) * kChunk;
+      float w[8];
+      if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, a.vec, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float sg = a.z ? sigmoid(z[c][i]) : 1.0f, gate = a.z ? z[c][i] * sg : 1.0f;
+        const float n = a.gate_first ? x[c][i] * gate * inv : x[c][i] * inv;
+        const float wn = a.norm_w ? w[i] : 1.0f;
+        const float da = a.gate_first ? d[c][i] : d[c][i] * gate;
+        // (with one value the difference cancels: what is left is the epsilon's part)
+        const float dy = a.norm_w && a.n == 1 ? inv * inv * inv * a.eps * (da * wn) : inv * (da * wn - n * k);
+        if (a.z) {
+          const float dgate = a.gate_first ? dy * x[c][i] : d[c][i] * (n * wn);
+          t[c][i] = dgate * sg * (1.0f + z[c][i] * (1.0f - sg));
+        }
+        x[c][i] = a.gate_first && a.z ? dy * gate : dy;
+      }
+      if (act && a.dx) put8(a.dx, dense, i0, a.n, a.grad_dtype, a.vec, x[c]);
+      if (act && a.dz) put8(a.dz, dense, i0, a.n, a.grad_dtype, a.vec, t[c]);
+    }
+  }
+
+  // partial rows: one per workgroup where its teams share a weight row, else one per team
+  const size_t cols = a.n;
+  if (a.w_period == 1 && TEAMS > 1) {
+    constexpr int kRow = TPR * NCH * 8;
+    __shared__ float acc[4][kRow];
+    for (int which = 0; which < 3; ++which) {
+      float (*v)[8] = which == 0 ? aw : which == 1 ? as : ao;
+      const bool need = which == 0 ? a.dnorm_w != nullptr : which == 1 ? a.dscale != nullptr : a.dout_w != nullptr;
+      if (!need) continue;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float s = v[c][i];
+#pragma unroll
+          for (int o = TPR; o < 64; o <<= 1) s += __shfl_xor(s, o);
+          if ((threadIdx.x & 63) < TPR) acc[threadIdx.x >> 6][(l + c * TPR) * 8 + i] = s;
+        }
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.n; i += 256)
+        a.part[(static_cast<size_t>(blockIdx.x) * 3 + which) * cols + i] = acc[0][i] + acc[1][i] + acc[2][i] + acc[3][i];
+      __syncthreads();
+    }
+  } else {
+    float* p = a.part + static_cast<size_t>(team) * 3 * cols;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int i0 = (l + c * TPR) * kChunk;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i < a.n) {
+          if (a.dnorm_w) p[i0 + i] = aw[c][i];
+          if (a.dscale) p[cols + i0 + i] = as[c][i];
+          if (a.dout_w) p[2 * cols + i0 + i] = ao[c][i];
+        }
+    }
+  }
+}
+
+// Column sums of the partial rows: 16 columns x 16 runs of partials per workgroup
+__global__ __launch_bounds__(256) void norm_reduce_kernel(NormArgs a) {
+  __shared__ float sh[16][17];
+  const int which = blockIdx.z, wr = blockIdx.y;
+  float* out = which == 0 ? a.dnorm_w : which == 1 ? a.dscale : a.dout_w;
+  if (!out) return;
+  const int c = threadIdx.x & 15, run = threadIdx.x >> 4;
+  const int col = blockIdx.x * 16 + c;
+  float s = 0.0f;
+  if (col < a.n)
+    for (int p = wr + run * a.w_period; p < a.parts; p += 16 * a.w_period)
+      s += a.part[(static_cast<size_t>(p) * 3 + which) * a.n + col];
+  sh[run][c] = s;
+  __syncthreads();
+  if (run == 0 && col < a.n) {
+    float t = sh[0][c];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t += sh[i][c];
+    out[static_cast<size_t>(wr) * a.n + col] = t;
+  }
+}
+
+template <int TPR, int NCH>
+hipError_t fwd(const NormArgs& a, hipStream_t s) {
+  constexpr int RPB = 256 / TPR;
+  return timed_launch(s, [&] {
+    hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH>), dim3(static_cast<unsigned>((a.rows + RPB - 1) / RPB)), dim3(256), 0, s, a);
+  });
+}
+
+long gcd(long a, long b) { return b == 0 ? a : gcd(b, a % b); }
+
+struct BwdShape {
+  int tpr, nch;
+  long blocks;
+};
+
+// Lanes per row of the backward kernel, and its workgroups: four per CU where
+// there are rows for them, a whole number of turns round the weight rows.
+BwdShape bwd_shape(long rows, int n, int period) {
+  BwdShape b;
+  const int chunks = (n + kChunk - 1) / kChunk;
+  b.tpr = chunks <= 16 ? 16 : chunks <= 32 ? 32 : chunks <= 64 ? 64 : 256;
+  b.nch = b.tpr < 256 ? 1 : (chunks + 255) / 256;
+  b.nch = b.nch <= 2 ? b.nch : b.nch <= 4 ? 4 : 8;
+  const long teams = 256 / b.tpr;
+  long blocks = (rows + teams - 1) / teams;
+  blocks = blocks < 1 ? 1 : blocks < 1024 ? blocks : 1024;
+  const long unit = period / gcd(period, teams);
+  b.blocks = (blocks + unit - 1) / unit * unit;
+  return b;
+}
+
+template <int TPR, int NCH>
+hipError_t bwd(const NormArgs& a, long blocks, hipStream_t s) {
+  return timed_launch(s, [&] {
+    hipLaunchKernelGGL((norm_bwd_kernel<TPR, NCH>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+  });
+}
+
+}  // namespace
+
+int norm_bwd_parts(long rows, int n, int period) {
+  const BwdShape b = bwd_shape(rows, n, period);
+  return static_cast<int>(period == 1 ? b.blocks : b.blocks * (256 / b.tpr));
+}
+
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
+  if (a.rows == 0) return hipSuccess;
+  const int chunks = (a.n + kChunk - 1) / kChunk;
+  if (chunks <= 16) return fwd<16, 1>(a, s);
+  if (chunks <= 32) return fwd<32, 1>(a, s);
+  // a wave per row needs no barrier; with few rows four waves share one
+  if (a.rows >= 1024 && chunks <= 512) {
+    switch ((chunks + 63) / 64) {
+      case 1: return fwd<64, 1>(a, s);
+      case 2: return fwd<64, 2>(a, s);
+      case 3: return fwd<64, 3>(a, s);
+      case 4: return fwd<64, 4>(a, s);
+      case 5: return fwd<64, 5>(a, s);
+      case 6: return fwd<64, 6>(a, s);
+      default: return fwd<64, 8>(a, s);
+    }
+  }
+  if (chunks <= 256) return fwd<256, 1>(a, s);
+  if (chunks <= 512) return fwd<256, 2>(a, s);
+  if (chunks <= 1024) return fwd<256, 4>(a, s);
+  return fwd<256, 8>(a, s);
+}
+
+// (without rows the kernels still run: the weight gradients are then zeros)
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
+  const BwdShape b = bwd_shape(a.rows, a.n, a.w_period);
+  hipError_t e;
+  if (b.tpr == 16) e = bwd<16, 1>(a, b.blocks, s);
+  else if (b.tpr == 32) e = bwd<32, 1>(a, b.blocks, s);
+  else if (b.tpr == 64) e = bwd<64, 1>(a, b.blocks, s);
+  else if (b.nch == 1) e = bwd<256, 1>(a, b.blocks, s);
+  else if (b.nch == 2) e = bwd<256, 2>(a, b.blocks, s);
+  else if (b.nch == 4) e = bwd<256, 4>(a, b.blocks, s);
+  else e = bwd<256, 8>(a, b.blocks, s);
+  if (e != hipSuccess || (!a.dnorm_w && !a.dscale && !a.dout_w)) return e;
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((a.n + 15) / 16, a.w_period, 3), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -1,0 +1,168 @@
+// Device helpers of the gated delta rule's kernels: 16 x 16 x 32 bf16 matrix
+// products on operands held as one to three bf16 parts, and the sequence and
+// chunk bookkeeping.
+//
+// Operand fragment (A: row = lane % 16, B: column = lane % 16): 8 values along
+// the contraction per lane, in slots (lane / 16, j).  Any assignment of
+// contraction indices to slots gives the same product as long as A and B agree:
+//   natural:  32 s + 8 (lane / 16) + j         (contraction over tokens)
+//   tiled:    32 s + 16 (j / 4) + 4 (lane / 16) + j % 4   (contraction over key
+//             channels: the order in which an accumulator tile holds its rows,
+//             so a state tile is an operand without any exchange of lanes)
+// Accumulator tile: column = lane % 16, row = 4 (lane / 16) + i.
+#pragma once
+#include "delta.h"
+#include "ssm_device.h"
+
+namespace ssm {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <int NP>
+struct Frag {
+  uint4 p[NP];
+};
+
+// Two floats' leading 16 bits, packed (the first in the low half).
+__device__ __forceinline__ uint32_t pack_hi(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ uint32_t pack_rne(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ float hi_part(float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
+
+// Splits two floats into NP bf16 parts: leading bits by truncation (the
+// remainder is exact), the last part rounded to nearest.  Three parts hold all
+// 24 bits of the significand.
+template <int NP>
+__device__ __forceinline__ void split2(float a, float b, uint32_t (&out)[NP]) {
+#pragma unroll
+  for (int p = 0; p < NP - 1; ++p) {
+    out[p] = pack_hi(a, b);
+    a -= hi_part(a);
+    b -= hi_part(b);
+  }
+  out[NP - 1] = pack_rne(a, b);
+}
+
+template <int NP>
+__device__ __forceinline__ Frag<NP> split8(const float (&v)[8]) {
+  Frag<NP> f;
+  uint32_t w[4][NP];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2<NP>(v[2 * i], v[2 * i + 1], w[i]);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) f.p[p] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+  return f;
+}
+
+// acc += A B over the products of parts whose weight reaches the longer
+// operand's last part.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Frag<NA>& a, const Frag<NB>& b, f32x4 acc) {
+  constexpr int n = NA > NB ? NA : NB;
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j < n)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.p[i]),
+                                                      __builtin_bit_cast(bf16x8, b.p[j]), acc, 0, 0, 0);
+  return acc;
+}
+
+// Fragments in memory: [fragment][part][lane] of 16 bytes.
+template <int NP>
+__device__ __forceinline__ Frag<NP> load_frag(const unsigned char* base, int idx, int lane) {
+  Frag<NP> f;
+  const uint4* p = reinterpret_cast<const uint4*>(base) + (static_cast<size_t>(idx) * NP) * 64 + lane;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) f.p[i] = p[i * 64];
+  return f;
+}
+template <int NP>
+__device__ __forceinline__ void store_frag(unsigned char* base, int idx, int lane, const Frag<NP>& f) {
+  uint4* p = reinterpret_cast<uint4*>(base) + (static_cast<size_t>(idx) * NP) * 64 + lane;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) p[i * 64] = f.p[i];
+}
+
+// Fragments kept of a lower (upper) triangular 64 x 64 operand: row tile i
+// needs the token step s (32 columns) only where it meets the triangle.
+__device__ __forceinline__ int low_frag(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }
+__device__ __forceinline__ int up_frag(int i, int s) { return i < 2 ? 2 * i + s : i + 2; }
+
+// Waits for this wave's LDS accesses and joins the workgroup; global loads and
+// stores stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+struct DeltaSeq {
+  long t0;     // first token
+  int len;
+  long slot0;  // first chunk slot
+};
+
+// Offsets outside [0, tokens] or out of order are clamped, so no access leaves
+// the tensors whatever cu holds.  Sequence s of a packed call owns the slots
+// from cu[s] / 64 + s on, which leaves every sequence room for its chunks
+// without a prefix sum over the sequences before it.
+__device__ __forceinline__ DeltaSeq delta_seq(const DeltaArgs& a, int s) {
+  DeltaSeq q;
+  if (a.cu) {
+    long b = a.cu[s], e = a.cu[s + 1];
+    b = b < 0 ? 0 : (b > a.tokens ? a.tokens : b);
+    e = e < b ? b : (e > a.tokens ? a.tokens : e);
+    q.t0 = b;
+    q.len = static_cast<int>(e - b);
+    q.slot0 = b / kDeltaC + s;
+  } else {
+    q.t0 = static_cast<long>(s) * a.seqlen;
+    q.len = a.seqlen;
+    q.slot0 = static_cast<long>(s) * ((a.seqlen + kDeltaC - 1) / kDeltaC);
+  }
+  return q;
+}
+
+// The chunk in a slot: its first token and length (0: an unused slot).
+__device__ __forceinline__ int delta_chunk(const DeltaArgs& a, long slot, long* t0) {
+  int s;
+  if (a.cu) {
+    int lo = 0, hi = a.nseq - 1;
+    while (lo < hi) {  // the last sequence whose slots begin at or before this one
+      const int mid = (lo + hi + 1) >> 1;
+      long b = a.cu[mid];
+      b = b < 0 ? 0 : (b > a.tokens ? a.tokens : b);
+      if (b / kDeltaC + mid <= slot) lo = mid;
+      else hi = mid - 1;
+    }
+    s = lo;
+  } else {
+    s = static_cast<int>(slot / ((a.seqlen + kDeltaC - 1) / kDeltaC));
+  }
+  const DeltaSeq q = delta_seq(a, s);
+  const long c = slot - q.slot0;
+  const long left = q.len - c * kDeltaC;
+  if (c < 0 || left <= 0) return 0;
+  *t0 = q.t0 + c * kDeltaC;
+  return left < kDeltaC ? static_cast<int>(left) : kDeltaC;
+}
+
+// Workgroup b's (group, slice) for `slices` workgroups per group: the slices of
+// a group go to one XCD (blocks are dealt round the 8 XCDs), whose L2 then
+// serves the group's shared operands.  The grid holds 8 ceil(groups / 8) slices
+// workgroups; group >= groups: nothing to do.
+__device__ __forceinline__ void xcd_group(unsigned b, unsigned slices, long* group, unsigned* slice) {
+  const unsigned x = b & 7u, rest = b >> 3;
+  *slice = rest % slices;
+  *group = static_cast<long>(rest / slices) * 8 + x;
+}
+
+}  // namespace ssm

@@ -1,0 +1,488 @@
+// The walk of the gated delta rule over the chunks of a sequence, forward and in
+// reverse (equations in delta.h).
+//
+// One workgroup of four waves holds NV slices of 16 value channels of one
+// (sequence, head): S is K x 16 NV in accumulator tiles, K / 64 tiles of 16 key
+// channels per wave and slice.  A chunk has three dependent products (k S^T,
+// T R, the state update); between them the waves exchange their tiles through
+// LDS, each split once, by the wave that made it, into bf16 parts:
+//   1. R = beta v - (beta e^G rk) (K S)       wave w: tokens 16 w .. 16 w + 15
+//   2. u = T R                                same tokens
+//   3. S <- e^{G_C} S + K^T (e^{G_C-G} rk u)  wave w: its own key channels
+//      o = (scale e^G rq) (Q S) + P u         its own tokens, transposed, so a
+//                                             lane stores 4 neighbouring channels
+// Every operand that does not depend on the state comes from the prep kernel in
+// the lanes' order, so it goes from memory to registers, asked for as soon as its
+// registers are free of the chunk before.
+#include "delta_device.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kPitch = 72;  // tokens per LDS row of an exchanged [channel][token] tile (144 bytes: no bank conflicts)
+
+template <typename T>
+__device__ __forceinline__ float ldv(const void* p, size_t i) { return to_f32(static_cast<const T*>(p)[i]); }
+
+// 4 consecutive outputs of a row, any dtype; vec: they are all inside and aligned
+__device__ __forceinline__ void store4(void* p, size_t i, bool bf16, bool vec, int left, f32x4 v) {
+  if (bf16) {
+    uint16_t* o = static_cast<uint16_t*>(p) + i;
+    const uint32_t a = pack_rne(v[0], v[1]), b = pack_rne(v[2], v[3]);
+    if (vec) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(a, b);
+    } else {
+      if (left > 0) o[0] = static_cast<uint16_t>(a);
+      if (left > 1) o[1] = static_cast<uint16_t>(a >> 16);
+      if (left > 2) o[2] = static_cast<uint16_t>(b);
+      if (left > 3) o[3] = static_cast<uint16_t>(b >> 16);
+    }
+  } else {
+    float* o = static_cast<float*>(p) + i;
+    if (vec) {
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (left > e) o[e] = v[e];
+    }
+  }
+}
+
+// state rows (V, K): 4 consecutive key channels from d of row v
+__device__ __forceinline__ f32x4 load_state4(const float* s, long row, int d, int K, bool ok, bool vec) {
+  f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (!ok) return r;
+  const float* p = s + row * K + d;
+  if (vec) {
+    if (d < K) r = *reinterpret_cast<const f32x4*>(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (d + e < K) r[e] = p[e];
+  }
+  return r;
+}
+__device__ __forceinline__ void store_state4(float* s, long row, int d, int K, bool ok, bool vec, f32x4 v) {
+  if (!ok) return;
+  float* p = s + row * K + d;
+  if (vec) {
+    if (d < K) *reinterpret_cast<f32x4*>(p) = v;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (d + e < K) p[e] = v[e];
+  }
+}
+
+// A wave's tile (tokens 16 w + 4 q + i, channel r) as NP parts into [channel][token]
+template <int NP>
+__device__ __forceinline__ void put_tile(uint16_t* dst, int r, int t, f32x4 v) {
+  uint32_t a[NP], b[NP];
+  split2<NP>(v[0], v[1], a);
+  split2<NP>(v[2], v[3], b);
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+    *reinterpret_cast<uint2*>(dst + (p * 16 + r) * kPitch + t) = make_uint2(a[p], b[p]);
+}
+// The operand of token step s from such a tile
+template <int NP>
+__device__ __forceinline__ Frag<NP> get_tile(const uint16_t* src, int r, int q, int s) {
+  Frag<NP> f;
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+    f.p[p] = *reinterpret_cast<const uint4*>(src + (p * 16 + r) * kPitch + 32 * s + 8 * q);
+  return f;
+}
+
+// State tiles -> operand parts: [slab of 32 key channels][part][lane] 16 bytes, a
+// tile filling half of each lane's 8 slots.
+template <int NP, int ND>
+__device__ __forceinline__ void put_state(unsigned char* dst, int ct, int lane, f32x4 v) {
+  uint32_t a[NP], b[NP];
+  split2<NP>(v[0], v[1], a);
+  split2<NP>(v[2], v[3], b);
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+    *reinterpret_cast<uint2*>(dst + (((ct >> 1) * NP + p) * 64 + lane) * 16 + (ct & 1) * 8) = make_uint2(a[p], b[p]);
+}
+
+template <typename IN, int KP, int NV, bool SAVE>
+__global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices, int o_bf16, int vec_o) {
+  using Parts = DeltaParts<IN>;
+  constexpr int NI = Parts::in, NS = Parts::state, NO = Parts::out;
+  constexpr int ND = KP / 32, CT = KP / 64;
+  constexpr int kState = ND * NS * kDeltaFrag;
+  __shared__ __align__(16) unsigned char Ssh[NV * kState];
+  __shared__ __align__(16) uint16_t Rsh[NV][NS * 16 * kPitch];
+  __shared__ __align__(16) uint16_t Ush[NV][NS * 16 * kPitch];
+  __shared__ __align__(16) uint16_t Wsh[SAVE ? 1 : NV][SAVE ? 8 : NO * 16 * kPitch];
+
+  long group;
+  unsigned slice;
+  xcd_group(blockIdx.x, slices, &group, &slice);
+  if (group >= static_cast<long>(a.nseq) * a.h) return;
+  const int seq = static_cast<int>(group / a.h), head = static_cast<int>(group - static_cast<long>(seq) * a.h);
+  const int kh = head / (a.h / a.hk);
+  const DeltaSeq sq = delta_seq(a, seq);
+  const int nch = (sq.len + kDeltaC - 1) / kDeltaC;
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), r = lane & 15, q = lane >> 4;
+  const int v0 = static_cast<int>(slice) * 16 * NV;
+
+  f32x4 S[CT][NV];
+#pragma unroll
+  for (int i = 0; i < CT; ++i)
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
+      S[i][e] = a.state_in ? load_state4(a.state_in, group * a.V + v, d, a.K, v < a.V, a.vec_state)
+                           : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, S[i][e]);
+    }
+
+  for (int c = 0; c < nch; ++c) {
+    const long slot = sq.slot0 + c;
+    const size_t hc = static_cast<size_t>(slot) * a.h + head, kc = static_cast<size_t>(slot) * a.hk + kh;
+    const unsigned char* kf = a.kf + kc * (4 * ND * NI * kDeltaFrag);
+    const unsigned char* qf = a.qf + kc * (4 * ND * NI * kDeltaFrag);
+    const unsigned char* ktf = a.ktf + kc * (4 * ND * NI * kDeltaFrag);
+    const unsigned char* tf = a.tf + hc * (kDeltaTri * NS * kDeltaFrag);
+    const unsigned char* pf = SAVE ? nullptr : a.pf + hc * (kDeltaTri * NO * kDeltaFrag);
+    const float* sc = a.sc + hc * kDeltaSc;
+    const long t0 = sq.t0 + static_cast<long>(c) * kDeltaC;
+    const int n = min(kDeltaC, sq.len - c * kDeltaC);
+
+    if (SAVE) {  // the state entering the chunk, (K, V) rows
+#pragma unroll
+      for (int i = 0; i < CT; ++i)
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+          const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
+          float* dst = a.s_chunk + (hc * a.K + d) * a.V + v;
+          if (v < a.V)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (d + x < a.K) dst[static_cast<long>(x) * a.V] = S[i][e][x];
+        }
+    }
+
+    // v and the coefficients of this wave's tokens
+    const f32x4 beta = *reinterpret_cast<const f32x4*>(sc + kScBeta * kDeltaC + 16 * w + 4 * q);
+    const f32x4 cr = *reinterpret_cast<const f32x4*>(sc + kScR * kDeltaC + 16 * w + 4 * q);
+    const f32x4 cu = *reinterpret_cast<const f32x4*>(sc + kScU * kDeltaC + 16 * w + 4 * q);
+    const float co = sc[kScO * kDeltaC + 16 * w + r];
+    const float gamma = sc[kScGamma * kDeltaC];
+    f32x4 vv[NV];
+#pragma unroll
+    for (int e = 0; e < NV; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * w + 4 * q + i, v = v0 + 16 * e + r;
+        const bool ok = t < n && v < a.V;
+        vv[e][i] = ok ? ldv<IN>(a.v, (t0 + t) * a.v_stride + static_cast<long>(head) * a.V + v) : 0.0f;
+      }
+    Frag<NI> fk[ND], fq[SAVE ? 1 : ND];
+#pragma unroll
+    for (int s = 0; s < ND; ++s) {
+      fk[s] = load_frag<NI>(kf, w * ND + s, lane);
+      if (!SAVE) fq[s] = load_frag<NI>(qf, w * ND + s, lane);
+    }
+    Frag<NS> ft[2];
+    Frag<NO> fp[2];
+    ft[0] = load_frag<NS>(tf, low_frag(w, 0), lane);
+    if (!SAVE) fp[0] = load_frag<NO>(pf, low_frag(w, 0), lane);
+    if (w >= 2) {
+      ft[1] = load_frag<NS>(tf, low_frag(w, 1), lane);
+      if (!SAVE) fp[1] = load_frag<NO>(pf, low_frag(w, 1), lane);
+    }
+    Frag<NI> fkt[CT][2];
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) fkt[i][s] = load_frag<NI>(ktf, 2 * (w * CT + i) + s, lane);
+
+    lds_barrier();  // the state's parts
+    f32x4 ot[NV];
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      f32x4 ks = {0.0f, 0.0f, 0.0f, 0.0f};
+      ot[e] = ks;
+#pragma unroll
+      for (int s = 0; s < ND; ++s) {
+        const Frag<NS> st = load_frag<NS>(Ssh + e * kState, s, lane);
+        ks = mma(fk[s], st, ks);
+        if (!SAVE) {
+          Frag<NO> so;
+#pragma unroll
+          for (int p = 0; p < NO; ++p) so.p[p] = st.p[p];
+          ot[e] = mma(so, fq[s], ot[e]);
+        }
+      }
+      f32x4 rr;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rr[i] = fmaf(beta[i], vv[e][i], -cr[i] * ks[i]);
+      put_tile<NS>(Rsh[e], r, 16 * w + 4 * q, rr);
+    }
+    lds_barrier();  // R
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+      u = mma(ft[0], get_tile<NS>(Rsh[e], r, q, 0), u);
+      if (w >= 2) u = mma(ft[1], get_tile<NS>(Rsh[e], r, q, 1), u);
+      f32x4 us;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) us[i] = cu[i] * u[i];
+      put_tile<NS>(Ush[e], r, 16 * w + 4 * q, us);
+      if (!SAVE) {
+        put_tile<NO>(Wsh[e], r, 16 * w + 4 * q, u);
+      } else {
+        const int v = v0 + 16 * e + r;
+        float* dst = a.u_chunk + (hc * kDeltaC + 16 * w + 4 * q) * a.V + v;
+        if (v < a.V)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[static_cast<long>(i) * a.V] = u[i];
+      }
+    }
+    lds_barrier();  // u
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      const Frag<NS> u0 = get_tile<NS>(Ush[e], r, q, 0), u1 = get_tile<NS>(Ush[e], r, q, 1);
+#pragma unroll
+      for (int i = 0; i < CT; ++i) {
+        f32x4 s = S[i][e];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[x] *= gamma;
+        s = mma(fkt[i][0], u0, s);
+        s = mma(fkt[i][1], u1, s);
+        S[i][e] = s;
+        put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, s);
+      }
+      if (!SAVE) {
+        f32x4 o = ot[e];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[x] *= co;
+        o = mma(get_tile<NO>(Wsh[e], r, q, 0), fp[0], o);
+        if (w >= 2) o = mma(get_tile<NO>(Wsh[e], r, q, 1), fp[1], o);
+        const int t = 16 * w + r, v = v0 + 16 * e + 4 * q, left = a.V - v;
+        if (t < n && left > 0)
+          store4(a.o, (static_cast<size_t>(t0 + t) * a.h + head) * a.V + v, o_bf16, vec_o && left >= 4, left, o);
+      }
+    }
+  }
+
+  if (!SAVE && a.state_out)
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
+        const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
+        store_state4(a.state_out, group * a.V + v, d, a.K, v < a.V, a.vec_state, S[i][e]);
+      }
+}
+
+// The reverse walk: with D the gradient of the state leaving a chunk,
+//   dU = P^T do + (e^{G_C-G} rk) (K D),  dR = T^T dU,
+//   D <- e^{G_C} D + Q^T (scale e^G rq do) - K^T (beta e^G rk dR),
+// the same three dependent products per chunk as the forward walk; D and dR are
+// kept for the gradients' kernel.
+template <typename IN, int KP, int NV>
+__global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int slices, int do_bf16) {
+  using Parts = DeltaParts<IN>;
+  constexpr int NI = Parts::in, NS = Parts::state;
+  constexpr int ND = KP / 32, CT = KP / 64;
+  constexpr int kState = ND * NS * kDeltaFrag;
+  __shared__ __align__(16) unsigned char Ssh[NV * kState];
+  __shared__ __align__(16) uint16_t Rsh[NV][NS * 16 * kPitch];
+  __shared__ __align__(16) uint16_t Ush[NV][NS * 16 * kPitch];
+  __shared__ __align__(16) uint16_t Dsh[NV][NS * 16 * kPitch];   // do
+  __shared__ __align__(16) uint16_t Csh[NV][NS * 16 * kPitch];   // scale e^G rq do
+
+  long group;
+  unsigned slice;
+  xcd_group(blockIdx.x, slices, &group, &slice);
+  if (group >= static_cast<long>(a.nseq) * a.h) return;
+  const int seq = static_cast<int>(group / a.h), head = static_cast<int>(group - static_cast<long>(seq) * a.h);
+  const int kh = head / (a.h / a.hk);
+  const DeltaSeq sq = delta_seq(a, seq);
+  const int nch = (sq.len + kDeltaC - 1) / kDeltaC;
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), r = lane & 15, q = lane >> 4;
+  const int v0 = static_cast<int>(slice) * 16 * NV;
+
+  f32x4 D[CT][NV];
+#pragma unroll
+  for (int i = 0; i < CT; ++i)
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
+      D[i][e] = a.dstate_out ? load_state4(a.dstate_out, group * a.V + v, d, a.K, v < a.V, a.vec_state)
+                             : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, D[i][e]);
+    }
+
+  for (int c = nch - 1; c >= 0; --c) {
+    const long slot = sq.slot0 + c;
+    const size_t hc = static_cast<size_t>(slot) * a.h + head, kc = static_cast<size_t>(slot) * a.hk + kh;
+    const unsigned char* kf = a.kf + kc * (4 * ND * NI * kDeltaFrag);
+    const unsigned char* ktf = a.ktf + kc * (4 * ND * NI * kDeltaFrag);
+    const unsigned char* qtf = a.qtf + kc * (4 * ND * NI * kDeltaFrag);
+    const unsigned char* ttf = a.ttf + hc * (kDeltaTri * NS * kDeltaFrag);
+    const unsigned char* ptf = a.ptf + hc * (kDeltaTri * NS * kDeltaFrag);
+    const float* sc = a.sc + hc * kDeltaSc;
+    const long t0 = sq.t0 + static_cast<long>(c) * kDeltaC;
+    const int n = min(kDeltaC, sq.len - c * kDeltaC);
+
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
+        const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
+        float* dst = a.ds_chunk + (hc * a.K + d) * a.V + v;
+        if (v < a.V)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (d + x < a.K) dst[static_cast<long>(x) * a.V] = D[i][e][x];
+      }
+
+    const f32x4 cr = *reinterpret_cast<const f32x4*>(sc + kScR * kDeltaC + 16 * w + 4 * q);
+    const f32x4 cu = *reinterpret_cast<const f32x4*>(sc + kScU * kDeltaC + 16 * w + 4 * q);
+    const f32x4 co = *reinterpret_cast<const f32x4*>(sc + kScO * kDeltaC + 16 * w + 4 * q);
+    const float gamma = sc[kScGamma * kDeltaC];
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      f32x4 dv, cd;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * w + 4 * q + i, v = v0 + 16 * e + r;
+        const bool ok = t < n && v < a.V;
+        const size_t at = (static_cast<size_t>(t0 + (ok ? t : 0)) * a.h + head) * a.V + (ok ? v : 0);
+        dv[i] = ok ? (do_bf16 ? ldv<bf16s>(a.dout, at) : ldv<float>(a.dout, at)) : 0.0f;
+        cd[i] = co[i] * dv[i];
+      }
+      put_tile<NS>(Dsh[e], r, 16 * w + 4 * q, dv);
+      put_tile<NS>(Csh[e], r, 16 * w + 4 * q, cd);
+    }
+    Frag<NI> fk[ND];
+#pragma unroll
+    for (int s = 0; s < ND; ++s) fk[s] = load_frag<NI>(kf, w * ND + s, lane);
+    Frag<NS> ft[2], fp[2];
+    ft[1] = load_frag<NS>(ttf, up_frag(w, 1), lane);
+    fp[1] = load_frag<NS>(ptf, up_frag(w, 1), lane);
+    if (w < 2) {
+      ft[0] = load_frag<NS>(ttf, up_frag(w, 0), lane);
+      fp[0] = load_frag<NS>(ptf, up_frag(w, 0), lane);
+    }
+    Frag<NI> fkt[CT][2], fqt[CT][2];
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        fkt[i][s] = load_frag<NI>(ktf, 2 * (w * CT + i) + s, lane);
+        fqt[i][s] = load_frag<NI>(qtf, 2 * (w * CT + i) + s, lane);
+      }
+
+    lds_barrier();  // D's parts, do
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < ND; ++s) x = mma(fk[s], load_frag<NS>(Ssh + e * kState, s, lane), x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] *= cu[i];
+      x = mma(fp[1], get_tile<NS>(Dsh[e], r, q, 1), x);
+      if (w < 2) x = mma(fp[0], get_tile<NS>(Dsh[e], r, q, 0), x);
+      put_tile<NS>(Rsh[e], r, 16 * w + 4 * q, x);
+    }
+    lds_barrier();  // dU
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+      y = mma(ft[1], get_tile<NS>(Rsh[e], r, q, 1), y);
+      if (w < 2) y = mma(ft[0], get_tile<NS>(Rsh[e], r, q, 0), y);
+      f32x4 ys;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ys[i] = -cr[i] * y[i];
+      put_tile<NS>(Ush[e], r, 16 * w + 4 * q, ys);
+      const int v = v0 + 16 * e + r;
+      float* dst = a.dr_chunk + (hc * kDeltaC + 16 * w + 4 * q) * a.V + v;
+      if (v < a.V)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[static_cast<long>(i) * a.V] = y[i];
+    }
+    lds_barrier();  // dR
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+#pragma unroll
+      for (int i = 0; i < CT; ++i) {
+        f32x4 s = D[i][e];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[x] *= gamma;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          s = mma(fkt[i][k], get_tile<NS>(Ush[e], r, q, k), s);
+          s = mma(fqt[i][k], get_tile<NS>(Csh[e], r, q, k), s);
+        }
+        D[i][e] = s;
+        put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, s);
+      }
+    }
+    lds_barrier();  // do's tiles may be written again
+  }
+
+  if (a.dstate_in)
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
+        const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
+        store_state4(a.dstate_in, group * a.V + v, d, a.K, v < a.V, a.vec_state, D[i][e]);
+      }
+}
+
+unsigned grid_of(const DeltaArgs& a, int slices) {
+  const long groups = static_cast<long>(a.nseq) * a.h;
+  return static_cast<unsigned>((groups + 7) / 8 * 8 * slices);
+}
+
+// Value channels per workgroup: 32 once that still leaves every CU a workgroup
+// (the operands of T, P and the keys are then read half as often and a chunk's
+// three exchanges serve twice the work), else 16.
+bool wide(const DeltaArgs& a) {
+  return static_cast<long>(a.nseq) * a.h * ((a.V + 31) / 32) >= 256 && a.V > 16;
+}
+
+template <typename IN, int KP, int NV>
+hipError_t go(const DeltaLaunch& l, int what, hipStream_t s) {
+  const int slices = (l.a.V + 16 * NV - 1) / (16 * NV);
+  const dim3 grid(grid_of(l.a, slices));
+  const int ob = l.o_dtype == kBF16;
+  const int vec_o = l.a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(l.a.o) & (ob ? 7 : 15)) == 0;
+  if (what == 0)
+    hipLaunchKernelGGL((delta_pass_kernel<IN, KP, NV, false>), grid, dim3(256), 0, s, l.a, slices, ob, vec_o);
+  else if (what == 1)
+    hipLaunchKernelGGL((delta_pass_kernel<IN, KP, NV, true>), grid, dim3(256), 0, s, l.a, slices, 0, 0);
+  else
+    hipLaunchKernelGGL((delta_reverse_kernel<IN, KP, NV>), grid, dim3(256), 0, s, l.a, slices, l.do_dtype == kBF16);
+  return hipGetLastError();
+}
+
+template <typename IN, int KP>
+hipError_t pick_nv(const DeltaLaunch& l, int what, hipStream_t s) {
+  return wide(l.a) ? go<IN, KP, 2>(l, what, s) : go<IN, KP, 1>(l, what, s);
+}
+
+template <typename IN>
+hipError_t pick_k(const DeltaLaunch& l, int what, hipStream_t s) {
+  return delta_kp(l.a.K) == 64 ? pick_nv<IN, 64>(l, what, s) : pick_nv<IN, 128>(l, what, s);
+}
+
+hipError_t pick(const DeltaLaunch& l, int what, hipStream_t s) {
+  if (l.a.nseq == 0) return hipSuccess;
+  return l.in_dtype == kBF16 ? pick_k<bf16s>(l, what, s) : pick_k<float>(l, what, s);
+}
+
+}  // namespace
+
+hipError_t launch_delta_pass(const DeltaLaunch& l, bool save, hipStream_t s) { return pick(l, save ? 1 : 0, s); }
+hipError_t launch_delta_reverse(const DeltaLaunch& l, hipStream_t s) { return pick(l, 2, s); }
+
+}  // namespace ssm

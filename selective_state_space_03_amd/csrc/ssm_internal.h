@@ -17,6 +17,9 @@ struct TimingEvents {
 };
 TimingEvents timing_events();
 
+// Sets ssm_last_error() for this thread and returns status ("" with SSM_OK).
+int32_t set_error(int32_t status, const char* detail);
+
 // Launches `launch` on `s` between the timing events, when set.
 template <typename F>
 hipError_t timed_launch(hipStream_t s, F&& launch) {
