@@ -22,44 +22,62 @@ namespace {
 
 constexpr int kChunk = 8;
 
-// 8 values from element i0 of a row of n; vec: elements per aligned access
-__device__ __forceinline__ void get8(const void* base, size_t row, int i0, int n, int dtype, int vec, float (&v)[8]) {
+// 8 values from element i0 of a row of n, as loaded (vec: elements per aligned
+// access).  Types and alignment are uniform branches; widening is kept apart from
+// loading, so that a row's loads are all in flight before the first is waited for.
+struct Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ Raw raw8(const void* base, size_t row, int i0, int n, int dtype, int vec) {
+  Raw r;
+  r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
   if (dtype == kBF16) {
     const uint16_t* p = static_cast<const uint16_t*>(base) + row + i0;
     if (vec == 8) {
-      const uint4 r = load16_if(p, i0 < n);
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+      if (i0 < n) r.a = *reinterpret_cast<const uint4*>(p);
     } else if (vec == 4) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint2 r = make_uint2(0u, 0u);
-        if (i0 + 4 * h < n) r = *reinterpret_cast<const uint2*>(p + 4 * h);
-        v[4 * h] = __uint_as_float(r.x << 16); v[4 * h + 1] = __uint_as_float(r.x & 0xffff0000u);
-        v[4 * h + 2] = __uint_as_float(r.y << 16); v[4 * h + 3] = __uint_as_float(r.y & 0xffff0000u);
-      }
+      uint2 x = make_uint2(0u, 0u), y = x;
+      if (i0 < n) x = *reinterpret_cast<const uint2*>(p);
+      if (i0 + 4 < n) y = *reinterpret_cast<const uint2*>(p + 4);
+      r.a = make_uint4(x.x, x.y, y.x, y.y);
     } else {
+      uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i0 + i < n ? __uint_as_float(static_cast<uint32_t>(p[i]) << 16) : 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        v[i] = 0u;
+        if (i0 + i < n) v[i] = p[i];
+      }
+      r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
   } else {
     const float* p = static_cast<const float*>(base) + row + i0;
     if (vec >= 4) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 r = load16_if(p + 4 * h, i0 + 4 * h < n);
-        v[4 * h] = __uint_as_float(r.x); v[4 * h + 1] = __uint_as_float(r.y);
-        v[4 * h + 2] = __uint_as_float(r.z); v[4 * h + 3] = __uint_as_float(r.w);
-      }
+      if (i0 < n) r.a = *reinterpret_cast<const uint4*>(p);
+      if (i0 + 4 < n) r.b = *reinterpret_cast<const uint4*>(p + 4);
     } else {
+      uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i0 + i < n ? p[i] : 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        v[i] = 0u;
+        if (i0 + i < n) v[i] = __float_as_uint(p[i]);
+      }
+      r.a = make_uint4(v[0], v[1], v[2], v[3]);
+      r.b = make_uint4(v[4], v[5], v[6], v[7]);
     }
   }
+  return r;
+}
+__device__ __forceinline__ void widen(const Raw& r, int dtype, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w}, x[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
+  const bool bf = dtype == kBF16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = __uint_as_float(bf ? (i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16) : w[i]);
+    v[4 + i] = __uint_as_float(bf ? (i & 1 ? w[2 + (i >> 1)] & 0xffff0000u : w[2 + (i >> 1)] << 16) : x[i]);
+  }
+}
+__device__ __forceinline__ void get8(const void* base, size_t row, int i0, int n, int dtype, int vec, float (&v)[8]) {
+  widen(raw8(base, row, i0, n, dtype, vec), dtype, v);
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -142,17 +160,21 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
   const size_t dense = static_cast<size_t>(row) * a.n;
   const size_t wo = static_cast<size_t>(row % a.w_period) * a.n;
 
-  float y[NCH][8], g[NCH][8], t[NCH][8];
+  Raw rx[NCH], rz[NCH], rr[NCH];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int i0 = (l + c * TPR) * kChunk;
-    get8(a.x, xo, i0, a.n, a.x_dtype, a.vec, y[c]);
-    if (a.z) get8(a.z, zo, i0, a.n, a.x_dtype, a.vec, g[c]);
-    if (a.res) get8(a.res, dense, i0, a.n, a.res_dtype, a.vec, t[c]);
+    rx[c] = raw8(a.x, xo, i0, a.n, a.x_dtype, a.vec);
+    if (a.z) rz[c] = raw8(a.z, zo, i0, a.n, a.x_dtype, a.vec);
+    if (a.res) rr[c] = raw8(a.res, dense, i0, a.n, a.res_dtype, a.vec);
   }
+  float y[NCH][8], g[NCH][8], t[NCH][8];
   float sum[1] = {0.0f};
 #pragma unroll
-  for (int c = 0; c < NCH; ++c)
+  for (int c = 0; c < NCH; ++c) {
+    widen(rx[c], a.x_dtype, y[c]);
+    if (a.z) widen(rz[c], a.x_dtype, g[c]);
+    if (a.res) widen(rr[c], a.res_dtype, t[c]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (a.z) {
@@ -161,6 +183,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
       }
       sum[0] = fmaf(y[c][i], y[c][i], sum[0]);
     }
+  }
   float inv = 1.0f;
   if (a.norm_w) {
     row_sums<TPR, 1>(sum, sh, turn);

@@ -71,7 +71,7 @@ struct DeltaArgs {
 
 struct DeltaLaunch {
   DeltaArgs a;
-  int in_dtype, o_dtype, do_dtype, grad_dtype;
+  int in_dtype, o_dtype, grad_dtype;
 };
 
 inline int delta_kp(int K) { return K <= 64 ? 64 : 128; }

@@ -429,7 +429,6 @@ ssm_status_t ssm_delta_chunk_bwd(const ssm_delta_chunk_bwd_params_t* p, void* st
   a.dg = p->dg;
   a.dbeta = p->dbeta;
   a.dstate_in = p->dstate_in;
-  l.do_dtype = p->x_dtype;
   l.grad_dtype = p->grad_dtype;
   a.vec_state = p->d_key % 4 == 0 && aligned({p->state_in, p->dstate_out, p->dstate_in}, 16);
   hipStream_t st = static_cast<hipStream_t>(stream);

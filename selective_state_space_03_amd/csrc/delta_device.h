@@ -91,6 +91,12 @@ __device__ __forceinline__ void store_frag(unsigned char* base, int idx, int lan
   for (int i = 0; i < NP; ++i) p[i * 64] = f.p[i];
 }
 
+template <int NP>
+__device__ __forceinline__ void zero_frag(Frag<NP>& f) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) f.p[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // Fragments kept of a lower (upper) triangular 64 x 64 operand: row tile i
 // needs the token step s (32 columns) only where it meets the triangle.
 __device__ __forceinline__ int low_frag(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }

@@ -21,9 +21,6 @@ namespace {
 
 constexpr int kPitch = 72;  // tokens per LDS row of an exchanged [channel][token] tile (144 bytes: no bank conflicts)
 
-template <typename T>
-__device__ __forceinline__ float ldv(const void* p, size_t i) { return to_f32(static_cast<const T*>(p)[i]); }
-
 // 4 consecutive outputs of a row, any dtype; vec: they are all inside and aligned
 __device__ __forceinline__ void store4(void* p, size_t i, bool bf16, bool vec, int left, f32x4 v) {
   if (bf16) {
@@ -140,15 +137,74 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
       put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, S[i][e]);
     }
 
-  for (int c = 0; c < nch; ++c) {
-    const long slot = sq.slot0 + c;
-    const size_t hc = static_cast<size_t>(slot) * a.h + head, kc = static_cast<size_t>(slot) * a.hk + kh;
-    const unsigned char* kf = a.kf + kc * (4 * ND * NI * kDeltaFrag);
-    const unsigned char* qf = a.qf + kc * (4 * ND * NI * kDeltaFrag);
-    const unsigned char* ktf = a.ktf + kc * (4 * ND * NI * kDeltaFrag);
+  // operands of the chunk at hand; each is asked for again, for the next chunk, right
+  // after its last use, so a chunk's loads have the rest of the chunk before to arrive
+  Frag<NI> fk[ND], fq[SAVE ? 1 : ND], fkt[CT][2];
+  Frag<NS> ft[2];
+  Frag<NO> fp[2];
+  // (waves 0 and 1 have no second step of the triangles: theirs stays zero, which costs
+  // nothing beside waves 2 and 3 and keeps the products free of branches: between a matrix
+  // instruction and the first use of its result the compiler's wait states are counted
+  // along one path only)
+  zero_frag(ft[1]);
+  zero_frag(fp[1]);
+  f32x4 beta, cr, cu;
+  IN vv[NV][4];  // as loaded: a conversion here would wait for the load
+  float co = 0.0f, gamma = 0.0f;
+  const size_t kstep = static_cast<size_t>(a.hk) * (4 * ND * NI * kDeltaFrag);
+  const size_t khead = (static_cast<size_t>(sq.slot0) * a.hk + kh) * (4 * ND * NI * kDeltaFrag);
+  const size_t hc0 = static_cast<size_t>(sq.slot0) * a.h + head;
+  auto load_rows = [&](int c) {  // what the first product uses
+    const float* sc = a.sc + (hc0 + static_cast<size_t>(c) * a.h) * kDeltaSc;
+#pragma unroll
+    for (int s = 0; s < ND; ++s) {
+      fk[s] = load_frag<NI>(a.kf + khead + c * kstep, w * ND + s, lane);
+      if (!SAVE) fq[s] = load_frag<NI>(a.qf + khead + c * kstep, w * ND + s, lane);
+    }
+    beta = *reinterpret_cast<const f32x4*>(sc + kScBeta * kDeltaC + 16 * w + 4 * q);
+    cr = *reinterpret_cast<const f32x4*>(sc + kScR * kDeltaC + 16 * w + 4 * q);
+    const long t0 = sq.t0 + static_cast<long>(c) * kDeltaC;
+    const int n = min(kDeltaC, sq.len - c * kDeltaC);
+#pragma unroll
+    for (int e = 0; e < NV; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // (rows past the end read the chunk's first and are dropped at their use)
+        const int t = 16 * w + 4 * q + i, v = v0 + 16 * e + r;
+        const long row = t0 + (t < n ? t : 0);
+        vv[e][i] = static_cast<const IN*>(a.v)[row * a.v_stride + static_cast<long>(head) * a.V + min(v, a.V - 1)];
+      }
+  };
+  auto load_tri = [&](int c) {  // T and the coefficients of u
+    const size_t hc = hc0 + static_cast<size_t>(c) * a.h;
     const unsigned char* tf = a.tf + hc * (kDeltaTri * NS * kDeltaFrag);
-    const unsigned char* pf = SAVE ? nullptr : a.pf + hc * (kDeltaTri * NO * kDeltaFrag);
+    ft[0] = load_frag<NS>(tf, low_frag(w, 0), lane);
+    if (w >= 2) ft[1] = load_frag<NS>(tf, low_frag(w, 1), lane);
+    cu = *reinterpret_cast<const f32x4*>(a.sc + hc * kDeltaSc + kScU * kDeltaC + 16 * w + 4 * q);
+  };
+  auto load_update = [&](int c) {
+    const size_t hc = hc0 + static_cast<size_t>(c) * a.h;
     const float* sc = a.sc + hc * kDeltaSc;
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) fkt[i][s] = load_frag<NI>(a.ktf + khead + c * kstep, 2 * (w * CT + i) + s, lane);
+    gamma = sc[kScGamma * kDeltaC];
+    if (!SAVE) {
+      const unsigned char* pf = a.pf + hc * (kDeltaTri * NO * kDeltaFrag);
+      fp[0] = load_frag<NO>(pf, low_frag(w, 0), lane);
+      if (w >= 2) fp[1] = load_frag<NO>(pf, low_frag(w, 1), lane);
+      co = sc[kScO * kDeltaC + 16 * w + r];
+    }
+  };
+  if (nch > 0) {
+    load_rows(0);
+    load_tri(0);
+    load_update(0);
+  }
+
+  for (int c = 0; c < nch; ++c) {
+    const size_t hc = hc0 + static_cast<size_t>(c) * a.h;
+    const int next = min(c + 1, nch - 1);
     const long t0 = sq.t0 + static_cast<long>(c) * kDeltaC;
     const int n = min(kDeltaC, sq.len - c * kDeltaC);
 
@@ -165,41 +221,6 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
               if (d + x < a.K) dst[static_cast<long>(x) * a.V] = S[i][e][x];
         }
     }
-
-    // v and the coefficients of this wave's tokens
-    const f32x4 beta = *reinterpret_cast<const f32x4*>(sc + kScBeta * kDeltaC + 16 * w + 4 * q);
-    const f32x4 cr = *reinterpret_cast<const f32x4*>(sc + kScR * kDeltaC + 16 * w + 4 * q);
-    const f32x4 cu = *reinterpret_cast<const f32x4*>(sc + kScU * kDeltaC + 16 * w + 4 * q);
-    const float co = sc[kScO * kDeltaC + 16 * w + r];
-    const float gamma = sc[kScGamma * kDeltaC];
-    f32x4 vv[NV];
-#pragma unroll
-    for (int e = 0; e < NV; ++e)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * w + 4 * q + i, v = v0 + 16 * e + r;
-        const bool ok = t < n && v < a.V;
-        vv[e][i] = ok ? ldv<IN>(a.v, (t0 + t) * a.v_stride + static_cast<long>(head) * a.V + v) : 0.0f;
-      }
-    Frag<NI> fk[ND], fq[SAVE ? 1 : ND];
-#pragma unroll
-    for (int s = 0; s < ND; ++s) {
-      fk[s] = load_frag<NI>(kf, w * ND + s, lane);
-      if (!SAVE) fq[s] = load_frag<NI>(qf, w * ND + s, lane);
-    }
-    Frag<NS> ft[2];
-    Frag<NO> fp[2];
-    ft[0] = load_frag<NS>(tf, low_frag(w, 0), lane);
-    if (!SAVE) fp[0] = load_frag<NO>(pf, low_frag(w, 0), lane);
-    if (w >= 2) {
-      ft[1] = load_frag<NS>(tf, low_frag(w, 1), lane);
-      if (!SAVE) fp[1] = load_frag<NO>(pf, low_frag(w, 1), lane);
-    }
-    Frag<NI> fkt[CT][2];
-#pragma unroll
-    for (int i = 0; i < CT; ++i)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) fkt[i][s] = load_frag<NI>(ktf, 2 * (w * CT + i) + s, lane);
 
     lds_barrier();  // the state's parts
     f32x4 ot[NV];
@@ -220,18 +241,23 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
       }
       f32x4 rr;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rr[i] = fmaf(beta[i], vv[e][i], -cr[i] * ks[i]);
+      for (int i = 0; i < 4; ++i)
+        rr[i] = fmaf(beta[i], 16 * w + 4 * q + i < n ? to_f32(vv[e][i]) : 0.0f, -cr[i] * ks[i]);
       put_tile<NS>(Rsh[e], r, 16 * w + 4 * q, rr);
     }
+    load_rows(next);
     lds_barrier();  // R
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f}, u1 = u;
       u = mma(ft[0], get_tile<NS>(Rsh[e], r, q, 0), u);
-      if (w >= 2) u = mma(ft[1], get_tile<NS>(Rsh[e], r, q, 1), u);
+      u1 = mma(ft[1], get_tile<NS>(Rsh[e], r, q, 1), u1);
       f32x4 us;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) us[i] = cu[i] * u[i];
+      for (int i = 0; i < 4; ++i) {
+        u[i] += u1[i];
+        us[i] = cu[i] * u[i];
+      }
       put_tile<NS>(Ush[e], r, 16 * w + 4 * q, us);
       if (!SAVE) {
         put_tile<NO>(Wsh[e], r, 16 * w + 4 * q, u);
@@ -243,6 +269,7 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
           for (int i = 0; i < 4; ++i) dst[static_cast<long>(i) * a.V] = u[i];
       }
     }
+    load_tri(next);
     lds_barrier();  // u
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
@@ -262,12 +289,13 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[x] *= co;
         o = mma(get_tile<NO>(Wsh[e], r, q, 0), fp[0], o);
-        if (w >= 2) o = mma(get_tile<NO>(Wsh[e], r, q, 1), fp[1], o);
+        o = mma(get_tile<NO>(Wsh[e], r, q, 1), fp[1], o);
         const int t = 16 * w + r, v = v0 + 16 * e + 4 * q, left = a.V - v;
         if (t < n && left > 0)
           store4(a.o, (static_cast<size_t>(t0 + t) * a.h + head) * a.V + v, o_bf16, vec_o && left >= 4, left, o);
       }
     }
+    load_update(next);
   }
 
   if (!SAVE && a.state_out)
@@ -286,7 +314,7 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
 // the same three dependent products per chunk as the forward walk; D and dR are
 // kept for the gradients' kernel.
 template <typename IN, int KP, int NV>
-__global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int slices, int do_bf16) {
+__global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int slices) {
   using Parts = DeltaParts<IN>;
   constexpr int NI = Parts::in, NS = Parts::state;
   constexpr int ND = KP / 32, CT = KP / 64;
@@ -294,7 +322,7 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
   __shared__ __align__(16) unsigned char Ssh[NV * kState];
   __shared__ __align__(16) uint16_t Rsh[NV][NS * 16 * kPitch];
   __shared__ __align__(16) uint16_t Ush[NV][NS * 16 * kPitch];
-  __shared__ __align__(16) uint16_t Dsh[NV][NS * 16 * kPitch];   // do
+  __shared__ __align__(16) uint16_t Dsh[NV][NI * 16 * kPitch];   // do
   __shared__ __align__(16) uint16_t Csh[NV][NS * 16 * kPitch];   // scale e^G rq do
 
   long group;
@@ -319,16 +347,68 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
       put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, D[i][e]);
     }
 
-  for (int c = nch - 1; c >= 0; --c) {
-    const long slot = sq.slot0 + c;
-    const size_t hc = static_cast<size_t>(slot) * a.h + head, kc = static_cast<size_t>(slot) * a.hk + kh;
-    const unsigned char* kf = a.kf + kc * (4 * ND * NI * kDeltaFrag);
-    const unsigned char* ktf = a.ktf + kc * (4 * ND * NI * kDeltaFrag);
-    const unsigned char* qtf = a.qtf + kc * (4 * ND * NI * kDeltaFrag);
-    const unsigned char* ttf = a.ttf + hc * (kDeltaTri * NS * kDeltaFrag);
-    const unsigned char* ptf = a.ptf + hc * (kDeltaTri * NS * kDeltaFrag);
+  // operands, asked for again right after their last use (as in the forward walk)
+  Frag<NI> fk[ND], fkt[CT][2], fqt[CT][2];
+  Frag<NS> ft[2], fp[2];
+  zero_frag(ft[0]);  // (waves 2 and 3 have no first step; without branches, as above)
+  zero_frag(fp[0]);
+  f32x4 cr, cu, co;
+  IN dv[NV][4];
+  float gamma = 0.0f;
+  const size_t kstep = static_cast<size_t>(a.hk) * (4 * ND * NI * kDeltaFrag);
+  const size_t khead = (static_cast<size_t>(sq.slot0) * a.hk + kh) * (4 * ND * NI * kDeltaFrag);
+  const size_t hc0 = static_cast<size_t>(sq.slot0) * a.h + head;
+  auto load_rows = [&](int c) {  // do and the first product's operands
+    const size_t hc = hc0 + static_cast<size_t>(c) * a.h;
     const float* sc = a.sc + hc * kDeltaSc;
+    const unsigned char* ptf = a.ptf + hc * (kDeltaTri * NS * kDeltaFrag);
+#pragma unroll
+    for (int s = 0; s < ND; ++s) fk[s] = load_frag<NI>(a.kf + khead + c * kstep, w * ND + s, lane);
+    fp[1] = load_frag<NS>(ptf, up_frag(w, 1), lane);
+    if (w < 2) fp[0] = load_frag<NS>(ptf, up_frag(w, 0), lane);
+    cu = *reinterpret_cast<const f32x4*>(sc + kScU * kDeltaC + 16 * w + 4 * q);
+  };
+  auto load_do = [&](int c) {
+    const float* sc = a.sc + (hc0 + static_cast<size_t>(c) * a.h) * kDeltaSc;
+    co = *reinterpret_cast<const f32x4*>(sc + kScO * kDeltaC + 16 * w + 4 * q);
     const long t0 = sq.t0 + static_cast<long>(c) * kDeltaC;
+    const int n = min(kDeltaC, sq.len - c * kDeltaC);
+#pragma unroll
+    for (int e = 0; e < NV; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * w + 4 * q + i, v = v0 + 16 * e + r;
+        const size_t row = static_cast<size_t>(t0 + (t < n ? t : 0));
+        dv[e][i] = static_cast<const IN*>(a.dout)[(row * a.h + head) * a.V + min(v, a.V - 1)];
+      }
+  };
+  auto load_tri = [&](int c) {
+    const size_t hc = hc0 + static_cast<size_t>(c) * a.h;
+    const unsigned char* ttf = a.ttf + hc * (kDeltaTri * NS * kDeltaFrag);
+    ft[1] = load_frag<NS>(ttf, up_frag(w, 1), lane);
+    if (w < 2) ft[0] = load_frag<NS>(ttf, up_frag(w, 0), lane);
+    cr = *reinterpret_cast<const f32x4*>(a.sc + hc * kDeltaSc + kScR * kDeltaC + 16 * w + 4 * q);
+  };
+  auto load_update = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        fkt[i][s] = load_frag<NI>(a.ktf + khead + c * kstep, 2 * (w * CT + i) + s, lane);
+        fqt[i][s] = load_frag<NI>(a.qtf + khead + c * kstep, 2 * (w * CT + i) + s, lane);
+      }
+    gamma = a.sc[(hc0 + static_cast<size_t>(c) * a.h) * kDeltaSc + kScGamma * kDeltaC];
+  };
+  if (nch > 0) {
+    load_do(nch - 1);
+    load_rows(nch - 1);
+    load_tri(nch - 1);
+    load_update(nch - 1);
+  }
+
+  for (int c = nch - 1; c >= 0; --c) {
+    const size_t hc = hc0 + static_cast<size_t>(c) * a.h;
+    const int next = max(c - 1, 0);
     const int n = min(kDeltaC, sq.len - c * kDeltaC);
 
 #pragma unroll
@@ -342,65 +422,44 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
           for (int x = 0; x < 4; ++x)
             if (d + x < a.K) dst[static_cast<long>(x) * a.V] = D[i][e][x];
       }
-
-    const f32x4 cr = *reinterpret_cast<const f32x4*>(sc + kScR * kDeltaC + 16 * w + 4 * q);
-    const f32x4 cu = *reinterpret_cast<const f32x4*>(sc + kScU * kDeltaC + 16 * w + 4 * q);
-    const f32x4 co = *reinterpret_cast<const f32x4*>(sc + kScO * kDeltaC + 16 * w + 4 * q);
-    const float gamma = sc[kScGamma * kDeltaC];
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      f32x4 dv, cd;
+      f32x4 dd, cd;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = 16 * w + 4 * q + i, v = v0 + 16 * e + r;
-        const bool ok = t < n && v < a.V;
-        const size_t at = (static_cast<size_t>(t0 + (ok ? t : 0)) * a.h + head) * a.V + (ok ? v : 0);
-        dv[i] = ok ? (do_bf16 ? ldv<bf16s>(a.dout, at) : ldv<float>(a.dout, at)) : 0.0f;
-        cd[i] = co[i] * dv[i];
+        dd[i] = 16 * w + 4 * q + i < n ? to_f32(dv[e][i]) : 0.0f;
+        cd[i] = co[i] * dd[i];
       }
-      put_tile<NS>(Dsh[e], r, 16 * w + 4 * q, dv);
+      put_tile<NI>(Dsh[e], r, 16 * w + 4 * q, dd);
       put_tile<NS>(Csh[e], r, 16 * w + 4 * q, cd);
     }
-    Frag<NI> fk[ND];
-#pragma unroll
-    for (int s = 0; s < ND; ++s) fk[s] = load_frag<NI>(kf, w * ND + s, lane);
-    Frag<NS> ft[2], fp[2];
-    ft[1] = load_frag<NS>(ttf, up_frag(w, 1), lane);
-    fp[1] = load_frag<NS>(ptf, up_frag(w, 1), lane);
-    if (w < 2) {
-      ft[0] = load_frag<NS>(ttf, up_frag(w, 0), lane);
-      fp[0] = load_frag<NS>(ptf, up_frag(w, 0), lane);
-    }
-    Frag<NI> fkt[CT][2], fqt[CT][2];
-#pragma unroll
-    for (int i = 0; i < CT; ++i)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        fkt[i][s] = load_frag<NI>(ktf, 2 * (w * CT + i) + s, lane);
-        fqt[i][s] = load_frag<NI>(qtf, 2 * (w * CT + i) + s, lane);
-      }
+    load_do(next);
 
     lds_barrier();  // D's parts, do
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
 #pragma unroll
       for (int s = 0; s < ND; ++s) x = mma(fk[s], load_frag<NS>(Ssh + e * kState, s, lane), x);
+      y = mma(fp[1], get_tile<NI>(Dsh[e], r, q, 1), y);
+      y = mma(fp[0], get_tile<NI>(Dsh[e], r, q, 0), y);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] *= cu[i];
-      x = mma(fp[1], get_tile<NS>(Dsh[e], r, q, 1), x);
-      if (w < 2) x = mma(fp[0], get_tile<NS>(Dsh[e], r, q, 0), x);
+      for (int i = 0; i < 4; ++i) x[i] = fmaf(cu[i], x[i], y[i]);
       put_tile<NS>(Rsh[e], r, 16 * w + 4 * q, x);
     }
+    load_rows(next);
     lds_barrier();  // dU
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f}, y0 = y;
       y = mma(ft[1], get_tile<NS>(Rsh[e], r, q, 1), y);
-      if (w < 2) y = mma(ft[0], get_tile<NS>(Rsh[e], r, q, 0), y);
+      y0 = mma(ft[0], get_tile<NS>(Rsh[e], r, q, 0), y0);
       f32x4 ys;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ys[i] = -cr[i] * y[i];
+      for (int i = 0; i < 4; ++i) {
+        y[i] += y0[i];
+        ys[i] = -cr[i] * y[i];
+      }
       put_tile<NS>(Ush[e], r, 16 * w + 4 * q, ys);
       const int v = v0 + 16 * e + r;
       float* dst = a.dr_chunk + (hc * kDeltaC + 16 * w + 4 * q) * a.V + v;
@@ -408,23 +467,27 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
 #pragma unroll
         for (int i = 0; i < 4; ++i) dst[static_cast<long>(i) * a.V] = y[i];
     }
+    load_tri(next);
     lds_barrier();  // dR
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
-        f32x4 s = D[i][e];
+        f32x4 s = D[i][e], s1 = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[x] *= gamma;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           s = mma(fkt[i][k], get_tile<NS>(Ush[e], r, q, k), s);
-          s = mma(fqt[i][k], get_tile<NS>(Csh[e], r, q, k), s);
+          s1 = mma(fqt[i][k], get_tile<NS>(Csh[e], r, q, k), s1);
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[x] += s1[x];
         D[i][e] = s;
         put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, s);
       }
     }
+    load_update(next);
     lds_barrier();  // do's tiles may be written again
   }
 
@@ -461,7 +524,7 @@ hipError_t go(const DeltaLaunch& l, int what, hipStream_t s) {
   else if (what == 1)
     hipLaunchKernelGGL((delta_pass_kernel<IN, KP, NV, true>), grid, dim3(256), 0, s, l.a, slices, 0, 0);
   else
-    hipLaunchKernelGGL((delta_reverse_kernel<IN, KP, NV>), grid, dim3(256), 0, s, l.a, slices, l.do_dtype == kBF16);
+    hipLaunchKernelGGL((delta_reverse_kernel<IN, KP, NV>), grid, dim3(256), 0, s, l.a, slices);
   return hipGetLastError();
 }
 
