@@ -24,9 +24,10 @@ constexpr int kDeltaMaxK = 128;    // key channels the kernels hold
 constexpr int kDeltaFrag = 1024;   // bytes of an operand fragment: 64 lanes x 8 bf16
 constexpr int kDeltaTri = 6;       // fragments of a triangular 64 x 64 operand (of 8)
 // floats of a (chunk, head)'s coefficients, in rows of 64: beta; beta e^G rk;
-// scale e^G rq; e^{G_C - G} rk; [e^{G_C}]; rk; rq; unused; G in 64 bits (2 rows)
-constexpr int kDeltaSc = 10 * kDeltaC;
-enum DeltaScRow { kScBeta = 0, kScR, kScO, kScU, kScGamma, kScRk, kScRq, kScPad, kScG };
+// scale e^G rq; e^{G_C - G} rk; [e^{G_C}]; rk; rq; e^G; G in 64 bits (2 rows);
+// e^{G_C - G}
+constexpr int kDeltaSc = 11 * kDeltaC;
+enum DeltaScRow { kScBeta = 0, kScR, kScO, kScU, kScGamma, kScRk, kScRq, kScEg, kScG, kScEl = kScG + 2 };
 
 // bf16 parts that stand for a 32-bit operand of a matrix product (its leading
 // 8, 16 or 24 bits): the inputs (bf16 inputs are exact in one), the state
@@ -61,8 +62,9 @@ struct DeltaArgs {
   unsigned char *qtf, *ttf, *ptf;  // backward only
   float* sc;
   // backward
-  float *s_chunk, *ds_chunk;       // (slots, h, K, V): state entering / state gradient leaving each chunk
-  float *u_chunk, *dr_chunk;       // (slots, h, 64, V)
+  // per (slot, head), K and V padded to delta_kp and delta_vp with zeros:
+  float *s_chunk, *ds_chunk;       // (K, V) state entering / state gradient leaving the chunk
+  float *u_chunk, *dr_chunk;       // (64, V)
   const void* dout;                // (tokens, h, V)
   const float* dstate_out;         // (nseq, h, V, K) or null
   void *dq, *dk, *dv;              // dense, or null
@@ -75,6 +77,7 @@ struct DeltaLaunch {
 };
 
 inline int delta_kp(int K) { return K <= 64 ? 64 : 128; }
+__host__ __device__ inline int delta_vp(int V) { return (V + 31) / 32 * 32; }
 hipError_t launch_delta_prep(const DeltaLaunch& l, bool backward, hipStream_t s);
 // The forward walk; save: also writes s_chunk and u_chunk, and no output.
 hipError_t launch_delta_pass(const DeltaLaunch& l, bool save, hipStream_t s);

@@ -110,7 +110,8 @@ DeltaWs delta_ws(const P* p, bool bwd) {
     w.qtf = take(rows);
     w.ttf = take(hc * ssm::kDeltaTri * ns * ssm::kDeltaFrag);
     w.ptf = take(hc * ssm::kDeltaTri * ns * ssm::kDeltaFrag);
-    const size_t state = hc * p->d_key * p->d_value * sizeof(float), rows64 = hc * ssm::kDeltaC * p->d_value * sizeof(float);
+    const size_t vp = ssm::delta_vp(p->d_value);
+    const size_t state = hc * ssm::delta_kp(p->d_key) * vp * sizeof(float), rows64 = hc * ssm::kDeltaC * vp * sizeof(float);
     w.s_chunk = take(state);
     w.ds_chunk = take(state);
     w.u_chunk = take(rows64);
@@ -137,7 +138,7 @@ ssm_status_t delta_seq_check(const P* p, bool bwd) {
     return fail(SSM_ERR_INVALID_ARG, "packed sequences need batch 1; without cu_seqlens num_seqs must equal batch");
   if (!aligned({p->cu_seqlens, p->state_in}, 4)) return fail(SSM_ERR_INVALID_ARG, "cu_seqlens or state_in is not 4-byte aligned");
   const long slots = delta_slots(p);
-  const long slices = (p->d_value + 15) / 16;
+  const long slices = ssm::delta_vp(p->d_value) / 16;
   if (slots * p->nheads > 0x7fffffffL || (static_cast<long>(p->num_seqs) * p->nheads + 7) * slices > 0x7fffffffL)
     return fail(SSM_ERR_UNSUPPORTED, "too many chunks, sequences and heads for one launch");
   const size_t need = delta_ws(p, bwd).total;

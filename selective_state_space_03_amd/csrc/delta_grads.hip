@@ -11,71 +11,168 @@
 // and through the norm, dq = scale rq (dq^ - q~ (q~.dq^)), q~ = rq q.
 //
 // One workgroup takes a (chunk, key head) and its value heads in turn, so the
-// shared heads' dq and dk are summed in registers in a fixed order.  Wave w
-// computes the tokens 16 w .. 16 w + 15.  Bound by the splitting of the 32-bit
-// operands (S, D, u, dR) into bf16 parts and the matrix products on them.
+// shared heads' dq and dk are summed in registers in a fixed order.  Wave w owns
+// the key channels 16 TW w .. (TW tiles of 16) for the products with S and D, so
+// those are read and split into bf16 parts once, and the tokens 16 w .. 16 w + 15
+// for everything else; the rows do, dR and u of 32 value channels at a time are
+// split by their token's wave and handed round through LDS, two buffers in turn,
+// with the next step's loads in flight.  64 x 64 products that meet a triangle
+// take only the halves inside it.
 #include "delta_device.h"
 
 namespace ssm {
 namespace {
 
-constexpr int kLP = 68;
+constexpr int kLP = 68;  // floats per LDS row of a 64 x 64 matrix
 
-// 8 consecutive values from column c of a row of `width` 32-bit values
-__device__ __forceinline__ void row8f(const float* row, int c, int width, bool ok, bool vec, float (&v)[8]) {
-  if (vec) {
+// 8 consecutive values of a row of `width`, as loaded, and widened.  vec: whole
+// aligned groups (width a multiple of 8); columns past the end read the row's
+// first ones and are dropped when widened.
+template <typename IN>
+struct Row8;
+template <>
+struct Row8<bf16s> {
+  uint4 a;
+  __device__ __forceinline__ void load(const bf16s* row, int c, int width, bool vec) {
+    if (vec) {
+      a = *reinterpret_cast<const uint4*>(row + (c < width ? c : 0));
+    } else {
+      uint32_t v[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 r = load16_if(row + c + 4 * h, ok && c + 4 * h < width);
-      v[4 * h] = __uint_as_float(r.x); v[4 * h + 1] = __uint_as_float(r.y);
-      v[4 * h + 2] = __uint_as_float(r.z); v[4 * h + 3] = __uint_as_float(r.w);
+      for (int i = 0; i < 8; ++i) v[i] = row[min(c + i, width - 1)].bits;
+      a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = ok && c + i < width ? row[c + i] : 0.0f;
   }
-}
-// the same of the inputs' type, 4-element accesses where vec
-__device__ __forceinline__ void row8i(const float* row, int c, int width, bool ok, bool vec, float (&v)[8]) {
-  row8f(row, c, width, ok, vec, v);
-}
-__device__ __forceinline__ void row8i(const bf16s* row, int c, int width, bool ok, bool vec, float (&v)[8]) {
-  if (vec) {
+  __device__ __forceinline__ void get(int left, float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint2 r = make_uint2(0u, 0u);
-      if (ok && c + 4 * h < width) r = *reinterpret_cast<const uint2*>(row + c + 4 * h);
-      v[4 * h] = __uint_as_float(r.x << 16); v[4 * h + 1] = __uint_as_float(r.x & 0xffff0000u);
-      v[4 * h + 2] = __uint_as_float(r.y << 16); v[4 * h + 3] = __uint_as_float(r.y & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = 2 * i < left ? __uint_as_float(w[i] << 16) : 0.0f;
+      v[2 * i + 1] = 2 * i + 1 < left ? __uint_as_float(w[i] & 0xffff0000u) : 0.0f;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = ok && c + i < width ? to_f32(row[c + i]) : 0.0f;
   }
+};
+template <>
+struct Row8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* row, int c, int width, bool vec) {
+    if (vec) {
+      const float4* p = reinterpret_cast<const float4*>(row + (c < width ? c : 0));
+      a = p[0];
+      b = p[1];
+    } else {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = row[min(c + i, width - 1)];
+      a = make_float4(v[0], v[1], v[2], v[3]);
+      b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+  __device__ __forceinline__ void get(int left, float (&v)[8]) const {
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? x[i] : 0.0f;
+  }
+};
+
+// 8 values into LDS in the inputs' type (they come from it), and from there as an operand
+__device__ __forceinline__ void put8(bf16s* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_hi(v[0], v[1]), pack_hi(v[2], v[3]), pack_hi(v[4], v[5]), pack_hi(v[6], v[7]));
+}
+__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ Frag<1> row_frag(const bf16s* p) {
+  Frag<1> f;
+  f.p[0] = *reinterpret_cast<const uint4*>(p);
+  return f;
+}
+__device__ __forceinline__ Frag<3> row_frag(const float* p) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  return split8<3>(v);
 }
 
+// A k and a q value, in their own type
+template <typename IN>
+struct KQ;
+template <>
+struct KQ<bf16s> {
+  uint32_t v;
+  __device__ __forceinline__ void set(bf16s k, bf16s q) {
+    v = static_cast<uint32_t>(k.bits) | static_cast<uint32_t>(q.bits) << 16;
+  }
+  __device__ __forceinline__ float k() const { return __uint_as_float(v << 16); }
+  __device__ __forceinline__ float q() const { return __uint_as_float(v & 0xffff0000u); }
+};
+template <>
+struct KQ<float> {
+  float a, b;
+  __device__ __forceinline__ void set(float k, float q) {
+    a = k;
+    b = q;
+  }
+  __device__ __forceinline__ float k() const { return a; }
+  __device__ __forceinline__ float q() const { return b; }
+};
+
+// Sum over the 16 lanes of a row, in every lane of it
 __device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) x += __shfl_xor(x, o);
+  x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x128, 0xf, 0xf, false));
+  x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x124, 0xf, 0xf, false));
+  x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x122, 0xf, 0xf, false));
+  x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x121, 0xf, 0xf, false));
   return x;
 }
 __device__ __forceinline__ float exp_of(double x) { return exp2_fast(static_cast<float>(x * 1.4426950408889634)); }
 
-__device__ __forceinline__ void put_grad(void* p, size_t i, int dtype, float v) {
-  if (dtype == kBF16) st<bf16s>(p, i, v);
-  else st<float>(p, i, v);
+// 8 gradients from element i on; vec: all inside and aligned, else the first `left`
+__device__ __forceinline__ void store8(void* p, size_t i, int dtype, bool vec, int left, const float (&v)[8]) {
+  if (dtype == kBF16) {
+    uint16_t* o = static_cast<uint16_t*>(p) + i;
+    const uint32_t w[4] = {pack_rne(v[0], v[1]), pack_rne(v[2], v[3]), pack_rne(v[4], v[5]), pack_rne(v[6], v[7])};
+    if (vec) {
+      *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) o[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+    }
+  } else {
+    float* o = static_cast<float*>(p) + i;
+    if (vec) {
+      reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) o[e] = v[e];
+    }
+  }
 }
 
 template <typename IN, int KP>
-__global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int grad_dtype, int vec_v, int vec_in) {
+__global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int grad_dtype, int vec_in, int vec_out,
+                                                              int vec_qk_out) {
   using Parts = DeltaParts<IN>;
   constexpr int NI = Parts::in, NS = Parts::state;
-  constexpr int ND = KP / 32, NT = KP / 16;
-  __shared__ __align__(16) float Wm[kDeltaC * kLP];
-  __shared__ __align__(16) float Mm[kDeltaC * kLP];
+  constexpr int ND = KP / 32, TW = KP / 64;
+  constexpr int kDo = 4 * NI * kDeltaFrag, kRow = 4 * NS * kDeltaFrag;
+  constexpr int kStage = kDo + 2 * kRow;
+  __shared__ __align__(16) unsigned char stage[2 * kStage];
+  __shared__ __align__(16) float WM[2 * kDeltaC * kLP];
+  float* const Wm = WM;
+  float* const Mm = WM + kDeltaC * kLP;
+  __shared__ float rowp[4][2][kDeltaC];
   __shared__ float colx[4][kDeltaC];
-  __shared__ float rowg[kDeltaC], rowb[kDeltaC], rowv[kDeltaC], rowc[kDeltaC];
-  __shared__ float sdots[4];
+  __shared__ __align__(16) float sc[kDeltaSc];  // the head's coefficients
+  __shared__ float rowx[kDeltaC], rowb[kDeltaC], rowv[kDeltaC], sdots[4], csums[4];
+  // after the last step the staging holds W and M as operands
+  unsigned char* const wf = stage;                                     // rows of W: lower triangle
+  unsigned char* const cf = stage + kDeltaTri * NS * kDeltaFrag;       // columns of W: upper triangle
+  unsigned char* const nf = stage;                                     // M + M^T, all 8
 
   const long slot = blockIdx.x / a.hk;
   const int kh = static_cast<int>(blockIdx.x - slot * a.hk);
@@ -84,99 +181,157 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int grad_
   const int n = delta_chunk(a, slot, &t0);
   if (n == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), r = lane & 15, q = lane >> 4;
+  const int vp = delta_vp(a.V), steps = vp / 32;
   const size_t kc = static_cast<size_t>(slot) * a.hk + kh;
-  const unsigned char* kf = a.kf + kc * (4 * ND * NI * kDeltaFrag);
-  const unsigned char* qf = a.qf + kc * (4 * ND * NI * kDeltaFrag);
-  const unsigned char* ktf = a.ktf + kc * (4 * ND * NI * kDeltaFrag);
-  const unsigned char* qtf = a.qtf + kc * (4 * ND * NI * kDeltaFrag);
+  const size_t kbytes = 4 * ND * NI * kDeltaFrag;
+  const unsigned char* ktf = a.ktf + kc * kbytes;
+  const unsigned char* qtf = a.qtf + kc * kbytes;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
-  // q, k in the accumulators' layout, and the products of k and q with k
-  f32x4 kC[NT], qC[NT], dqa[NT], dka[NT];
+  // the chunk's q and k rows, through the staging (zeros past the ends)
+  constexpr int pitch = KP + 16 / static_cast<int>(sizeof(IN));
+  static_assert(2 * kDeltaC * pitch * static_cast<int>(sizeof(IN)) <= 2 * kStage, "q and k rows fit the staging");
+  IN* const Ks = reinterpret_cast<IN*>(stage);
+  IN* const Qs = Ks + kDeltaC * pitch;
+  {
+    constexpr int per = KP / 8, each = kDeltaC * per / 256;
+    Row8<IN> rk[each], rq[each];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    dqa[j] = dka[j] = zero;
+    for (int i = 0; i < each; ++i) {
+      const int p = tid + 256 * i, t = p / per, d = (p % per) * 8;
+      const long tt = t0 + (t < n ? t : 0), off = static_cast<long>(kh) * a.K;
+      rk[i].load(static_cast<const IN*>(a.k) + tt * a.k_stride + off, d, a.K, a.vec_qk);
+      rq[i].load(static_cast<const IN*>(a.q) + tt * a.q_stride + off, d, a.K, a.vec_qk);
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * w + 4 * q + i, d = 16 * j + r;
-      const bool ok = t < n && d < a.K;
-      const long tt = t0 + (ok ? t : 0);
-      const long off = static_cast<long>(kh) * a.K + (ok ? d : 0);
-      kC[j][i] = ok ? to_f32(static_cast<const IN*>(a.k)[tt * a.k_stride + off]) : 0.0f;
-      qC[j][i] = ok ? to_f32(static_cast<const IN*>(a.q)[tt * a.q_stride + off]) : 0.0f;
+    for (int i = 0; i < each; ++i) {
+      const int p = tid + 256 * i, t = p / per, d = (p % per) * 8;
+      float v[8];
+      rk[i].get(t < n ? a.K - d : 0, v);
+      put8(Ks + t * pitch + d, v);
+      rq[i].get(t < n ? a.K - d : 0, v);
+      put8(Qs + t * pitch + d, v);
     }
   }
+  __syncthreads();
+  // q and k at this wave's channels, all tokens, in the accumulators' layout
+  KQ<IN> kq[TW][4][4];
+  f32x4 dqa[TW][4], dka[TW][4];
+#pragma unroll
+  for (int x = 0; x < TW; ++x)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dqa[x][i] = dka[x][i] = zero;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = (16 * i + 4 * q + e) * pitch + 16 * (w * TW + x) + r;
+        kq[x][i][e].set(Ks[at], Qs[at]);
+      }
+    }
   f32x4 kk[4], qk[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) kk[j] = qk[j] = zero;
 #pragma unroll
   for (int c = 0; c < ND; ++c) {
-    const Frag<NI> fk = load_frag<NI>(kf, w * ND + c, lane), fq = load_frag<NI>(qf, w * ND + c, lane);
+    const int off = 32 * c + 8 * q;
+    const Frag<NI> fk = row_frag(Ks + (16 * w + r) * pitch + off), fq = row_frag(Qs + (16 * w + r) * pitch + off);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j <= w) {
-        const Frag<NI> b = load_frag<NI>(kf, j * ND + c, lane);
-        kk[j] = mma(fk, b, kk[j]);
-        qk[j] = mma(fq, b, qk[j]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const Frag<NI> b = row_frag(Ks + (16 * j + r) * pitch + off);
+      kk[j] = mma(fk, b, kk[j]);
+      qk[j] = mma(fq, b, qk[j]);
+    }
   }
+  __syncthreads();
 
+#pragma unroll 1
   for (int hr = 0; hr < rep; ++hr) {
     const int head = kh * rep + hr;
     const size_t hc = static_cast<size_t>(slot) * a.h + head;
-    const float* sc = a.sc + hc * kDeltaSc;
+    for (int i = tid; i < kDeltaSc; i += 256) sc[i] = a.sc[hc * kDeltaSc + i];  // (seen by all after the first step's barrier)
     const double* G = reinterpret_cast<const double*>(sc + kScG * kDeltaC);
-    const float* Sg = a.s_chunk + hc * a.K * a.V;
-    const float* Dg = a.ds_chunk + hc * a.K * a.V;
-    const float* Ug = a.u_chunk + hc * kDeltaC * a.V;
-    const float* Rg = a.dr_chunk + hc * kDeltaC * a.V;
     const int trow = 16 * w + r;  // this lane's token as an operand's row
-    const size_t orow = (static_cast<size_t>(t0 + (trow < n ? trow : 0)) * a.h + head) * a.V;
-    const IN* vrow = static_cast<const IN*>(a.v) + (t0 + (trow < n ? trow : 0)) * a.v_stride + static_cast<long>(head) * a.V;
+    const bool live = trow < n;
+    const size_t orow = (static_cast<size_t>(t0 + (live ? trow : 0)) * a.h + head) * a.V;
+    const IN* const dorow = static_cast<const IN*>(a.dout) + orow;
+    const IN* const vrow = static_cast<const IN*>(a.v) + (t0 + (live ? trow : 0)) * a.v_stride + static_cast<long>(head) * a.V;
+    const float* const rrow = a.dr_chunk + (hc * kDeltaC + trow) * vp;
+    const float* const urow = a.u_chunk + (hc * kDeltaC + trow) * vp;
+    const float* const srow = a.s_chunk + (hc * KP + 16 * w * TW + r) * vp;
+    const float* const grow = a.ds_chunk + (hc * KP + 16 * w * TW + r) * vp;
 
-    f32x4 sdo[NT], sdr[NT], dsu[NT], dp[4], dl[4];
+    f32x4 sdo[TW][4], sdr[TW][4], dsu[TW][4], dp[4], dl[4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) sdo[j] = sdr[j] = dsu[j] = zero;
+    for (int i = 0; i < 4; ++i) {
+      dp[i] = dl[i] = zero;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dp[j] = dl[j] = zero;
+      for (int x = 0; x < TW; ++x) sdo[x][i] = sdr[x][i] = dsu[x][i] = zero;
+    }
     float sdot = 0.0f, drv = 0.0f;
-    const float brow = sc[kScBeta * kDeltaC + trow];
-#pragma unroll 1
-    for (int c = 0; c < a.V; c += 32) {
-      const int vc = c + 8 * q;
-      float x[8], y[8];
-      row8i(static_cast<const IN*>(a.dout) + orow, vc, a.V, trow < n, vec_in, x);
-      const Frag<NI> fdo = split8<NI>(x);
-      row8f(Rg + static_cast<size_t>(trow) * a.V, vc, a.V, true, vec_v, x);
-      const Frag<NS> fdr = split8<NS>(x);
-      row8i(vrow, vc, a.V, trow < n, vec_in, y);
+    const float brow = a.sc[hc * kDeltaSc + kScBeta * kDeltaC + trow];
+
+    Row8<IN> ldo, lv;
+    Row8<float> lr, lu, ls[TW], ld[TW];
+    auto load_step = [&](int c) {
+      const int vc = 32 * c + 8 * q;
+      ldo.load(dorow, vc, a.V, vec_in);
+      lv.load(vrow, vc, a.V, vec_in);
+      lr.load(rrow, vc, vp, true);
+      lu.load(urow, vc, vp, true);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        drv = fmaf(x[i], y[i], drv);
-        if (a.dv && trow < n && vc + i < a.V) put_grad(a.dv, orow + vc + i, grad_dtype, brow * x[i]);
+      for (int x = 0; x < TW; ++x) {
+        ls[x].load(srow + static_cast<size_t>(16 * x) * vp, vc, vp, true);
+        ld[x].load(grow + static_cast<size_t>(16 * x) * vp, vc, vp, true);
       }
-      row8f(Ug + static_cast<size_t>(trow) * a.V, vc, a.V, true, vec_v, x);
-      const Frag<NS> fu = split8<NS>(x);
+    };
+    load_step(0);
+#pragma unroll 1
+    for (int c = 0; c < steps; ++c) {
+      unsigned char* const sdf = stage + (c & 1) * kStage;
+      unsigned char* const srf = sdf + kDo;
+      unsigned char* const suf = srf + kRow;
+      const int vc = 32 * c + 8 * q, left = live ? a.V - vc : 0;
+      float x8[8], y8[8];
+      ldo.get(left, x8);
+      store_frag<NI>(sdf, w, lane, split8<NI>(x8));
+      lr.get(8, x8);
+      store_frag<NS>(srf, w, lane, split8<NS>(x8));
+      lv.get(left, y8);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j <= w) {
-          row8f(Ug + static_cast<size_t>(16 * j + r) * a.V, vc, a.V, true, vec_v, x);
-          const Frag<NS> b = split8<NS>(x);
-          dp[j] = mma(fdo, b, dp[j]);
-          dl[j] = mma(fdr, b, dl[j]);
+      for (int i = 0; i < 8; ++i) drv = fmaf(x8[i], y8[i], drv);
+      if (a.dv && left > 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x8[i] *= brow;
+        store8(a.dv, orow + vc, grad_dtype, vec_out, left, x8);
+      }
+      lu.get(8, x8);
+      store_frag<NS>(suf, w, lane, split8<NS>(x8));
+      Frag<NS> fs[TW], fd[TW];
+#pragma unroll
+      for (int x = 0; x < TW; ++x) {
+        ls[x].get(8, x8);
+        ld[x].get(8, y8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sdot = fmaf(x8[i], y8[i], sdot);
+        fs[x] = split8<NS>(x8);
+        fd[x] = split8<NS>(y8);
+      }
+      load_step(min(c + 1, steps - 1));
+      lds_barrier();
+      const Frag<NI> mydo = load_frag<NI>(sdf, w, lane);
+      const Frag<NS> mydr = load_frag<NS>(srf, w, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Frag<NI> fo = load_frag<NI>(sdf, i, lane);
+        const Frag<NS> fr = load_frag<NS>(srf, i, lane), fu = load_frag<NS>(suf, i, lane);
+#pragma unroll
+        for (int x = 0; x < TW; ++x) {
+          sdo[x][i] = mma(fo, fs[x], sdo[x][i]);
+          sdr[x][i] = mma(fr, fs[x], sdr[x][i]);
+          dsu[x][i] = mma(fu, fd[x], dsu[x][i]);
         }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int d = 16 * j + r;
-        row8f(Sg + static_cast<size_t>(d) * a.V, vc, a.V, d < a.K, vec_v, x);
-        row8f(Dg + static_cast<size_t>(d) * a.V, vc, a.V, d < a.K, vec_v, y);
-        if ((j & 3) == w)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sdot = fmaf(x[i], y[i], sdot);
-        const Frag<NS> fs = split8<NS>(x), fd = split8<NS>(y);
-        sdo[j] = mma(fdo, fs, sdo[j]);
-        sdr[j] = mma(fdr, fs, sdr[j]);
-        dsu[j] = mma(fu, fd, dsu[j]);
+        dp[i] = mma(mydo, fu, dp[i]);
+        dl[i] = mma(mydr, fu, dl[i]);
       }
     }
     drv += __shfl_xor(drv, 16);
@@ -186,101 +341,114 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int grad_
     if (lane == 0) sdots[w] = sdot;
     if (q == 0) rowv[trow] = drv;
 
-    // W, M and the exponents' parts in the 64 x 64 products
-    float gt[4], bt[4], rkt[4], rqt[4], rx[4] = {0, 0, 0, 0}, rb[4] = {0, 0, 0, 0};
-    double Gt[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * w + 4 * q + i;
-      Gt[i] = G[t];
-      gt[i] = exp_of(Gt[i]);
-      bt[i] = sc[kScBeta * kDeltaC + t];
-      rkt[i] = sc[kScRk * kDeltaC + t];
-      rqt[i] = sc[kScRq * kDeltaC + t];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int s = 16 * j + r;
-      const double Gs = G[s];
-      const float rks = sc[kScRk * kDeltaC + s];
-      float cx = 0.0f;
+    {  // W, M and the exponents' parts in the 64 x 64 products: tokens 16 w ..
+      float bt[4], rkt[4], rqt[4], rx[4] = {0, 0, 0, 0}, rb[4] = {0, 0, 0, 0};
+      double Gt[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 16 * w + 4 * q + i;
-        const float e = s <= t ? exp_of(Gt[i] - Gs) : 0.0f;
-        const float wv = s <= t ? dp[j][i] * e : 0.0f;
-        const float le = s < t ? -dl[j][i] * e : 0.0f;  // dL E
-        const float kkv = rkt[i] * rks * kk[j][i];
-        const float xv = wv * (a.scale * rqt[i] * rks * qk[j][i]) + le * bt[i] * kkv;
-        Wm[t * kLP + s] = wv;
-        Mm[t * kLP + s] = le * bt[i];
-        rx[i] += xv;
-        rb[i] = fmaf(le, kkv, rb[i]);
-        cx += xv;
+        Gt[i] = G[t];
+        bt[i] = sc[kScBeta * kDeltaC + t];
+        rkt[i] = sc[kScRk * kDeltaC + t];
+        rqt[i] = a.scale * sc[kScRq * kDeltaC + t];
       }
-      cx += __shfl_xor(cx, 16);
-      cx += __shfl_xor(cx, 32);
-      if (q == 0) colx[w][s] = cx;
-    }
-    // the terms that meet the states, and their parts of the exponents
-    const double GC = G[kDeltaC - 1];
-    float sa[4] = {0, 0, 0, 0}, sb[4] = {0, 0, 0, 0}, scx[4] = {0, 0, 0, 0};
-    float el[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) el[i] = exp_of(GC - Gt[i]);
+      for (int j = 0; j < 4; ++j) {
+        const int s = 16 * j + r;
+        const double Gs = G[s];
+        const float rks = sc[kScRk * kDeltaC + s];
+        float cx = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+        for (int i = 0; i < 4; ++i) {
+          const int t = 16 * w + 4 * q + i;
+          const double diff = s <= t ? Gt[i] - Gs : -1e4;  // 0 above the diagonal, where e^{G_t - G_s} may overflow
+          const float e = exp_of(diff);
+          const float wv = s <= t ? dp[j][i] * e : 0.0f;
+          const float le = s < t ? -dl[j][i] * e : 0.0f;  // dL E
+          const float kkv = rkt[i] * rks * kk[j][i];
+          const float xv = wv * (rqt[i] * rks * qk[j][i]) + le * bt[i] * kkv;
+          Wm[t * kLP + s] = wv;
+          Mm[t * kLP + s] = le * bt[i];
+          rx[i] += xv;
+          rb[i] = fmaf(le, kkv, rb[i]);
+          cx += xv;
+        }
+        cx += __shfl_xor(cx, 16);
+        cx += __shfl_xor(cx, 32);
+        if (q == 0) colx[w][s] = cx;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float xq = gt[i] * sdo[j][i], xr = gt[i] * sdr[j][i], xu = el[i] * dsu[j][i];
-        sa[i] = fmaf(qC[j][i], xq, sa[i]);
-        sb[i] = fmaf(kC[j][i], xr, sb[i]);
-        scx[i] = fmaf(kC[j][i], xu, scx[i]);
-        dqa[j][i] += xq;
-        dka[j][i] += xu - bt[i] * xr;
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * w + 4 * q + i;
-      const float av = sum16(sa[i]) * rqt[i] * a.scale, bv = sum16(sb[i]) * rkt[i], cv = sum16(scx[i]) * rkt[i];
-      const float x = sum16(rx[i]), y = sum16(rb[i]);
-      if (r == 0) {
-        rowg[t] = av - bt[i] * bv - cv + x;
-        rowc[t] = cv;
-        rowb[t] = y - bv;
+        const float x = sum16(rx[i]), y = sum16(rb[i]);
+        if (r == 0) {
+          rowx[16 * w + 4 * q + i] = x;
+          rowb[16 * w + 4 * q + i] = y;
+        }
       }
     }
+    // the terms that meet the states, and their parts of the exponents
+    float cs = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * i + 4 * q + e;
+        const float gt = sc[kScEg * kDeltaC + t], el = sc[kScEl * kDeltaC + t], bt = sc[kScBeta * kDeltaC + t];
+        const float rk = sc[kScRk * kDeltaC + t], rq = a.scale * sc[kScRq * kDeltaC + t];
+        float sa = 0.0f, sb = 0.0f, su = 0.0f;
+#pragma unroll
+        for (int x = 0; x < TW; ++x) {
+          const float xq = gt * sdo[x][i][e], xr = gt * sdr[x][i][e], xu = el * dsu[x][i][e];
+          sa = fmaf(kq[x][i][e].q(), xq, sa);
+          sb = fmaf(kq[x][i][e].k(), xr, sb);
+          su = fmaf(kq[x][i][e].k(), xu, su);
+          dqa[x][i][e] += xq;
+          dka[x][i][e] += xu - bt * xr;
+        }
+        cs = fmaf(rk, su, cs);
+        sa = sum16(rq * sa - rk * fmaf(bt, sb, su));
+        sb = sum16(rk * sb);
+        if (r == 0) {
+          rowp[w][0][t] = sa;
+          rowp[w][1][t] = sb;
+        }
+      }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) cs += __shfl_xor(cs, o);
+    if (lane == 0) csums[w] = cs;
     __syncthreads();
-    // products of W and M with the rows of k and q
+    float nn[2][8];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      float wr[8], wc[8], nn[8];
+      float wr[8], wc[8];
       const int t = 16 * w + r, k0 = 32 * s + 8 * q;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float rk = sc[kScRk * kDeltaC + k0 + i], rq = sc[kScRq * kDeltaC + k0 + i];
         wr[i] = Wm[t * kLP + k0 + i] * rk;
         wc[i] = Wm[(k0 + i) * kLP + t] * (a.scale * rq);
-        nn[i] = (Mm[t * kLP + k0 + i] + Mm[(k0 + i) * kLP + t]) * rk;
+        nn[s][i] = (Mm[t * kLP + k0 + i] + Mm[(k0 + i) * kLP + t]) * rk;
       }
-      const Frag<NS> fw = split8<NS>(wr), fc = split8<NS>(wc), fn = split8<NS>(nn);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const Frag<NI> bk = load_frag<NI>(ktf, 2 * j + s, lane), bq = load_frag<NI>(qtf, 2 * j + s, lane);
-        if (s == 0 || w >= 2) dqa[j] = mma(fw, bk, dqa[j]);
-        if (s == 1 || w < 2) dka[j] = mma(fc, bq, dka[j]);
-        dka[j] = mma(fn, bk, dka[j]);
-      }
+      if (s == 0 || w >= 2) store_frag<NS>(wf, low_frag(w, s), lane, split8<NS>(wr));
+      if (s == 1 || w < 2) store_frag<NS>(cf, up_frag(w, s), lane, split8<NS>(wc));
     }
-    // dbeta, and dg as the running sum from the chunk's end
-    if (w == 0) {
-      double g = static_cast<double>(rowg[lane]) -
-                 (static_cast<double>(colx[0][lane]) + colx[1][lane] + colx[2][lane] + colx[3][lane]);
-      double cs = rowc[lane];
+    Frag<NI> bk[TW][2], bq[TW][2];
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) cs += __shfl_xor(cs, o);
+    for (int x = 0; x < TW; ++x)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        bk[x][s] = load_frag<NI>(ktf, 2 * (w * TW + x) + s, lane);
+        bq[x][s] = load_frag<NI>(qtf, 2 * (w * TW + x) + s, lane);
+      }
+    // dbeta, and dg as the running sum from the chunk's end
+    if (w == 3) {
+      const float av = rowp[0][0][lane] + rowp[1][0][lane] + rowp[2][0][lane] + rowp[3][0][lane];
+      const float bv = rowp[0][1][lane] + rowp[1][1][lane] + rowp[2][1][lane] + rowp[3][1][lane];
+      double g = static_cast<double>(av) + rowx[lane] -
+                 (static_cast<double>(colx[0][lane]) + colx[1][lane] + colx[2][lane] + colx[3][lane]);
       if (lane == kDeltaC - 1)
-        g += cs + static_cast<double>(sc[kScGamma * kDeltaC]) * (static_cast<double>(sdots[0]) + sdots[1] + sdots[2] + sdots[3]);
+        g += static_cast<double>(csums[0]) + csums[1] + csums[2] + csums[3] +
+             static_cast<double>(sc[kScGamma * kDeltaC]) * (static_cast<double>(sdots[0]) + sdots[1] + sdots[2] + sdots[3]);
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const double up = __shfl_down(g, o);
@@ -289,52 +457,102 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaArgs a, int grad_
       if (lane < n) {
         const size_t at = static_cast<size_t>(t0 + lane) * a.h + head;
         if (a.dg) a.dg[at] = static_cast<float>(g);
-        if (a.dbeta) a.dbeta[at] = rowv[lane] + rowb[lane];
+        if (a.dbeta) a.dbeta[at] = rowv[lane] + rowb[lane] - bv;
       }
     }
     __syncthreads();
-  }
-
-  // through the norms
-  const float* sc = a.sc + (static_cast<size_t>(slot) * a.h + kh * rep) * kDeltaSc;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = 16 * w + 4 * q + i;
-    const float rq = sc[kScRq * kDeltaC + t], rk = sc[kScRk * kDeltaC + t];
-    float dq = 0.0f, dk = 0.0f;
-    if (a.qk_norm) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        dq = fmaf(qC[j][i], dqa[j][i], dq);
-        dk = fmaf(kC[j][i], dka[j][i], dk);
-      }
-      dq = sum16(dq) * rq * rq;
-      dk = sum16(dk) * rk * rk;
-    }
-    if (t < n) {
-      const size_t at = (static_cast<size_t>(t0 + t) * a.hk + kh) * a.K;
+      for (int s = 0; s < 2; ++s) {
+        if (s <= i / 2) {
+          const Frag<NS> f = load_frag<NS>(wf, low_frag(i, s), lane);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int d = 16 * j + r;
-        if (d < a.K) {
-          if (a.dq) put_grad(a.dq, at + d, grad_dtype, a.scale * rq * (dqa[j][i] - qC[j][i] * dq));
-          if (a.dk) put_grad(a.dk, at + d, grad_dtype, rk * (dka[j][i] - kC[j][i] * dk));
+          for (int x = 0; x < TW; ++x) dqa[x][i] = mma(f, bk[x][s], dqa[x][i]);
+        }
+        if (s >= i / 2) {
+          const Frag<NS> f = load_frag<NS>(cf, up_frag(i, s), lane);
+#pragma unroll
+          for (int x = 0; x < TW; ++x) dka[x][i] = mma(f, bq[x][s], dka[x][i]);
         }
       }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) store_frag<NS>(nf, 2 * w + s, lane, split8<NS>(nn[s]));
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Frag<NS> f = load_frag<NS>(nf, 2 * i + s, lane);
+#pragma unroll
+        for (int x = 0; x < TW; ++x) dka[x][i] = mma(f, bk[x][s], dka[x][i]);
+      }
+    __syncthreads();
+  }
+
+  // through the norms (rk and rq are the same for every head), and out by whole rows
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float dq = 0.0f, dk = 0.0f;
+#pragma unroll
+      for (int x = 0; x < TW; ++x) {
+        dq = fmaf(kq[x][i][e].q(), dqa[x][i][e], dq);
+        dk = fmaf(kq[x][i][e].k(), dka[x][i][e], dk);
+      }
+      dq = sum16(dq);
+      dk = sum16(dk);
+      if (r == 0) {
+        rowp[w][0][16 * i + 4 * q + e] = dq;
+        rowp[w][1][16 * i + 4 * q + e] = dk;
+      }
     }
+  __syncthreads();
+  constexpr int opitch = KP + 4;
+  static_assert(kDeltaC * opitch <= 2 * kDeltaC * kLP, "a gradient's rows fit W and M");
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * i + 4 * q + e;
+        const float rr = sc[(which ? kScRk : kScRq) * kDeltaC + t];
+        float dot = rowp[0][which][t] + rowp[1][which][t] + rowp[2][which][t] + rowp[3][which][t];
+        dot = a.qk_norm ? dot * rr * rr : 0.0f;
+#pragma unroll
+        for (int x = 0; x < TW; ++x) {
+          const float g = which ? dka[x][i][e] - kq[x][i][e].k() * dot : dqa[x][i][e] - kq[x][i][e].q() * dot;
+          WM[t * opitch + 16 * (w * TW + x) + r] = (which ? 1.0f : a.scale) * rr * g;
+        }
+      }
+    __syncthreads();
+    void* const dst = which ? a.dk : a.dq;
+    constexpr int per = KP / 8;
+#pragma unroll
+    for (int p = tid; p < kDeltaC * per; p += 256) {
+      const int t = p / per, d = (p % per) * 8;
+      const float4 x = *reinterpret_cast<const float4*>(WM + t * opitch + d);
+      const float4 y = *reinterpret_cast<const float4*>(WM + t * opitch + d + 4);
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      if (dst && t < n && d < a.K) store8(dst, (static_cast<size_t>(t0 + t) * a.hk + kh) * a.K + d, grad_dtype, vec_qk_out, a.K - d, v);
+    }
+    __syncthreads();
   }
 }
 
 template <typename IN, int KP>
 hipError_t go(const DeltaLaunch& l, hipStream_t s) {
   const DeltaArgs& a = l.a;
-  const int vec_v = a.V % 4 == 0;
-  const uintptr_t need = l.in_dtype == kBF16 ? 7 : 15;
-  const int vec_in = vec_v && a.v_stride % 4 == 0 &&
-                     ((reinterpret_cast<uintptr_t>(a.v) | reinterpret_cast<uintptr_t>(a.dout)) & need) == 0;
-  hipLaunchKernelGGL((delta_grads_kernel<IN, KP>), dim3(static_cast<unsigned>(a.slots * a.hk)), dim3(256), 0, s, a,
-                     l.grad_dtype, vec_v, vec_in);
-  return hipGetLastError();
+  auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
+  const int vec_in = a.V % 8 == 0 && a.v_stride % 8 == 0 && al16(a.v) && al16(a.dout);
+  const int vec_out = a.V % 8 == 0 && al16(a.dv), vec_qk_out = a.K % 8 == 0 && al16(a.dq) && al16(a.dk);
+  return timed_launch(s, [&] {
+    hipLaunchKernelGGL((delta_grads_kernel<IN, KP>), dim3(static_cast<unsigned>(a.slots * a.hk)), dim3(256), 0, s, a,
+                       l.grad_dtype, vec_in, vec_out, vec_qk_out);
+  });
 }
 
 }  // namespace

@@ -125,6 +125,7 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
   const int nch = (sq.len + kDeltaC - 1) / kDeltaC;
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), r = lane & 15, q = lane >> 4;
   const int v0 = static_cast<int>(slice) * 16 * NV;
+  [[maybe_unused]] const int vp = delta_vp(a.V);
 
   f32x4 S[CT][NV];
 #pragma unroll
@@ -168,7 +169,7 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
 #pragma unroll
     for (int e = 0; e < NV; ++e)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // (rows past the end read the chunk's first and are dropped at their use)
+      for (int i = 0; i < 4; ++i) {  // (rows and channels past the end read others and are dropped at their use)
         const int t = 16 * w + 4 * q + i, v = v0 + 16 * e + r;
         const long row = t0 + (t < n ? t : 0);
         vv[e][i] = static_cast<const IN*>(a.v)[row * a.v_stride + static_cast<long>(head) * a.V + min(v, a.V - 1)];
@@ -214,11 +215,9 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
 #pragma unroll
         for (int e = 0; e < NV; ++e) {
           const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
-          float* dst = a.s_chunk + (hc * a.K + d) * a.V + v;
-          if (v < a.V)
+          float* dst = a.s_chunk + (hc * KP + d) * vp + v;
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (d + x < a.K) dst[static_cast<long>(x) * a.V] = S[i][e][x];
+          for (int x = 0; x < 4; ++x) dst[static_cast<long>(x) * vp] = S[i][e][x];
         }
     }
 
@@ -242,7 +241,7 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
       f32x4 rr;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        rr[i] = fmaf(beta[i], 16 * w + 4 * q + i < n ? to_f32(vv[e][i]) : 0.0f, -cr[i] * ks[i]);
+        rr[i] = fmaf(beta[i], 16 * w + 4 * q + i < n && v0 + 16 * e + r < a.V ? to_f32(vv[e][i]) : 0.0f, -cr[i] * ks[i]);
       put_tile<NS>(Rsh[e], r, 16 * w + 4 * q, rr);
     }
     load_rows(next);
@@ -263,10 +262,9 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
         put_tile<NO>(Wsh[e], r, 16 * w + 4 * q, u);
       } else {
         const int v = v0 + 16 * e + r;
-        float* dst = a.u_chunk + (hc * kDeltaC + 16 * w + 4 * q) * a.V + v;
-        if (v < a.V)
+        float* dst = a.u_chunk + (hc * kDeltaC + 16 * w + 4 * q) * vp + v;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dst[static_cast<long>(i) * a.V] = u[i];
+        for (int i = 0; i < 4; ++i) dst[static_cast<long>(i) * vp] = u[i];
       }
     }
     load_tri(next);
@@ -335,6 +333,7 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
   const int nch = (sq.len + kDeltaC - 1) / kDeltaC;
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), r = lane & 15, q = lane >> 4;
   const int v0 = static_cast<int>(slice) * 16 * NV;
+  [[maybe_unused]] const int vp = delta_vp(a.V);
 
   f32x4 D[CT][NV];
 #pragma unroll
@@ -416,18 +415,16 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
 #pragma unroll
       for (int e = 0; e < NV; ++e) {
         const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
-        float* dst = a.ds_chunk + (hc * a.K + d) * a.V + v;
-        if (v < a.V)
+        float* dst = a.ds_chunk + (hc * KP + d) * vp + v;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (d + x < a.K) dst[static_cast<long>(x) * a.V] = D[i][e][x];
+        for (int x = 0; x < 4; ++x) dst[static_cast<long>(x) * vp] = D[i][e][x];
       }
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
       f32x4 dd, cd;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        dd[i] = 16 * w + 4 * q + i < n ? to_f32(dv[e][i]) : 0.0f;
+        dd[i] = 16 * w + 4 * q + i < n && v0 + 16 * e + r < a.V ? to_f32(dv[e][i]) : 0.0f;
         cd[i] = co[i] * dd[i];
       }
       put_tile<NI>(Dsh[e], r, 16 * w + 4 * q, dd);
@@ -462,10 +459,9 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
       }
       put_tile<NS>(Ush[e], r, 16 * w + 4 * q, ys);
       const int v = v0 + 16 * e + r;
-      float* dst = a.dr_chunk + (hc * kDeltaC + 16 * w + 4 * q) * a.V + v;
-      if (v < a.V)
+      float* dst = a.dr_chunk + (hc * kDeltaC + 16 * w + 4 * q) * vp + v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dst[static_cast<long>(i) * a.V] = y[i];
+      for (int i = 0; i < 4; ++i) dst[static_cast<long>(i) * vp] = y[i];
     }
     load_tri(next);
     lds_barrier();  // dR
@@ -515,12 +511,15 @@ bool wide(const DeltaArgs& a) {
 
 template <typename IN, int KP, int NV>
 hipError_t go(const DeltaLaunch& l, int what, hipStream_t s) {
-  const int slices = (l.a.V + 16 * NV - 1) / (16 * NV);
+  // (the kept tiles are padded: their slices cover delta_vp channels)
+  const int slices = ((what == 0 ? l.a.V : delta_vp(l.a.V)) + 16 * NV - 1) / (16 * NV);
   const dim3 grid(grid_of(l.a, slices));
   const int ob = l.o_dtype == kBF16;
   const int vec_o = l.a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(l.a.o) & (ob ? 7 : 15)) == 0;
   if (what == 0)
-    hipLaunchKernelGGL((delta_pass_kernel<IN, KP, NV, false>), grid, dim3(256), 0, s, l.a, slices, ob, vec_o);
+    return timed_launch(s, [&] {
+      hipLaunchKernelGGL((delta_pass_kernel<IN, KP, NV, false>), grid, dim3(256), 0, s, l.a, slices, ob, vec_o);
+    });
   else if (what == 1)
     hipLaunchKernelGGL((delta_pass_kernel<IN, KP, NV, true>), grid, dim3(256), 0, s, l.a, slices, 0, 0);
   else

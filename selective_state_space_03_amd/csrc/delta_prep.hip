@@ -228,11 +228,13 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
   }
   if (tid < kDeltaC) {
     const double G = Gs[tid], GC = Gs[kDeltaC - 1];
-    const float eg = exp_of(G);
+    const float eg = exp_of(G), el = exp_of(GC - G);
     sc[kScBeta * kDeltaC + tid] = bs[tid];
     sc[kScR * kDeltaC + tid] = bs[tid] * eg * rks[tid];
     sc[kScO * kDeltaC + tid] = a.scale * eg * rqs[tid];
-    sc[kScU * kDeltaC + tid] = exp_of(GC - G) * rks[tid];
+    sc[kScU * kDeltaC + tid] = el * rks[tid];
+    sc[kScEg * kDeltaC + tid] = eg;
+    sc[kScEl * kDeltaC + tid] = el;
     sc[kScRk * kDeltaC + tid] = rks[tid];
     sc[kScRq * kDeltaC + tid] = rqs[tid];
     reinterpret_cast<double*>(sc + kScG * kDeltaC)[tid] = G;
