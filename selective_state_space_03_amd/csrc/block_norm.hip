@@ -318,7 +318,9 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (act) ao[c][i] = fmaf(d[c][i] * t[c][i], oi, ao[c][i]);
-          d[c][i] = fmaf(d[c][i] * ow[i], oi, -k * t[c][i]);
+          d[c][i] *= ow[i] * oi;
+          // (with one value the difference cancels: what is left is the epsilon's part)
+          d[c][i] = a.n == 1 ? d[c][i] * (a.eps * oi * oi) : fmaf(-k, t[c][i], d[c][i]);
         }
       }
     } else if (!a.dout) {
@@ -372,7 +374,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a) {
         const float n = a.gate_first ? x[c][i] * gate * inv : x[c][i] * inv;
         const float wn = a.norm_w ? w[i] : 1.0f;
         const float da = a.gate_first ? d[c][i] : d[c][i] * gate;
-        // (with one value the difference cancels: what is left is the epsilon's part)
+        // (one value: as above)
         const float dy = a.norm_w && a.n == 1 ? inv * inv * inv * a.eps * (da * wn) : inv * (da * wn - n * k);
         if (a.z) {
           const float dgate = a.gate_first ? dy * x[c][i] : d[c][i] * (n * wn);

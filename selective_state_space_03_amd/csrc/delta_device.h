@@ -102,6 +102,66 @@ __device__ __forceinline__ void zero_frag(Frag<NP>& f) {
 __device__ __forceinline__ int low_frag(int i, int s) { return i < 2 ? i : 2 * i - 2 + s; }
 __device__ __forceinline__ int up_frag(int i, int s) { return i < 2 ? 2 * i + s : i + 2; }
 
+// 8 consecutive values of a row of `width`, as loaded, and widened.  vec: whole
+// aligned groups (width a multiple of 8); columns past the end read the row's
+// first ones and are dropped when widened.
+template <typename IN>
+struct Row8;
+template <>
+struct Row8<bf16s> {
+  uint4 a;
+  __device__ __forceinline__ void load(const bf16s* row, int c, int width, bool vec) {
+    if (vec) {
+      a = *reinterpret_cast<const uint4*>(row + (c < width ? c : 0));
+    } else {
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = row[min(c + i, width - 1)].bits;
+      a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+  }
+  __device__ __forceinline__ void get(int left, float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = 2 * i < left ? __uint_as_float(w[i] << 16) : 0.0f;
+      v[2 * i + 1] = 2 * i + 1 < left ? __uint_as_float(w[i] & 0xffff0000u) : 0.0f;
+    }
+  }
+};
+template <>
+struct Row8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* row, int c, int width, bool vec) {
+    if (vec) {
+      const float4* p = reinterpret_cast<const float4*>(row + (c < width ? c : 0));
+      a = p[0];
+      b = p[1];
+    } else {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = row[min(c + i, width - 1)];
+      a = make_float4(v[0], v[1], v[2], v[3]);
+      b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+  __device__ __forceinline__ void get(int left, float (&v)[8]) const {
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? x[i] : 0.0f;
+  }
+};
+
+// 8 values into LDS in the inputs' type (they come from it)
+__device__ __forceinline__ void put8(bf16s* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_hi(v[0], v[1]), pack_hi(v[2], v[3]), pack_hi(v[4], v[5]), pack_hi(v[6], v[7]));
+}
+__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 // Waits for this wave's LDS accesses and joins the workgroup; global loads and
 // stores stay in flight across it.
 __device__ __forceinline__ void lds_barrier() {

@@ -12,11 +12,11 @@
 //
 // One workgroup takes a (chunk, key head) and its value heads in turn, so the
 // shared heads' dq and dk are summed in registers in a fixed order.  Wave w owns
-// the key channels 16 TW w .. (TW tiles of 16) for the products with S and D, so
-// those are read and split into bf16 parts once, and the tokens 16 w .. 16 w + 15
-// for everything else; the rows do, dR and u of 32 value channels at a time are
-// split by their token's wave and handed round through LDS, two buffers in turn,
-// with the next step's loads in flight.  64 x 64 products that meet a triangle
+// the key channels 16 w .. 16 w + 15 for the products with S and D, so those are
+// read and split into bf16 parts once, and a share of the tokens of row tile
+// rt = w % 4 for everything else; the rows do, dR and u of 32 value channels at a
+// time are split by their token's waves and handed round through LDS, two buffers
+// in turn, with the next step's loads in flight.  64 x 64 products that meet a triangle
 // take only the halves inside it.
 #include "delta_device.h"
 
@@ -25,65 +25,7 @@ namespace {
 
 constexpr int kLP = 68;  // floats per LDS row of a 64 x 64 matrix
 
-// 8 consecutive values of a row of `width`, as loaded, and widened.  vec: whole
-// aligned groups (width a multiple of 8); columns past the end read the row's
-// first ones and are dropped when widened.
-template <typename IN>
-struct Row8;
-template <>
-struct Row8<bf16s> {
-  uint4 a;
-  __device__ __forceinline__ void load(const bf16s* row, int c, int width, bool vec) {
-    if (vec) {
-      a = *reinterpret_cast<const uint4*>(row + (c < width ? c : 0));
-    } else {
-      uint32_t v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = row[min(c + i, width - 1)].bits;
-      a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-    }
-  }
-  __device__ __forceinline__ void get(int left, float (&v)[8]) const {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = 2 * i < left ? __uint_as_float(w[i] << 16) : 0.0f;
-      v[2 * i + 1] = 2 * i + 1 < left ? __uint_as_float(w[i] & 0xffff0000u) : 0.0f;
-    }
-  }
-};
-template <>
-struct Row8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* row, int c, int width, bool vec) {
-    if (vec) {
-      const float4* p = reinterpret_cast<const float4*>(row + (c < width ? c : 0));
-      a = p[0];
-      b = p[1];
-    } else {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = row[min(c + i, width - 1)];
-      a = make_float4(v[0], v[1], v[2], v[3]);
-      b = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  }
-  __device__ __forceinline__ void get(int left, float (&v)[8]) const {
-    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? x[i] : 0.0f;
-  }
-};
-
-// 8 values into LDS in the inputs' type (they come from it), and from there as an operand
-__device__ __forceinline__ void put8(bf16s* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack_hi(v[0], v[1]), pack_hi(v[2], v[3]), pack_hi(v[4], v[5]), pack_hi(v[6], v[7]));
-}
-__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+// 8 consecutive values of such a row as an operand
 __device__ __forceinline__ Frag<1> row_frag(const bf16s* p) {
   Frag<1> f;
   f.p[0] = *reinterpret_cast<const uint4*>(p);
@@ -153,22 +95,24 @@ __device__ __forceinline__ void store8(void* p, size_t i, int dtype, bool vec, i
   }
 }
 
-template <typename IN, int KP>
-__global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int grad_dtype, int vec_in, int vec_out,
-                                                              int vec_qk_out) {
+// VEC: rows of q, k, v, do, dq, dk and dv take 16-byte accesses (else element by element)
+template <typename IN, int KP, bool VEC>
+__global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs a, int grad_dtype) {
   using Parts = DeltaParts<IN>;
   constexpr int NI = Parts::in, NS = Parts::state;
-  constexpr int ND = KP / 32, TW = KP / 64;
+  constexpr int ND = KP / 32, NW = KP / 16, NT = 64 * NW;  // a wave per 16 key channels
+  constexpr int JT = 16 / NW;                              // column tiles (and, halved, token steps) per wave of a row tile
   constexpr int kDo = 4 * NI * kDeltaFrag, kRow = 4 * NS * kDeltaFrag;
   constexpr int kStage = kDo + 2 * kRow;
   __shared__ __align__(16) unsigned char stage[2 * kStage];
   __shared__ __align__(16) float WM[2 * kDeltaC * kLP];
   float* const Wm = WM;
   float* const Mm = WM + kDeltaC * kLP;
-  __shared__ float rowp[4][2][kDeltaC];
+  __shared__ float kkq[2][kDeltaC * kLP];   // k k^T, scale q k^T, with the norms
+  __shared__ float rowp[NW][2][kDeltaC];
   __shared__ float colx[4][kDeltaC];
   __shared__ __align__(16) float sc[kDeltaSc];  // the head's coefficients
-  __shared__ float rowx[kDeltaC], rowb[kDeltaC], rowv[kDeltaC], sdots[4], csums[4];
+  __shared__ float rowx[NW / 4][kDeltaC], rowb[NW / 4][kDeltaC], rowv[kDeltaC], sdots[NW], csums[NW];
   // after the last step the staging holds W and M as operands
   unsigned char* const wf = stage;                                     // rows of W: lower triangle
   unsigned char* const cf = stage + kDeltaTri * NS * kDeltaFrag;       // columns of W: upper triangle
@@ -181,6 +125,7 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
   const int n = delta_chunk(a, slot, &t0);
   if (n == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), r = lane & 15, q = lane >> 4;
+  const int rt = w & 3, hf = w >> 2;  // this wave's row tile, and its share of that tile's work
   const int vp = delta_vp(a.V), steps = vp / 32;
   const size_t kc = static_cast<size_t>(slot) * a.hk + kh;
   const size_t kbytes = 4 * ND * NI * kDeltaFrag;
@@ -194,18 +139,18 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
   IN* const Ks = reinterpret_cast<IN*>(stage);
   IN* const Qs = Ks + kDeltaC * pitch;
   {
-    constexpr int per = KP / 8, each = kDeltaC * per / 256;
+    constexpr int per = KP / 8, each = kDeltaC * per / NT;
     Row8<IN> rk[each], rq[each];
 #pragma unroll
     for (int i = 0; i < each; ++i) {
-      const int p = tid + 256 * i, t = p / per, d = (p % per) * 8;
+      const int p = tid + NT * i, t = p / per, d = (p % per) * 8;
       const long tt = t0 + (t < n ? t : 0), off = static_cast<long>(kh) * a.K;
-      rk[i].load(static_cast<const IN*>(a.k) + tt * a.k_stride + off, d, a.K, a.vec_qk);
-      rq[i].load(static_cast<const IN*>(a.q) + tt * a.q_stride + off, d, a.K, a.vec_qk);
+      rk[i].load(static_cast<const IN*>(a.k) + tt * a.k_stride + off, d, a.K, VEC);
+      rq[i].load(static_cast<const IN*>(a.q) + tt * a.q_stride + off, d, a.K, VEC);
     }
 #pragma unroll
     for (int i = 0; i < each; ++i) {
-      const int p = tid + 256 * i, t = p / per, d = (p % per) * 8;
+      const int p = tid + NT * i, t = p / per, d = (p % per) * 8;
       float v[8];
       rk[i].get(t < n ? a.K - d : 0, v);
       put8(Ks + t * pitch + d, v);
@@ -215,31 +160,44 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
   }
   __syncthreads();
   // q and k at this wave's channels, all tokens, in the accumulators' layout
-  KQ<IN> kq[TW][4][4];
-  f32x4 dqa[TW][4], dka[TW][4];
+  KQ<IN> kq[4][4];
+  f32x4 dqa[4], dka[4];
 #pragma unroll
-  for (int x = 0; x < TW; ++x)
+  for (int i = 0; i < 4; ++i) {
+    dqa[i] = dka[i] = zero;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dqa[x][i] = dka[x][i] = zero;
+    for (int e = 0; e < 4; ++e) {
+      const int at = (16 * i + 4 * q + e) * pitch + 16 * w + r;
+      kq[i][e].set(Ks[at], Qs[at]);
+    }
+  }
+  {  // the products of k and q with k, which every head uses, stay in LDS
+    const float* nrm = a.sc + (static_cast<size_t>(slot) * a.h + kh * rep) * kDeltaSc;
+    f32x4 kk[JT], qk[JT];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int at = (16 * i + 4 * q + e) * pitch + 16 * (w * TW + x) + r;
-        kq[x][i][e].set(Ks[at], Qs[at]);
+    for (int j = 0; j < JT; ++j) kk[j] = qk[j] = zero;
+#pragma unroll
+    for (int c = 0; c < ND; ++c) {
+      const int off = 32 * c + 8 * q;
+      const Frag<NI> fk = row_frag(Ks + (16 * rt + r) * pitch + off), fq = row_frag(Qs + (16 * rt + r) * pitch + off);
+#pragma unroll
+      for (int j = 0; j < JT; ++j) {
+        const Frag<NI> b = row_frag(Ks + (16 * (hf * JT + j) + r) * pitch + off);
+        kk[j] = mma(fk, b, kk[j]);
+        qk[j] = mma(fq, b, qk[j]);
       }
     }
-  f32x4 kk[4], qk[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) kk[j] = qk[j] = zero;
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * rt + 4 * q + i;
+      const float rk = nrm[kScRk * kDeltaC + t], rq = a.scale * nrm[kScRq * kDeltaC + t];
 #pragma unroll
-  for (int c = 0; c < ND; ++c) {
-    const int off = 32 * c + 8 * q;
-    const Frag<NI> fk = row_frag(Ks + (16 * w + r) * pitch + off), fq = row_frag(Qs + (16 * w + r) * pitch + off);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const Frag<NI> b = row_frag(Ks + (16 * j + r) * pitch + off);
-      kk[j] = mma(fk, b, kk[j]);
-      qk[j] = mma(fq, b, qk[j]);
+      for (int j = 0; j < JT; ++j) {
+        const int s = 16 * (hf * JT + j) + r;
+        const float rks = nrm[kScRk * kDeltaC + s];
+        kkq[0][t * kLP + s] = rk * rks * kk[j][i];
+        kkq[1][t * kLP + s] = rq * rks * qk[j][i];
+      }
     }
   }
   __syncthreads();
@@ -248,43 +206,48 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
   for (int hr = 0; hr < rep; ++hr) {
     const int head = kh * rep + hr;
     const size_t hc = static_cast<size_t>(slot) * a.h + head;
-    for (int i = tid; i < kDeltaSc; i += 256) sc[i] = a.sc[hc * kDeltaSc + i];  // (seen by all after the first step's barrier)
+    constexpr int kScEach = (kDeltaSc + NT - 1) / NT;
+    float scr[kScEach];
+#pragma unroll
+    for (int i = 0; i < kScEach; ++i) scr[i] = a.sc[hc * kDeltaSc + min(tid + NT * i, kDeltaSc - 1)];
     const double* G = reinterpret_cast<const double*>(sc + kScG * kDeltaC);
-    const int trow = 16 * w + r;  // this lane's token as an operand's row
+    const int trow = 16 * rt + r;  // this lane's token as an operand's row
     const bool live = trow < n;
     const size_t orow = (static_cast<size_t>(t0 + (live ? trow : 0)) * a.h + head) * a.V;
     const IN* const dorow = static_cast<const IN*>(a.dout) + orow;
     const IN* const vrow = static_cast<const IN*>(a.v) + (t0 + (live ? trow : 0)) * a.v_stride + static_cast<long>(head) * a.V;
-    const float* const rrow = a.dr_chunk + (hc * kDeltaC + trow) * vp;
     const float* const urow = a.u_chunk + (hc * kDeltaC + trow) * vp;
-    const float* const srow = a.s_chunk + (hc * KP + 16 * w * TW + r) * vp;
-    const float* const grow = a.ds_chunk + (hc * KP + 16 * w * TW + r) * vp;
+    const float* const rrow = NW == 4 || hf == 0 ? a.dr_chunk + (hc * kDeltaC + trow) * vp : urow;
+    const float* const srow = a.s_chunk + (hc * KP + 16 * w + r) * vp;
+    const float* const grow = a.ds_chunk + (hc * KP + 16 * w + r) * vp;
 
-    f32x4 sdo[TW][4], sdr[TW][4], dsu[TW][4], dp[4], dl[4];
+    f32x4 sdo[4], sdr[4], dsu[4], dp[JT], dl[JT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dp[i] = dl[i] = zero;
+    for (int i = 0; i < 4; ++i) sdo[i] = sdr[i] = dsu[i] = zero;
 #pragma unroll
-      for (int x = 0; x < TW; ++x) sdo[x][i] = sdr[x][i] = dsu[x][i] = zero;
-    }
+    for (int j = 0; j < JT; ++j) dp[j] = dl[j] = zero;
     float sdot = 0.0f, drv = 0.0f;
     const float brow = a.sc[hc * kDeltaSc + kScBeta * kDeltaC + trow];
 
+    // the rows of a tile: do, dR and v by its first wave, u by its last
+    const bool first = hf == 0;
     Row8<IN> ldo, lv;
-    Row8<float> lr, lu, ls[TW], ld[TW];
+    Row8<float> lr, lu, ls, ld;  // (with two waves to a tile lr holds dR in one, u in the other)
     auto load_step = [&](int c) {
       const int vc = 32 * c + 8 * q;
-      ldo.load(dorow, vc, a.V, vec_in);
-      lv.load(vrow, vc, a.V, vec_in);
-      lr.load(rrow, vc, vp, true);
-      lu.load(urow, vc, vp, true);
-#pragma unroll
-      for (int x = 0; x < TW; ++x) {
-        ls[x].load(srow + static_cast<size_t>(16 * x) * vp, vc, vp, true);
-        ld[x].load(grow + static_cast<size_t>(16 * x) * vp, vc, vp, true);
+      if (first) {
+        ldo.load(dorow, vc, a.V, VEC);
+        lv.load(vrow, vc, a.V, VEC);
       }
+      lr.load(rrow, vc, vp, true);
+      if (NW == 4) lu.load(urow, vc, vp, true);
+      ls.load(srow, vc, vp, true);
+      ld.load(grow, vc, vp, true);
     };
     load_step(0);
+#pragma unroll
+    for (int i = 0; i < kScEach; ++i)  // (seen by all after the first step's barrier)
+      if (tid + NT * i < kDeltaSc) sc[tid + NT * i] = scr[i];
 #pragma unroll 1
     for (int c = 0; c < steps; ++c) {
       unsigned char* const sdf = stage + (c & 1) * kStage;
@@ -292,46 +255,46 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
       unsigned char* const suf = srf + kRow;
       const int vc = 32 * c + 8 * q, left = live ? a.V - vc : 0;
       float x8[8], y8[8];
-      ldo.get(left, x8);
-      store_frag<NI>(sdf, w, lane, split8<NI>(x8));
+      if (first) {
+        ldo.get(left, x8);
+        store_frag<NI>(sdf, rt, lane, split8<NI>(x8));
+      }
       lr.get(8, x8);
-      store_frag<NS>(srf, w, lane, split8<NS>(x8));
-      lv.get(left, y8);
+      store_frag<NS>(NW == 4 || hf == 0 ? srf : suf, rt, lane, split8<NS>(x8));
+      if (first) {
+        lv.get(left, y8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) drv = fmaf(x8[i], y8[i], drv);
-      if (a.dv && left > 0) {
+        for (int i = 0; i < 8; ++i) drv = fmaf(x8[i], y8[i], drv);
+        if (a.dv && left > 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x8[i] *= brow;
-        store8(a.dv, orow + vc, grad_dtype, vec_out, left, x8);
+          for (int i = 0; i < 8; ++i) x8[i] *= brow;
+          store8(a.dv, orow + vc, grad_dtype, VEC, left, x8);
+        }
       }
-      lu.get(8, x8);
-      store_frag<NS>(suf, w, lane, split8<NS>(x8));
-      Frag<NS> fs[TW], fd[TW];
-#pragma unroll
-      for (int x = 0; x < TW; ++x) {
-        ls[x].get(8, x8);
-        ld[x].get(8, y8);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sdot = fmaf(x8[i], y8[i], sdot);
-        fs[x] = split8<NS>(x8);
-        fd[x] = split8<NS>(y8);
+      if (NW == 4) {
+        lu.get(8, x8);
+        store_frag<NS>(suf, rt, lane, split8<NS>(x8));
       }
+      ls.get(8, x8);
+      ld.get(8, y8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sdot = fmaf(x8[i], y8[i], sdot);
+      const Frag<NS> fs = split8<NS>(x8), fd = split8<NS>(y8);
       load_step(min(c + 1, steps - 1));
       lds_barrier();
-      const Frag<NI> mydo = load_frag<NI>(sdf, w, lane);
-      const Frag<NS> mydr = load_frag<NS>(srf, w, lane);
+      const Frag<NI> mydo = load_frag<NI>(sdf, rt, lane);
+      const Frag<NS> mydr = load_frag<NS>(srf, rt, lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const Frag<NI> fo = load_frag<NI>(sdf, i, lane);
-        const Frag<NS> fr = load_frag<NS>(srf, i, lane), fu = load_frag<NS>(suf, i, lane);
+        sdo[i] = mma(load_frag<NI>(sdf, i, lane), fs, sdo[i]);
+        sdr[i] = mma(load_frag<NS>(srf, i, lane), fs, sdr[i]);
+        dsu[i] = mma(load_frag<NS>(suf, i, lane), fd, dsu[i]);
+      }
 #pragma unroll
-        for (int x = 0; x < TW; ++x) {
-          sdo[x][i] = mma(fo, fs[x], sdo[x][i]);
-          sdr[x][i] = mma(fr, fs[x], sdr[x][i]);
-          dsu[x][i] = mma(fu, fd[x], dsu[x][i]);
-        }
-        dp[i] = mma(mydo, fu, dp[i]);
-        dl[i] = mma(mydr, fu, dl[i]);
+      for (int j = 0; j < JT; ++j) {
+        const Frag<NS> fu = load_frag<NS>(suf, hf * JT + j, lane);
+        dp[j] = mma(mydo, fu, dp[j]);
+        dl[j] = mma(mydr, fu, dl[j]);
       }
     }
     drv += __shfl_xor(drv, 16);
@@ -339,34 +302,31 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) sdot += __shfl_xor(sdot, o);
     if (lane == 0) sdots[w] = sdot;
-    if (q == 0) rowv[trow] = drv;
+    if (first && q == 0) rowv[trow] = drv;
 
-    {  // W, M and the exponents' parts in the 64 x 64 products: tokens 16 w ..
-      float bt[4], rkt[4], rqt[4], rx[4] = {0, 0, 0, 0}, rb[4] = {0, 0, 0, 0};
+    {  // W, M and the exponents' parts in the 64 x 64 products: row tile rt
+      float bt[4], rx[4] = {0, 0, 0, 0}, rb[4] = {0, 0, 0, 0};
       double Gt[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = 16 * w + 4 * q + i;
+        const int t = 16 * rt + 4 * q + i;
         Gt[i] = G[t];
         bt[i] = sc[kScBeta * kDeltaC + t];
-        rkt[i] = sc[kScRk * kDeltaC + t];
-        rqt[i] = a.scale * sc[kScRq * kDeltaC + t];
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int s = 16 * j + r;
+      for (int j = 0; j < JT; ++j) {
+        const int s = 16 * (hf * JT + j) + r;
         const double Gs = G[s];
-        const float rks = sc[kScRk * kDeltaC + s];
         float cx = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int t = 16 * w + 4 * q + i;
+          const int t = 16 * rt + 4 * q + i;
           const double diff = s <= t ? Gt[i] - Gs : -1e4;  // 0 above the diagonal, where e^{G_t - G_s} may overflow
           const float e = exp_of(diff);
           const float wv = s <= t ? dp[j][i] * e : 0.0f;
           const float le = s < t ? -dl[j][i] * e : 0.0f;  // dL E
-          const float kkv = rkt[i] * rks * kk[j][i];
-          const float xv = wv * (rqt[i] * rks * qk[j][i]) + le * bt[i] * kkv;
+          const float kkv = kkq[0][t * kLP + s];
+          const float xv = wv * kkq[1][t * kLP + s] + le * bt[i] * kkv;
           Wm[t * kLP + s] = wv;
           Mm[t * kLP + s] = le * bt[i];
           rx[i] += xv;
@@ -375,14 +335,14 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
         }
         cx += __shfl_xor(cx, 16);
         cx += __shfl_xor(cx, 32);
-        if (q == 0) colx[w][s] = cx;
+        if (q == 0) colx[rt][s] = cx;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float x = sum16(rx[i]), y = sum16(rb[i]);
         if (r == 0) {
-          rowx[16 * w + 4 * q + i] = x;
-          rowb[16 * w + 4 * q + i] = y;
+          rowx[hf][16 * rt + 4 * q + i] = x;
+          rowb[hf][16 * rt + 4 * q + i] = y;
         }
       }
     }
@@ -395,16 +355,11 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
         const int t = 16 * i + 4 * q + e;
         const float gt = sc[kScEg * kDeltaC + t], el = sc[kScEl * kDeltaC + t], bt = sc[kScBeta * kDeltaC + t];
         const float rk = sc[kScRk * kDeltaC + t], rq = a.scale * sc[kScRq * kDeltaC + t];
-        float sa = 0.0f, sb = 0.0f, su = 0.0f;
-#pragma unroll
-        for (int x = 0; x < TW; ++x) {
-          const float xq = gt * sdo[x][i][e], xr = gt * sdr[x][i][e], xu = el * dsu[x][i][e];
-          sa = fmaf(kq[x][i][e].q(), xq, sa);
-          sb = fmaf(kq[x][i][e].k(), xr, sb);
-          su = fmaf(kq[x][i][e].k(), xu, su);
-          dqa[x][i][e] += xq;
-          dka[x][i][e] += xu - bt * xr;
-        }
+        const float xq = gt * sdo[i][e], xr = gt * sdr[i][e], xu = el * dsu[i][e];
+        float sa = kq[i][e].q() * xq, sb = kq[i][e].k() * xr;
+        const float su = kq[i][e].k() * xu;
+        dqa[i][e] += xq;
+        dka[i][e] += xu - bt * xr;
         cs = fmaf(rk, su, cs);
         sa = sum16(rq * sa - rk * fmaf(bt, sb, su));
         sb = sum16(rk * sb);
@@ -417,38 +372,49 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
     for (int o = 1; o < 64; o <<= 1) cs += __shfl_xor(cs, o);
     if (lane == 0) csums[w] = cs;
     __syncthreads();
-    float nn[2][8];
+    constexpr int SW = JT / 2;  // token steps of this wave's row tile
+    float nn[SW][8];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int x = 0; x < SW; ++x) {
+      const int s = SW == 2 ? x : hf;
       float wr[8], wc[8];
-      const int t = 16 * w + r, k0 = 32 * s + 8 * q;
+      const int t = 16 * rt + r, k0 = 32 * s + 8 * q;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float rk = sc[kScRk * kDeltaC + k0 + i], rq = sc[kScRq * kDeltaC + k0 + i];
         wr[i] = Wm[t * kLP + k0 + i] * rk;
         wc[i] = Wm[(k0 + i) * kLP + t] * (a.scale * rq);
-        nn[s][i] = (Mm[t * kLP + k0 + i] + Mm[(k0 + i) * kLP + t]) * rk;
+        nn[x][i] = (Mm[t * kLP + k0 + i] + Mm[(k0 + i) * kLP + t]) * rk;
       }
-      if (s == 0 || w >= 2) store_frag<NS>(wf, low_frag(w, s), lane, split8<NS>(wr));
-      if (s == 1 || w < 2) store_frag<NS>(cf, up_frag(w, s), lane, split8<NS>(wc));
+      if (s == 0 || rt >= 2) store_frag<NS>(wf, low_frag(rt, s), lane, split8<NS>(wr));
+      if (s == 1 || rt < 2) store_frag<NS>(cf, up_frag(rt, s), lane, split8<NS>(wc));
     }
-    Frag<NI> bk[TW][2], bq[TW][2];
+    Frag<NI> bk[2], bq[2];
 #pragma unroll
-    for (int x = 0; x < TW; ++x)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        bk[x][s] = load_frag<NI>(ktf, 2 * (w * TW + x) + s, lane);
-        bq[x][s] = load_frag<NI>(qtf, 2 * (w * TW + x) + s, lane);
-      }
+    for (int s = 0; s < 2; ++s) {
+      bk[s] = load_frag<NI>(ktf, 2 * w + s, lane);
+      bq[s] = load_frag<NI>(qtf, 2 * w + s, lane);
+    }
     // dbeta, and dg as the running sum from the chunk's end
     if (w == 3) {
-      const float av = rowp[0][0][lane] + rowp[1][0][lane] + rowp[2][0][lane] + rowp[3][0][lane];
-      const float bv = rowp[0][1][lane] + rowp[1][1][lane] + rowp[2][1][lane] + rowp[3][1][lane];
-      double g = static_cast<double>(av) + rowx[lane] -
+      float av = 0.0f, bv = 0.0f, rx = 0.0f, rb = 0.0f;
+      double cs = 0.0, sd = 0.0;
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        av += rowp[x][0][lane];
+        bv += rowp[x][1][lane];
+        cs += csums[x];
+        sd += sdots[x];
+      }
+#pragma unroll
+      for (int x = 0; x < NW / 4; ++x) {
+        rx += rowx[x][lane];
+        rb += rowb[x][lane];
+      }
+      double g = static_cast<double>(av) + rx -
                  (static_cast<double>(colx[0][lane]) + colx[1][lane] + colx[2][lane] + colx[3][lane]);
       if (lane == kDeltaC - 1)
-        g += static_cast<double>(csums[0]) + csums[1] + csums[2] + csums[3] +
-             static_cast<double>(sc[kScGamma * kDeltaC]) * (static_cast<double>(sdots[0]) + sdots[1] + sdots[2] + sdots[3]);
+        g += cs + static_cast<double>(sc[kScGamma * kDeltaC]) * sd;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const double up = __shfl_down(g, o);
@@ -457,7 +423,7 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
       if (lane < n) {
         const size_t at = static_cast<size_t>(t0 + lane) * a.h + head;
         if (a.dg) a.dg[at] = static_cast<float>(g);
-        if (a.dbeta) a.dbeta[at] = rowv[lane] + rowb[lane] - bv;
+        if (a.dbeta) a.dbeta[at] = rowv[lane] + rb - bv;
       }
     }
     __syncthreads();
@@ -465,29 +431,17 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        if (s <= i / 2) {
-          const Frag<NS> f = load_frag<NS>(wf, low_frag(i, s), lane);
-#pragma unroll
-          for (int x = 0; x < TW; ++x) dqa[x][i] = mma(f, bk[x][s], dqa[x][i]);
-        }
-        if (s >= i / 2) {
-          const Frag<NS> f = load_frag<NS>(cf, up_frag(i, s), lane);
-#pragma unroll
-          for (int x = 0; x < TW; ++x) dka[x][i] = mma(f, bq[x][s], dka[x][i]);
-        }
+        if (s <= i / 2) dqa[i] = mma(load_frag<NS>(wf, low_frag(i, s), lane), bk[s], dqa[i]);
+        if (s >= i / 2) dka[i] = mma(load_frag<NS>(cf, up_frag(i, s), lane), bq[s], dka[i]);
       }
     __syncthreads();
 #pragma unroll
-    for (int s = 0; s < 2; ++s) store_frag<NS>(nf, 2 * w + s, lane, split8<NS>(nn[s]));
+    for (int x = 0; x < SW; ++x) store_frag<NS>(nf, 2 * rt + (SW == 2 ? x : hf), lane, split8<NS>(nn[x]));
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Frag<NS> f = load_frag<NS>(nf, 2 * i + s, lane);
-#pragma unroll
-        for (int x = 0; x < TW; ++x) dka[x][i] = mma(f, bk[x][s], dka[x][i]);
-      }
+      for (int s = 0; s < 2; ++s) dka[i] = mma(load_frag<NS>(nf, 2 * i + s, lane), bk[s], dka[i]);
     __syncthreads();
   }
 
@@ -496,14 +450,7 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float dq = 0.0f, dk = 0.0f;
-#pragma unroll
-      for (int x = 0; x < TW; ++x) {
-        dq = fmaf(kq[x][i][e].q(), dqa[x][i][e], dq);
-        dk = fmaf(kq[x][i][e].k(), dka[x][i][e], dk);
-      }
-      dq = sum16(dq);
-      dk = sum16(dk);
+      const float dq = sum16(kq[i][e].q() * dqa[i][e]), dk = sum16(kq[i][e].k() * dka[i][e]);
       if (r == 0) {
         rowp[w][0][16 * i + 4 * q + e] = dq;
         rowp[w][1][16 * i + 4 * q + e] = dk;
@@ -520,24 +467,23 @@ __global__ __launch_bounds__(256, 1) void delta_grads_kernel(DeltaArgs a, int gr
       for (int e = 0; e < 4; ++e) {
         const int t = 16 * i + 4 * q + e;
         const float rr = sc[(which ? kScRk : kScRq) * kDeltaC + t];
-        float dot = rowp[0][which][t] + rowp[1][which][t] + rowp[2][which][t] + rowp[3][which][t];
-        dot = a.qk_norm ? dot * rr * rr : 0.0f;
+        float dot = 0.0f;
 #pragma unroll
-        for (int x = 0; x < TW; ++x) {
-          const float g = which ? dka[x][i][e] - kq[x][i][e].k() * dot : dqa[x][i][e] - kq[x][i][e].q() * dot;
-          WM[t * opitch + 16 * (w * TW + x) + r] = (which ? 1.0f : a.scale) * rr * g;
-        }
+        for (int x = 0; x < NW; ++x) dot += rowp[x][which][t];
+        dot = a.qk_norm ? dot * rr * rr : 0.0f;
+        const float g = which ? dka[i][e] - kq[i][e].k() * dot : dqa[i][e] - kq[i][e].q() * dot;
+        WM[t * opitch + 16 * w + r] = (which ? 1.0f : a.scale) * rr * g;
       }
     __syncthreads();
     void* const dst = which ? a.dk : a.dq;
     constexpr int per = KP / 8;
 #pragma unroll
-    for (int p = tid; p < kDeltaC * per; p += 256) {
+    for (int p = tid; p < kDeltaC * per; p += NT) {
       const int t = p / per, d = (p % per) * 8;
       const float4 x = *reinterpret_cast<const float4*>(WM + t * opitch + d);
       const float4 y = *reinterpret_cast<const float4*>(WM + t * opitch + d + 4);
       const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      if (dst && t < n && d < a.K) store8(dst, (static_cast<size_t>(t0 + t) * a.hk + kh) * a.K + d, grad_dtype, vec_qk_out, a.K - d, v);
+      if (dst && t < n && d < a.K) store8(dst, (static_cast<size_t>(t0 + t) * a.hk + kh) * a.K + d, grad_dtype, VEC, a.K - d, v);
     }
     __syncthreads();
   }
@@ -547,11 +493,12 @@ template <typename IN, int KP>
 hipError_t go(const DeltaLaunch& l, hipStream_t s) {
   const DeltaArgs& a = l.a;
   auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  const int vec_in = a.V % 8 == 0 && a.v_stride % 8 == 0 && al16(a.v) && al16(a.dout);
-  const int vec_out = a.V % 8 == 0 && al16(a.dv), vec_qk_out = a.K % 8 == 0 && al16(a.dq) && al16(a.dk);
+  const bool vec = a.vec_qk && a.V % 8 == 0 && a.v_stride % 8 == 0 && al16(a.v) && al16(a.dout) && al16(a.dv) &&
+                   al16(a.dq) && al16(a.dk);
+  const dim3 grid(static_cast<unsigned>(a.slots * a.hk)), block(KP * 4);
   return timed_launch(s, [&] {
-    hipLaunchKernelGGL((delta_grads_kernel<IN, KP>), dim3(static_cast<unsigned>(a.slots * a.hk)), dim3(256), 0, s, a,
-                       l.grad_dtype, vec_in, vec_out, vec_qk_out);
+    if (vec) hipLaunchKernelGGL((delta_grads_kernel<IN, KP, true>), grid, block, 0, s, a, l.grad_dtype);
+    else hipLaunchKernelGGL((delta_grads_kernel<IN, KP, false>), grid, block, 0, s, a, l.grad_dtype);
   });
 }
 

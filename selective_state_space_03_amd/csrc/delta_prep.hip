@@ -8,7 +8,7 @@
 // holds a reset, g very negative, would lose their digits in 32); the inverse in
 // 32 bits: the four 16 x 16 diagonal blocks by substitution, one wave each, the
 // blocks below them as T_ij = -T_ii sum_m L_im T_mj with 32-bit matrix
-// instructions, one diagonal after the other.  q and k enter the products
+// instructions, first within the two halves, then between them.  q and k enter the products
 // unscaled (bf16 rows are exact operands); the reciprocal norms, decays, gates
 // and the readout scale are folded into L, P and per-token coefficients.
 #include "delta_device.h"
@@ -17,48 +17,6 @@ namespace ssm {
 namespace {
 
 constexpr int kLP = 68;  // floats per LDS row of a 64 x 64 matrix
-
-template <typename IN>
-__device__ __forceinline__ void row8(const IN* row, int d0, int K, bool vec, float (&v)[8]);
-
-template <>
-__device__ __forceinline__ void row8<bf16s>(const bf16s* row, int d0, int K, bool vec, float (&v)[8]) {
-  if (vec) {
-    const uint4 r = load16_if(row + d0, d0 < K);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = d0 + i < K ? to_f32(row[d0 + i]) : 0.0f;
-  }
-}
-template <>
-__device__ __forceinline__ void row8<float>(const float* row, int d0, int K, bool vec, float (&v)[8]) {
-  if (vec) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 r = load16_if(row + d0 + 4 * h, d0 < K);
-      v[4 * h] = __uint_as_float(r.x); v[4 * h + 1] = __uint_as_float(r.y);
-      v[4 * h + 2] = __uint_as_float(r.z); v[4 * h + 3] = __uint_as_float(r.w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = d0 + i < K ? row[d0 + i] : 0.0f;
-  }
-}
-
-__device__ __forceinline__ void put8(bf16s* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack_hi(v[0], v[1]), pack_hi(v[2], v[3]), pack_hi(v[4], v[5]), pack_hi(v[6], v[7]));
-}
-__device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
 
 // 8 values of an LDS tile as an operand: `lo` and `hi` point at 4 consecutive ones each
 __device__ __forceinline__ Frag<1> frag44(const bf16s* lo, const bf16s* hi) {
@@ -114,7 +72,7 @@ __device__ __forceinline__ f32x4 mma16(const float* A, const float* B, int r, in
 __device__ __forceinline__ float exp_of(double x) { return exp2_fast(static_cast<float>(x * 1.4426950408889634)); }
 
 template <typename IN, int KP, bool BWD>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int parts) {
   using Parts = DeltaParts<IN>;
   constexpr int NI = Parts::in, NS = Parts::state, NO = Parts::out;
   constexpr int ND = KP / 32;                              // 32-channel steps
@@ -123,60 +81,67 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
   constexpr int mat = kDeltaC * kLP * 4;
   __shared__ __align__(16) unsigned char qk_raw[2 * tile > mat ? 2 * tile : mat];
   __shared__ __align__(16) float Lm[kDeltaC * kLP];
-  __shared__ __align__(16) float Tm[kDeltaC * kLP];
   __shared__ double Gs[kDeltaC];
   __shared__ float bs[kDeltaC], rks[kDeltaC], rqs[kDeltaC];
   IN* const Ks = reinterpret_cast<IN*>(qk_raw);
   IN* const Qs = reinterpret_cast<IN*>(qk_raw + tile);
-  float* const Pm = reinterpret_cast<float*>(qk_raw);  // after the last use of Ks and Qs
+  // after the last use of Ks and Qs their room holds a head's P, then its T
+  float* const Pm = reinterpret_cast<float*>(qk_raw);
+  float* const Tm = Pm;
 
-  const long slot = blockIdx.x / a.h;
-  const int head = static_cast<int>(blockIdx.x - slot * a.h);
-  const int kh = head / (a.h / a.hk);
+  const unsigned groups = static_cast<unsigned>(a.hk) * parts;
+  const long slot = blockIdx.x / groups;
+  const int kp = static_cast<int>(blockIdx.x - slot * groups);
+  const int kh = kp / parts, part = kp - kh * parts;
+  const int rep = a.h / a.hk;
+  const int h0 = kh * rep + static_cast<int>(static_cast<long>(part) * rep / parts);
+  const int h1 = kh * rep + static_cast<int>(static_cast<long>(part + 1) * rep / parts);
   long t0 = 0;
   const int n = delta_chunk(a, slot, &t0);
   if (n == 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, r = lane & 15, q = lane >> 4;
-  float* const sc = a.sc + (slot * a.h + head) * kDeltaSc;
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), r = lane & 15, q = lane >> 4;
 
-  if (w == 0) {
-    const size_t at = static_cast<size_t>(t0 + lane) * a.h + head;
-    double g = lane < n ? static_cast<double>(a.g[at]) : 0.0;
-    g = g < -1e4 ? -1e4 : g;  // e^-10000 is 0 in 32 bits already; -inf would make differences NaN
+  // the chunk's q and k rows, zeros past its end and past K; wave 0 also holds the
+  // next head's g and beta
+  const size_t grow = static_cast<size_t>(t0 + (lane < n ? lane : 0)) * a.h;
+  float gl = a.g[grow + h0], bl = a.beta[grow + h0];
+  {
+    constexpr int per = KP / 8, each = kDeltaC * per / 256;
+    Row8<IN> rk[each], rq[each];
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double up = __shfl_up(g, o);
-      if (lane >= o) g += up;
+    for (int i = 0; i < each; ++i) {
+      const int p = tid + 256 * i, t = p / per, d = (p % per) * 8;
+      const long tt = t0 + (t < n ? t : 0), off = static_cast<long>(kh) * a.K;
+      rk[i].load(static_cast<const IN*>(a.k) + tt * a.k_stride + off, d, a.K, a.vec_qk);
+      rq[i].load(static_cast<const IN*>(a.q) + tt * a.q_stride + off, d, a.K, a.vec_qk);
     }
-    Gs[lane] = g;
-    bs[lane] = lane < n ? a.beta[at] : 0.0f;
-  }
-  {  // the chunk's q and k rows, zeros past its end and past K
-    constexpr int per = KP / 8;
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      const IN* src = static_cast<const IN*>(which ? a.q : a.k);
-      const long stride = which ? a.q_stride : a.k_stride;
-      IN* dst = which ? Qs : Ks;
-      float* rs = which ? rqs : rks;
 #pragma unroll
-      for (int p = tid; p < kDeltaC * per; p += 256) {
-        const int t = p / per, d0 = (p % per) * 8;
-        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        if (t < n) row8<IN>(src + (t0 + t) * stride + static_cast<long>(kh) * a.K, d0, a.K, a.vec_qk, v);
-        put8(dst + t * pitch + d0, v);
-        float ss = 0.0f;
+    for (int i = 0; i < each; ++i) {
+      const int p = tid + 256 * i, t = p / per, d = (p % per) * 8;
+      float v[8], u[8], sk = 0.0f, sq = 0.0f;
+      rk[i].get(t < n ? a.K - d : 0, v);
+      rq[i].get(t < n ? a.K - d : 0, u);
+      put8(Ks + t * pitch + d, v);
+      put8(Qs + t * pitch + d, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+      for (int x = 0; x < 8; ++x) {
+        sk = fmaf(v[x], v[x], sk);
+        sq = fmaf(u[x], u[x], sq);
+      }
 #pragma unroll
-        for (int o = 1; o < per; o <<= 1) ss += __shfl_xor(ss, o);
-        if (d0 == 0) rs[t] = a.qk_norm ? 1.0f / sqrtf(ss + a.eps) : 1.0f;
+      for (int o = 1; o < per; o <<= 1) {
+        sk += __shfl_xor(sk, o);
+        sq += __shfl_xor(sq, o);
+      }
+      if (d == 0) {
+        rks[t] = a.qk_norm ? 1.0f / sqrtf(sk + a.eps) : 1.0f;
+        rqs[t] = a.qk_norm ? 1.0f / sqrtf(sq + a.eps) : 1.0f;
       }
     }
   }
   __syncthreads();
 
-  // k k^T and q k^T, row tile w against the column tiles up to it
+  // k k^T and q k^T, row tile w
   f32x4 kk[4], qk[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -186,133 +151,193 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
     const Frag<NI> fk = frag44(Ks + (16 * w + r) * pitch + off, Ks + (16 * w + r) * pitch + off + 4);
     const Frag<NI> fq = frag44(Qs + (16 * w + r) * pitch + off, Qs + (16 * w + r) * pitch + off + 4);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j <= w) {
-        const Frag<NI> b = frag44(Ks + (16 * j + r) * pitch + off, Ks + (16 * j + r) * pitch + off + 4);
-        kk[j] = mma(fk, b, kk[j]);
-        qk[j] = mma(fq, b, qk[j]);
-      }
+    for (int j = 0; j < 4; ++j) {  // (the tiles above the diagonal too: no branch among the products)
+      const Frag<NI> b = frag44(Ks + (16 * j + r) * pitch + off, Ks + (16 * j + r) * pitch + off + 4);
+      kk[j] = mma(fk, b, kk[j]);
+      qk[j] = mma(fq, b, qk[j]);
+    }
   }
+  // norms and the readout scale go into the products, which every head shares
+  float rkt[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int i = 0; i < 4; ++i) {
+    const int t = 16 * w + 4 * q + i;
+    rkt[i] = rks[t];
+    const float rqt = a.scale * rqs[t];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * w + 4 * q + i, s = 16 * j + r;
-      const bool in = s <= t;  // above the diagonal the decay may overflow: never formed
-      const float dec = in ? exp_of(Gs[t] - Gs[s]) * rks[s] : 0.0f;
-      Lm[t * kLP + s] = s < t ? bs[t] * rks[t] * dec * kk[j][i] : 0.0f;
-      qk[j][i] = in ? a.scale * rqs[t] * dec * qk[j][i] : 0.0f;
+    for (int j = 0; j < 4; ++j) {
+      kk[j][i] *= rkt[i] * rks[16 * j + r];
+      qk[j][i] *= rqt * rks[16 * j + r];
     }
   }
   // operands shared by the key head's value heads
-  if (head % (a.h / a.hk) == 0) {
+  if (part == 0) {
     const size_t at = static_cast<size_t>(slot) * a.hk + kh;
-    unsigned char* kf = a.kf + at * (4 * ND * NI * kDeltaFrag);
-    unsigned char* qf = a.qf + at * (4 * ND * NI * kDeltaFrag);
+    constexpr size_t bytes = 4 * ND * NI * kDeltaFrag;
 #pragma unroll
     for (int c = 0; c < ND; ++c) {
       const int o = (16 * w + r) * pitch + 32 * c + 4 * q;
-      store_frag<NI>(kf, w * ND + c, lane, frag44(Ks + o, Ks + o + 16));
-      store_frag<NI>(qf, w * ND + c, lane, frag44(Qs + o, Qs + o + 16));
+      store_frag<NI>(a.kf + at * bytes, w * ND + c, lane, frag44(Ks + o, Ks + o + 16));
+      if (!BWD) store_frag<NI>(a.qf + at * bytes, w * ND + c, lane, frag44(Qs + o, Qs + o + 16));
     }
-    unsigned char* ktf = a.ktf + at * (4 * ND * NI * kDeltaFrag);
-    unsigned char* qtf = BWD ? a.qtf + at * (4 * ND * NI * kDeltaFrag) : nullptr;
 #pragma unroll
     for (int ct = w; ct < KP / 16; ct += 4)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int o = (32 * s + 8 * q) * pitch + 16 * ct + r;
-        store_frag<NI>(ktf, 2 * ct + s, lane, frag_col(Ks + o, pitch));
-        if (BWD) store_frag<NI>(qtf, 2 * ct + s, lane, frag_col(Qs + o, pitch));
+        store_frag<NI>(a.ktf + at * bytes, 2 * ct + s, lane, frag_col(Ks + o, pitch));
+        if (BWD) store_frag<NI>(a.qtf + at * bytes, 2 * ct + s, lane, frag_col(Qs + o, pitch));
       }
   }
-  if (tid < kDeltaC) {
-    const double G = Gs[tid], GC = Gs[kDeltaC - 1];
-    const float eg = exp_of(G), el = exp_of(GC - G);
-    sc[kScBeta * kDeltaC + tid] = bs[tid];
-    sc[kScR * kDeltaC + tid] = bs[tid] * eg * rks[tid];
-    sc[kScO * kDeltaC + tid] = a.scale * eg * rqs[tid];
-    sc[kScU * kDeltaC + tid] = el * rks[tid];
-    sc[kScEg * kDeltaC + tid] = eg;
-    sc[kScEl * kDeltaC + tid] = el;
-    sc[kScRk * kDeltaC + tid] = rks[tid];
-    sc[kScRq * kDeltaC + tid] = rqs[tid];
-    reinterpret_cast<double*>(sc + kScG * kDeltaC)[tid] = G;
-    if (tid == 0) sc[kScGamma * kDeltaC] = exp_of(GC);
-  }
-  __syncthreads();
 
-  // P takes the rows' place; the diagonal blocks of T by substitution
+#pragma unroll 1
+  for (int head = h0; head < h1; ++head) {
+    const size_t at = static_cast<size_t>(slot) * a.h + head;
+    float* const sc = a.sc + at * kDeltaSc;
+    if (w == 0) {  // the running sum of g, in 64 bits
+      double g = lane < n ? static_cast<double>(gl) : 0.0;
+      g = g < -1e4 ? -1e4 : g;  // e^-10000 is 0 in 32 bits already; -inf would make differences NaN
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) Pm[(16 * w + 4 * q + i) * kLP + 16 * j + r] = qk[j][i];
-  {
-    float x[16];  // column r of block w's inverse (every 16-lane row of the wave alike)
-    const float* Lw = Lm + 16 * w * kLP + 16 * w;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float s = i == r ? 1.0f : 0.0f;
-#pragma unroll
-      for (int m = 0; m < i; ++m) s = fmaf(-Lw[i * kLP + m], x[m], s);
-      x[i] = s;
+      for (int o = 1; o < 64; o <<= 1) {
+        const double up = __shfl_up(g, o);
+        if (lane >= o) g += up;
+      }
+      const float b = lane < n ? bl : 0.0f;
+      Gs[lane] = g;
+      bs[lane] = b;
+      const int next = min(head + 1, h1 - 1);
+      gl = a.g[grow + next];
+      bl = a.beta[grow + next];
+      const double GC = __shfl(g, 63);
+      const float eg = exp_of(g), el = exp_of(GC - g), rk = rks[lane], rq = rqs[lane];
+      sc[kScBeta * kDeltaC + lane] = b;
+      sc[kScR * kDeltaC + lane] = b * eg * rk;
+      sc[kScO * kDeltaC + lane] = a.scale * eg * rq;
+      sc[kScU * kDeltaC + lane] = el * rk;
+      sc[kScEg * kDeltaC + lane] = eg;
+      sc[kScEl * kDeltaC + lane] = el;
+      sc[kScRk * kDeltaC + lane] = rk;
+      sc[kScRq * kDeltaC + lane] = rq;
+      reinterpret_cast<double*>(sc + kScG * kDeltaC)[lane] = g;
+      if (lane == 0) sc[kScGamma * kDeltaC] = exp_of(GC);
     }
+    __syncthreads();  // G; the room of q and k (or of the head before) is free
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * w + 4 * q + i;
+      const double Gt = Gs[t];
+      const float bt = bs[t];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int s = 16 * j + r;
+        // 0 above the diagonal, where the decay may overflow
+        const float dec = exp_of(s <= t ? Gt - Gs[s] : -1e4);
+        Lm[t * kLP + s] = s < t ? bt * dec * kk[j][i] : 0.0f;
+        Pm[t * kLP + s] = s <= t ? dec * qk[j][i] : 0.0f;
+      }
+    }
+    __syncthreads();
+    if (!BWD) {
+      unsigned char* pf = a.pf + at * (kDeltaTri * NO * kDeltaFrag);
+      for (int s = 0; s <= (w >> 1); ++s)
+        store_frag<NO>(pf, low_frag(w, s), lane, frag_row<NO>(Pm + (16 * w + r) * kLP + 32 * s + 8 * q));
+    } else {
+      unsigned char* ptf = a.ptf + at * (kDeltaTri * NS * kDeltaFrag);
+      for (int s = w >> 1; s < 2; ++s)
+        store_frag<NS>(ptf, up_frag(w, s), lane, frag_fcol<NS>(Pm + (32 * s + 8 * q) * kLP + 16 * w + r));
+    }
+    // the diagonal blocks of T by substitution: column r of block w's inverse in
+    // every 16-lane row of the wave; x[m] leaves the later rows' sums as soon as it is known
+    float x[16];
+    {
+      const float* Lw = Lm + 16 * w * kLP + 16 * w;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = i == r ? 1.0f : 0.0f;
+#pragma unroll
+      for (int m4 = 0; m4 < 4; ++m4) {  // four of L's columns at a time
+        float Lr[16][4];
+#pragma unroll
+        for (int i = 1; i < 16; ++i)
+          if (i > 4 * m4) {
+            const float4 f = *reinterpret_cast<const float4*>(Lw + i * kLP + 4 * m4);
+            Lr[i][0] = f.x; Lr[i][1] = f.y; Lr[i][2] = f.z; Lr[i][3] = f.w;
+          }
+#pragma unroll
+        for (int mm = 0; mm < 4; ++mm)
+#pragma unroll
+          for (int i = 1; i < 16; ++i)
+            if (i > 4 * m4 + mm) x[i] = fmaf(-Lr[i][mm], x[4 * m4 + mm], x[i]);
+        __builtin_amdgcn_sched_barrier(0);  // keeps the next columns' loads out of these registers
+      }
+    }
+    __syncthreads();  // P is out
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if ((i >> 2) == q) Tm[(16 * w + i) * kLP + 16 * w + r] = x[i];
     // blocks above the diagonal are read as operands where a step spans them
-    for (int j = w + 1; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) Tm[(16 * w + 4 * q + i) * kLP + 16 * j + r] = 0.0f;
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int dist = 1; dist < 4; ++dist) {
-    const int i = w, j = w - dist;  // one block of this diagonal per wave
-    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (j >= 0) {
-      for (int m = j; m < i; ++m)
-        sum = mma16(Lm + 16 * i * kLP + 16 * m, Tm + 16 * m * kLP + 16 * j, r, q, sum);
+    for (int j = 1; j < 4; ++j)
+      if (j > w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Tm[(16 * w + 4 * q + i) * kLP + 16 * j + r] = 0.0f;
+    __syncthreads();
+    // then T_ij = -T_ii sum_m L_im T_mj: the blocks (1, 0) and (3, 2), then the
+    // 32 x 32 block below the two halves, a wave per 16 x 16 block
+    const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+    {
+      const int i = w | 1, j = i - 1;  // waves 0, 1: block (1, 0); waves 2, 3: block (3, 2)
+      const f32x4 sum = mma16(Lm + 16 * i * kLP + 16 * j, Tm + 16 * j * kLP + 16 * j, r, q, z);
+      // (L's own block holds the sum now: both waves of a block write the same values)
 #pragma unroll
       for (int e = 0; e < 4; ++e) Tm[(16 * i + 4 * q + e) * kLP + 16 * j + r] = -sum[e];
-    }
-    __syncthreads();
-    if (j >= 0) {
-      const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-      sum = mma16(Tm + 16 * i * kLP + 16 * i, Tm + 16 * i * kLP + 16 * j, r, q, z);
-      // this wave alone reads and writes block (i, j) between the barriers
+      __syncthreads();
+      const f32x4 t = mma16(Tm + 16 * i * kLP + 16 * i, Tm + 16 * i * kLP + 16 * j, r, q, z);
+      __syncthreads();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) Tm[(16 * i + 4 * q + e) * kLP + 16 * j + r] = sum[e];
+      for (int e = 0; e < 4; ++e) Tm[(16 * i + 4 * q + e) * kLP + 16 * j + r] = t[e];
+      __syncthreads();
     }
-    __syncthreads();
-  }
-
-  const size_t at = static_cast<size_t>(slot) * a.h + head;
-  unsigned char* tf = a.tf + at * (kDeltaTri * NS * kDeltaFrag);
-  unsigned char* pf = BWD ? nullptr : a.pf + at * (kDeltaTri * NO * kDeltaFrag);
-  for (int s = 0; s <= (w >> 1); ++s) {
-    const int o = (16 * w + r) * kLP + 32 * s + 8 * q;
-    store_frag<NS>(tf, low_frag(w, s), lane, frag_row<NS>(Tm + o));
-    if (!BWD) store_frag<NO>(pf, low_frag(w, s), lane, frag_row<NO>(Pm + o));
-  }
-  if (BWD) {
-    unsigned char* ttf = a.ttf + at * (kDeltaTri * NS * kDeltaFrag);
-    unsigned char* ptf = a.ptf + at * (kDeltaTri * NS * kDeltaFrag);
-    for (int s = w >> 1; s < 2; ++s) {
-      const int o = (32 * s + 8 * q) * kLP + 16 * w + r;
-      store_frag<NS>(ttf, up_frag(w, s), lane, frag_fcol<NS>(Tm + o));
-      store_frag<NS>(ptf, up_frag(w, s), lane, frag_fcol<NS>(Pm + o));
+    {
+      const int i = 2 + (w >> 1), j = w & 1;
+      f32x4 sum = mma16(Lm + 16 * i * kLP, Tm + 16 * j, r, q, z);
+      sum = mma16(Lm + 16 * i * kLP + 16, Tm + 16 * kLP + 16 * j, r, q, sum);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Tm[(16 * i + 4 * q + e) * kLP + 16 * j + r] = -sum[e];
+      __syncthreads();
+      f32x4 t = mma16(Tm + 16 * i * kLP + 32, Tm + 32 * kLP + 16 * j, r, q, z);
+      t = mma16(Tm + 16 * i * kLP + 48, Tm + 48 * kLP + 16 * j, r, q, t);
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) Tm[(16 * i + 4 * q + e) * kLP + 16 * j + r] = t[e];
+      __syncthreads();
+    }
+    unsigned char* tf = a.tf + at * (kDeltaTri * NS * kDeltaFrag);
+    for (int s = 0; s <= (w >> 1); ++s)
+      store_frag<NS>(tf, low_frag(w, s), lane, frag_row<NS>(Tm + (16 * w + r) * kLP + 32 * s + 8 * q));
+    if (BWD) {
+      unsigned char* ttf = a.ttf + at * (kDeltaTri * NS * kDeltaFrag);
+      for (int s = w >> 1; s < 2; ++s)
+        store_frag<NS>(ttf, up_frag(w, s), lane, frag_fcol<NS>(Tm + (32 * s + 8 * q) * kLP + 16 * w + r));
     }
   }
 }
 
+// Workgroups per (chunk, key head): the value heads share the rows and their
+// products, so a workgroup takes as many as leave the GPU's CUs eight each.
+int head_parts(const DeltaArgs& a) {
+  const long rep = a.h / a.hk, want = 8L * 256, have = a.slots * a.hk;
+  const long parts = (want + have - 1) / have;
+  return static_cast<int>(parts < rep ? parts : rep);
+}
+
 template <typename IN, int KP>
 hipError_t go(const DeltaLaunch& l, bool bwd, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(l.a.slots * l.a.h));
+  const int parts = head_parts(l.a);
+  const dim3 grid(static_cast<unsigned>(l.a.slots * l.a.hk * parts));
   if (bwd)
-    hipLaunchKernelGGL((delta_prep_kernel<IN, KP, true>), grid, dim3(256), 0, s, l.a);
+    hipLaunchKernelGGL((delta_prep_kernel<IN, KP, true>), grid, dim3(256), 0, s, l.a, parts);
   else
-    hipLaunchKernelGGL((delta_prep_kernel<IN, KP, false>), grid, dim3(256), 0, s, l.a);
+    hipLaunchKernelGGL((delta_prep_kernel<IN, KP, false>), grid, dim3(256), 0, s, l.a, parts);
   return hipGetLastError();
 }
 

@@ -16,6 +16,11 @@ TOL = 1e-5
 BF, F32 = torch.bfloat16, torch.float32
 
 
+@pytest.fixture(autouse=True)
+def _seed():
+    torch.manual_seed(0)
+
+
 def _inputs(seed, rows, d, dtype, opt, res_dtype=F32):
     gen = torch.Generator(device=DEV).manual_seed(seed)
     rnd = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731

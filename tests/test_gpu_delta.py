@@ -19,6 +19,11 @@ TOL_F32 = 1e-5
 TOL_O_BF16 = 1e-4
 
 
+@pytest.fixture(autouse=True)
+def _seed():
+    torch.manual_seed(0)
+
+
 def _case(seed, n, L, Hk, H, K, V, dtype=torch.float32, unit=True, cu=None, state=True, gmin=-1.0):
     gen = torch.Generator(device=DEV).manual_seed(seed)
     rnd = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731
