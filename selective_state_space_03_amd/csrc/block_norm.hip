@@ -115,8 +115,9 @@ __device__ __forceinline__ void put8(void* base, size_t row, int i0, int n, int 
   }
 }
 
-// Sums of NS values over the TPR lanes of a row.  sh: NS x waves floats, one of
-// two copies used in turn, so a copy is rewritten only after a barrier has passed.
+// Sums of NS values over the TPR lanes of a row.  sh: per row of the workgroup two
+// copies of NS x waves floats used in turn, so a copy is rewritten only after a
+// barrier has passed.
 template <int TPR, int NS>
 __device__ __forceinline__ void row_sums(float (&x)[NS], float* sh, int& turn) {
 #pragma unroll
@@ -125,9 +126,9 @@ __device__ __forceinline__ void row_sums(float (&x)[NS], float* sh, int& turn) {
     for (int k = 0; k < NS; ++k) x[k] += __shfl_xor(x[k], o);
   if (TPR > 64) {
     constexpr int W = TPR / 64;
-    float* s = sh + (turn & 1) * 2 * W;
+    float* s = sh + (threadIdx.x / TPR) * 4 * W + (turn & 1) * 2 * W;
     ++turn;
-    const int w = threadIdx.x >> 6;
+    const int w = (threadIdx.x % TPR) >> 6;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
       for (int k = 0; k < NS; ++k) s[k * W + w] = x[k];
@@ -144,10 +145,16 @@ __device__ __forceinline__ void row_sums(float (&x)[NS], float* sh, int& turn) {
 
 __device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.0f + exp2_fast(-z * kLog2e)); }
 
-template <int TPR, int NCH>
+// XD, RD: the dtypes of x, z and out, and of the residual, where every row takes
+// 16-byte accesses; -1: types and accesses as a says (then a lane holds twice the
+// registers for its raw values and every pointer's alternatives)
+template <int TPR, int NCH, int XD, int RD>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
-  __shared__ float sh[4 * (TPR > 64 ? TPR / 64 : 1)];
+  __shared__ float sh[16];
   int turn = 0;
+  constexpr bool kKnown = XD >= 0;
+  const int vec = kKnown ? 8 : a.vec, xd = kKnown ? XD : a.x_dtype, rd = kKnown ? RD : a.res_dtype;
+  const int od = kKnown ? XD : a.out_dtype;
   constexpr int RPB = 256 / TPR;  // rows per workgroup
   const int l = threadIdx.x % TPR;
   const long row_raw = static_cast<long>(blockIdx.x) * RPB + threadIdx.x / TPR;
@@ -164,17 +171,17 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int i0 = (l + c * TPR) * kChunk;
-    rx[c] = raw8(a.x, xo, i0, a.n, a.x_dtype, a.vec);
-    if (a.z) rz[c] = raw8(a.z, zo, i0, a.n, a.x_dtype, a.vec);
-    if (a.res) rr[c] = raw8(a.res, dense, i0, a.n, a.res_dtype, a.vec);
+    rx[c] = raw8(a.x, xo, i0, a.n, xd, vec);
+    if (a.z) rz[c] = raw8(a.z, zo, i0, a.n, xd, vec);
+    if (a.res) rr[c] = raw8(a.res, dense, i0, a.n, rd, vec);
   }
   float y[NCH][8], g[NCH][8], t[NCH][8];
   float sum[1] = {0.0f};
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    widen(rx[c], a.x_dtype, y[c]);
-    if (a.z) widen(rz[c], a.x_dtype, g[c]);
-    if (a.res) widen(rr[c], a.res_dtype, t[c]);
+    widen(rx[c], xd, y[c]);
+    if (a.z) widen(rz[c], xd, g[c]);
+    if (a.res) widen(rr[c], rd, t[c]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (a.z) {
@@ -194,8 +201,8 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
   for (int c = 0; c < NCH; ++c) {
     const int i0 = (l + c * TPR) * kChunk;
     float w[8], sc[8];
-    if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, a.vec, w);
-    if (a.scale) get8(a.scale, 0, i0, a.n, kF32, a.vec, sc);
+    if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, vec, w);
+    if (a.scale) get8(a.scale, 0, i0, a.n, kF32, vec, sc);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float v = y[c][i];
@@ -206,7 +213,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
       t[c][i] = v;
       sum[0] = fmaf(v, v, sum[0]);
     }
-    if (act && a.res_out) put8(a.res_out, dense, i0, a.n, a.res_dtype, a.vec, t[c]);
+    if (act && a.res_out) put8(a.res_out, dense, i0, a.n, rd, vec, t[c]);
   }
   if (!a.out) return;
   if (a.out_w) {
@@ -219,20 +226,22 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
     const int i0 = (l + c * TPR) * kChunk;
     if (a.out_w) {
       float w[8];
-      get8(a.out_w, 0, i0, a.n, kF32, a.vec, w);
+      get8(a.out_w, 0, i0, a.n, kF32, vec, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) t[c][i] *= inv * w[i];
     }
-    put8(a.out, dense, i0, a.n, a.out_dtype, a.vec, t[c]);
+    put8(a.out, dense, i0, a.n, od, vec, t[c]);
   }
 }
 
-template <int TPR, int NCH>
+template <int TPR, int NCH, int XD, int RD>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a) {
-  constexpr int W = TPR > 64 ? TPR / 64 : 1;
   constexpr int TEAMS = 256 / TPR;
-  __shared__ float sh[4 * W];
+  __shared__ float sh[16];
   int turn = 0;
+  constexpr bool kKnown = XD >= 0;
+  const int vec = kKnown ? 8 : a.vec, xd = kKnown ? XD : a.x_dtype, rd = kKnown ? RD : a.res_dtype;
+  const int dod = kKnown ? XD : a.dout_dtype, drd = kKnown ? RD : a.dres_dtype, gd = kKnown ? XD : a.grad_dtype;
   const int l = threadIdx.x % TPR;
   const long team = static_cast<long>(blockIdx.x) * TEAMS + threadIdx.x / TPR;
   const long teams = static_cast<long>(gridDim.x) * TEAMS;  // a multiple of w_period
@@ -258,53 +267,60 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a) {
     const size_t zo = call_row * a.z_stride + static_cast<size_t>(grp) * a.n;
     const size_t dense = static_cast<size_t>(row) * a.n;
 
-    float x[NCH][8], z[NCH][8], t[NCH][8], d[NCH][8];
+    // (the loads of a row are all in flight before the first is widened)
+    Raw rx[NCH], rz[NCH], rr[NCH], ro[NCH], re[NCH];
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int i0 = (l + c * TPR) * kChunk;
-      get8(a.x, xo, i0, a.n, a.x_dtype, a.vec, x[c]);
-      if (a.z) get8(a.z, zo, i0, a.n, a.x_dtype, a.vec, z[c]);
-      if (a.res) {
-        get8(a.res, dense, i0, a.n, a.res_dtype, a.vec, t[c]);
-      } else {
+      rx[c] = raw8(a.x, xo, i0, a.n, xd, vec);
+      if (a.z) rz[c] = raw8(a.z, zo, i0, a.n, xd, vec);
+      if (a.res && a.out_w) rr[c] = raw8(a.res, dense, i0, a.n, rd, vec);
+      if (a.dout) ro[c] = raw8(a.dout, dense, i0, a.n, dod, vec);
+      if (a.dres) re[c] = raw8(a.dres, dense, i0, a.n, drd, vec);
+    }
+    float x[NCH][8], z[NCH][8], sg[NCH][8], d[NCH][8];  // sg: the gate's sigmoid
+    float sum[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[c][i] = 0.0f;
+    for (int c = 0; c < NCH; ++c) {
+      widen(rx[c], xd, x[c]);
+      if (a.z) widen(rz[c], xd, z[c]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sg[c][i] = a.z ? sigmoid(z[c][i]) : 1.0f;
+        if (!a.z) z[c][i] = 1.0f;
+        const float y = a.gate_first ? x[c][i] * (z[c][i] * sg[c][i]) : x[c][i];
+        sum[0] = fmaf(y, y, sum[0]);
       }
-      if (a.dout) get8(a.dout, dense, i0, a.n, a.dout_dtype, a.vec, d[c]);
     }
     float inv = 1.0f;
     if (a.norm_w) {
-      float sum[1] = {0.0f};
-#pragma unroll
-      for (int c = 0; c < NCH; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y = a.z && a.gate_first ? x[c][i] * (z[c][i] * sigmoid(z[c][i])) : x[c][i];
-          sum[0] = fmaf(y, y, sum[0]);
-        }
       row_sums<TPR, 1>(sum, sh, turn);
       inv = 1.0f / sqrtf(sum[0] * rn + a.eps);
     }
-    // the gated norm's value and, with an output norm, t and its two sums
-    float sum2[2] = {0.0f, 0.0f};
+    // with an output norm: t and its two sums, then the gradient of t
     if (a.out_w && a.dout) {
+      float sum2[2] = {0.0f, 0.0f};
+      float t[NCH][8];
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
         const int i0 = (l + c * TPR) * kChunk;
         float w[8], sc[8], ow[8];
-        if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, a.vec, w);
-        if (a.scale) get8(a.scale, 0, i0, a.n, kF32, a.vec, sc);
-        get8(a.out_w, 0, i0, a.n, kF32, a.vec, ow);
+        if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, vec, w);
+        if (a.scale) get8(a.scale, 0, i0, a.n, kF32, vec, sc);
+        get8(a.out_w, 0, i0, a.n, kF32, vec, ow);
+        if (a.res) widen(rr[c], rd, t[c]);
+        widen(ro[c], dod, d[c]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float v = x[c][i] * inv;
           if (a.norm_w) v *= w[i];
-          if (a.z) v *= z[c][i] * sigmoid(z[c][i]);
+          v *= z[c][i] * sg[c][i];
           if (a.scale) v *= sc[i];
-          const float tv = t[c][i] + v;
-          t[c][i] = tv;
-          sum2[0] = fmaf(tv, tv, sum2[0]);
-          sum2[1] = fmaf(d[c][i] * ow[i], tv, sum2[1]);
+          if (a.res) v += t[c][i];
+          t[c][i] = v;
+          d[c][i] *= ow[i];
+          sum2[0] = fmaf(v, v, sum2[0]);
+          sum2[1] = fmaf(d[c][i], v, sum2[1]);
         }
       }
       row_sums<TPR, 2>(sum2, sh, turn);
@@ -312,45 +328,45 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a) {
       const float k = sum2[1] * rn * oi * oi * oi;
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
-        const int i0 = (l + c * TPR) * kChunk;
-        float ow[8];
-        get8(a.out_w, 0, i0, a.n, kF32, a.vec, ow);
+        float dd[8];
+        widen(ro[c], dod, dd);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (act) ao[c][i] = fmaf(d[c][i] * t[c][i], oi, ao[c][i]);
-          d[c][i] *= ow[i] * oi;
+          if (act) ao[c][i] = fmaf(dd[i] * t[c][i], oi, ao[c][i]);
           // (with one value the difference cancels: what is left is the epsilon's part)
-          d[c][i] = a.n == 1 ? d[c][i] * (a.eps * oi * oi) : fmaf(-k, t[c][i], d[c][i]);
+          d[c][i] = a.n == 1 ? d[c][i] * oi * (a.eps * oi * oi) : fmaf(-k, t[c][i], d[c][i] * oi);
         }
       }
-    } else if (!a.dout) {
+    } else {
 #pragma unroll
-      for (int c = 0; c < NCH; ++c)
+      for (int c = 0; c < NCH; ++c) {
+        if (a.dout) widen(ro[c], dod, d[c]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) d[c][i] = 0.0f;
+        for (int i = 0; i < 8; ++i)
+          if (!a.dout) d[c][i] = 0.0f;
+      }
     }
-    float sum[1] = {0.0f};
+    sum[0] = 0.0f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int i0 = (l + c * TPR) * kChunk;
       if (a.dres) {
         float e[8];
-        get8(a.dres, dense, i0, a.n, a.dres_dtype, a.vec, e);
+        widen(re[c], drd, e);
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[c][i] += e[i];
       }
-      if (act && a.dresidual) put8(a.dresidual, dense, i0, a.n, a.res_dtype, a.vec, d[c]);
+      if (act && a.dresidual) put8(a.dresidual, dense, i0, a.n, rd, vec, d[c]);
       float w[8], sc[8];
-      if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, a.vec, w);
-      if (a.scale) get8(a.scale, 0, i0, a.n, kF32, a.vec, sc);
+      if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, vec, w);
+      if (a.scale) get8(a.scale, 0, i0, a.n, kF32, vec, sc);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float sg = a.z ? sigmoid(z[c][i]) : 1.0f, gate = a.z ? z[c][i] * sg : 1.0f;
+        const float gate = z[c][i] * sg[c][i];
         const float n = a.gate_first ? x[c][i] * gate * inv : x[c][i] * inv;  // normalised, before its weight
         const float wn = a.norm_w ? w[i] : 1.0f;
-        const float gated = a.gate_first ? n * wn : n * wn * gate;
         if (a.scale) {
-          if (act) as[c][i] = fmaf(d[c][i], gated, as[c][i]);
+          if (act) as[c][i] = fmaf(d[c][i], a.gate_first ? n * wn : n * wn * gate, as[c][i]);
           d[c][i] *= sc[i];
         }
         const float da = a.gate_first ? d[c][i] : d[c][i] * gate;
@@ -366,32 +382,31 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int i0 = (l + c * TPR) * kChunk;
-      float w[8];
-      if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, a.vec, w);
+      float w[8], dz[8];
+      if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, vec, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float sg = a.z ? sigmoid(z[c][i]) : 1.0f, gate = a.z ? z[c][i] * sg : 1.0f;
+        const float gate = z[c][i] * sg[c][i];
         const float n = a.gate_first ? x[c][i] * gate * inv : x[c][i] * inv;
         const float wn = a.norm_w ? w[i] : 1.0f;
         const float da = a.gate_first ? d[c][i] : d[c][i] * gate;
         // (one value: as above)
         const float dy = a.norm_w && a.n == 1 ? inv * inv * inv * a.eps * (da * wn) : inv * (da * wn - n * k);
-        if (a.z) {
-          const float dgate = a.gate_first ? dy * x[c][i] : d[c][i] * (n * wn);
-          t[c][i] = dgate * sg * (1.0f + z[c][i] * (1.0f - sg));
-        }
-        x[c][i] = a.gate_first && a.z ? dy * gate : dy;
+        const float dgate = a.gate_first ? dy * x[c][i] : d[c][i] * (n * wn);
+        dz[i] = dgate * sg[c][i] * (1.0f + z[c][i] * (1.0f - sg[c][i]));
+        x[c][i] = a.gate_first ? dy * gate : dy;
       }
-      if (act && a.dx) put8(a.dx, dense, i0, a.n, a.grad_dtype, a.vec, x[c]);
-      if (act && a.dz) put8(a.dz, dense, i0, a.n, a.grad_dtype, a.vec, t[c]);
+      if (act && a.dx) put8(a.dx, dense, i0, a.n, gd, vec, x[c]);
+      if (act && a.dz) put8(a.dz, dense, i0, a.n, gd, vec, dz);
     }
   }
 
   // partial rows: one per workgroup where its teams share a weight row, else one per team
   const size_t cols = a.n;
   if (a.w_period == 1 && TEAMS > 1) {
-    constexpr int kRow = TPR * NCH * 8;
-    __shared__ float acc[4][kRow];
+    constexpr int kRow = TPR * NCH * 8, SLOTS = TPR <= 64 ? 4 : TEAMS;
+    __shared__ float acc[SLOTS][kRow];
+    const int slot = TPR <= 64 ? threadIdx.x >> 6 : threadIdx.x / TPR;
     for (int which = 0; which < 3; ++which) {
       float (*v)[8] = which == 0 ? aw : which == 1 ? as : ao;
       const bool need = which == 0 ? a.dnorm_w != nullptr : which == 1 ? a.dscale != nullptr : a.dout_w != nullptr;
@@ -403,11 +418,15 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs a) {
           float s = v[c][i];
 #pragma unroll
           for (int o = TPR; o < 64; o <<= 1) s += __shfl_xor(s, o);
-          if ((threadIdx.x & 63) < TPR) acc[threadIdx.x >> 6][(l + c * TPR) * 8 + i] = s;
+          if ((threadIdx.x & 63) < TPR) acc[slot][(l + c * TPR) * 8 + i] = s;
         }
       __syncthreads();
-      for (int i = threadIdx.x; i < a.n; i += 256)
-        a.part[(static_cast<size_t>(blockIdx.x) * 3 + which) * cols + i] = acc[0][i] + acc[1][i] + acc[2][i] + acc[3][i];
+      for (int i = threadIdx.x; i < a.n; i += 256) {
+        float s = acc[0][i];
+#pragma unroll
+        for (int x = 1; x < SLOTS; ++x) s += acc[x][i];
+        a.part[(static_cast<size_t>(blockIdx.x) * 3 + which) * cols + i] = s;
+      }
       __syncthreads();
     }
   } else {
@@ -448,11 +467,26 @@ __global__ __launch_bounds__(256) void norm_reduce_kernel(NormArgs a) {
   }
 }
 
+// The type combinations that have kernels of their own (same: the other tensors
+// have the types of x and the residual), or -1
+int known_types(const NormArgs& a, bool same) {
+  if (a.vec != 8 || !same) return -1;
+  const int rd = a.res || a.dres ? a.res_dtype : a.x_dtype;
+  if (a.x_dtype == kBF16) return rd == kBF16 ? 2 : 1;
+  return rd == kF32 ? 0 : -1;
+}
+
 template <int TPR, int NCH>
 hipError_t fwd(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = 256 / TPR;
   return timed_launch(s, [&] {
-    hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH>), dim3(static_cast<unsigned>((a.rows + RPB - 1) / RPB)), dim3(256), 0, s, a);
+    const dim3 grid(static_cast<unsigned>((a.rows + RPB - 1) / RPB));
+    switch (known_types(a, !a.out || a.out_dtype == a.x_dtype)) {
+      case 0: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kF32, kF32>), grid, dim3(256), 0, s, a); break;
+      case 1: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kBF16, kF32>), grid, dim3(256), 0, s, a); break;
+      case 2: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kBF16, kBF16>), grid, dim3(256), 0, s, a); break;
+      default: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, -1, -1>), grid, dim3(256), 0, s, a);
+    }
   });
 }
 
@@ -468,7 +502,9 @@ struct BwdShape {
 BwdShape bwd_shape(long rows, int n, int period) {
   BwdShape b;
   const int chunks = (n + kChunk - 1) / kChunk;
-  b.tpr = chunks <= 16 ? 16 : chunks <= 32 ? 32 : chunks <= 64 ? 64 : 256;
+  // few registers per lane (three column sums and the row's values are held): two
+  // accesses of a lane to a row where 256 lanes allow it
+  b.tpr = chunks <= 16 ? 16 : chunks <= 32 ? 32 : chunks <= 64 ? 64 : chunks <= 128 ? 128 : 256;
   b.nch = b.tpr < 256 ? 1 : (chunks + 255) / 256;
   b.nch = b.nch <= 2 ? b.nch : b.nch <= 4 ? 4 : 8;
   const long teams = 256 / b.tpr;
@@ -482,7 +518,15 @@ BwdShape bwd_shape(long rows, int n, int period) {
 template <int TPR, int NCH>
 hipError_t bwd(const NormArgs& a, long blocks, hipStream_t s) {
   return timed_launch(s, [&] {
-    hipLaunchKernelGGL((norm_bwd_kernel<TPR, NCH>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    const bool same = (!a.dout || a.dout_dtype == a.x_dtype) && (!a.dres || a.dres_dtype == a.res_dtype) &&
+                      a.grad_dtype == a.x_dtype;
+    switch (known_types(a, same)) {
+      case 0: hipLaunchKernelGGL((norm_bwd_kernel<TPR, NCH, kF32, kF32>), grid, dim3(256), 0, s, a); break;
+      case 1: hipLaunchKernelGGL((norm_bwd_kernel<TPR, NCH, kBF16, kF32>), grid, dim3(256), 0, s, a); break;
+      case 2: hipLaunchKernelGGL((norm_bwd_kernel<TPR, NCH, kBF16, kBF16>), grid, dim3(256), 0, s, a); break;
+      default: hipLaunchKernelGGL((norm_bwd_kernel<TPR, NCH, -1, -1>), grid, dim3(256), 0, s, a);
+    }
   });
 }
 
@@ -523,6 +567,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
   if (b.tpr == 16) e = bwd<16, 1>(a, b.blocks, s);
   else if (b.tpr == 32) e = bwd<32, 1>(a, b.blocks, s);
   else if (b.tpr == 64) e = bwd<64, 1>(a, b.blocks, s);
+  else if (b.tpr == 128) e = bwd<128, 1>(a, b.blocks, s);
   else if (b.nch == 1) e = bwd<256, 1>(a, b.blocks, s);
   else if (b.nch == 2) e = bwd<256, 2>(a, b.blocks, s);
   else if (b.nch == 4) e = bwd<256, 4>(a, b.blocks, s);

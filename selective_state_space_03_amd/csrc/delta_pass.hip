@@ -104,6 +104,28 @@ __device__ __forceinline__ void put_state(unsigned char* dst, int ct, int lane, 
     *reinterpret_cast<uint2*>(dst + (((ct >> 1) * NP + p) * 64 + lane) * 16 + (ct & 1) * 8) = make_uint2(a[p], b[p]);
 }
 
+// The two tiles of a slab at once
+template <int NP>
+__device__ __forceinline__ void put_slab(unsigned char* dst, int slab, int lane, f32x4 v, f32x4 x) {
+  uint32_t a[NP], b[NP], c[NP], d[NP];
+  split2<NP>(v[0], v[1], a);
+  split2<NP>(v[2], v[3], b);
+  split2<NP>(x[0], x[1], c);
+  split2<NP>(x[2], x[3], d);
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+    *reinterpret_cast<uint4*>(dst + ((slab * NP + p) * 64 + lane) * 16) = make_uint4(a[p], b[p], c[p], d[p]);
+}
+// A wave's CT state tiles
+template <int NP, int ND, int CT, int NV>
+__device__ __forceinline__ void put_states(unsigned char* dst, int w, int lane, int e, const f32x4 (&S)[CT][NV]) {
+  if (CT == 2) {
+    put_slab<NP>(dst, w, lane, S[0][e], S[CT - 1][e]);
+  } else {
+    put_state<NP, ND>(dst, w, lane, S[0][e]);
+  }
+}
+
 template <typename IN, int KP, int NV, bool SAVE>
 __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices, int o_bf16, int vec_o) {
   using Parts = DeltaParts<IN>;
@@ -135,18 +157,19 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
       const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
       S[i][e] = a.state_in ? load_state4(a.state_in, group * a.V + v, d, a.K, v < a.V, a.vec_state)
                            : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, S[i][e]);
     }
+#pragma unroll
+  for (int e = 0; e < NV; ++e) put_states<NS, ND, CT, NV>(Ssh + e * kState, w, lane, e, S);
 
   // operands of the chunk at hand; each is asked for again, for the next chunk, right
   // after its last use, so a chunk's loads have the rest of the chunk before to arrive
   Frag<NI> fk[ND], fq[SAVE ? 1 : ND], fkt[CT][2];
   Frag<NS> ft[2];
   Frag<NO> fp[2];
-  // (waves 0 and 1 have no second step of the triangles: theirs stays zero, which costs
-  // nothing beside waves 2 and 3 and keeps the products free of branches: between a matrix
-  // instruction and the first use of its result the compiler's wait states are counted
-  // along one path only)
+  // Waves 0 and 1 have no second step of the triangles: theirs stays zero, which costs
+  // nothing beside waves 2 and 3 (skipping it measured the same) and keeps the products
+  // free of branches: between a matrix instruction and the first use of its result the
+  // compiler's wait states are counted along one path only.
   zero_frag(ft[1]);
   zero_frag(fp[1]);
   f32x4 beta, cr, cu;
@@ -280,8 +303,8 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
         s = mma(fkt[i][0], u0, s);
         s = mma(fkt[i][1], u1, s);
         S[i][e] = s;
-        put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, s);
       }
+      put_states<NS, ND, CT, NV>(Ssh + e * kState, w, lane, e, S);
       if (!SAVE) {
         f32x4 o = ot[e];
 #pragma unroll
@@ -343,13 +366,14 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
       const int v = v0 + 16 * e + r, d = 16 * (w * CT + i) + 4 * q;
       D[i][e] = a.dstate_out ? load_state4(a.dstate_out, group * a.V + v, d, a.K, v < a.V, a.vec_state)
                              : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, D[i][e]);
     }
+#pragma unroll
+  for (int e = 0; e < NV; ++e) put_states<NS, ND, CT, NV>(Ssh + e * kState, w, lane, e, D);
 
   // operands, asked for again right after their last use (as in the forward walk)
   Frag<NI> fk[ND], fkt[CT][2], fqt[CT][2];
   Frag<NS> ft[2], fp[2];
-  zero_frag(ft[0]);  // (waves 2 and 3 have no first step; without branches, as above)
+  zero_frag(ft[0]);  // (waves 2 and 3 have no first step; as above)
   zero_frag(fp[0]);
   f32x4 cr, cu, co;
   IN dv[NV][4];
@@ -480,8 +504,8 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[x] += s1[x];
         D[i][e] = s;
-        put_state<NS, ND>(Ssh + e * kState, w * CT + i, lane, s);
       }
+      put_states<NS, ND, CT, NV>(Ssh + e * kState, w, lane, e, D);
     }
     load_update(next);
     lds_barrier();  // do's tiles may be written again
