@@ -1,238 +1,16 @@
-// The norms before and after a block with its gate and residual scale, forward
-// and backward, in one pass over each row.
+// Backward of the block norm (formulas in block_norm_fwd.hip) from its inputs: a and
+// t are recomputed, so the forward saves nothing.  Three sums per row, each needing
+// the one before: sum y^2; sum t^2 with sum dout out_w t; sum dn n (dn the gradient
+// of the normalised y, n that value).
 //
-//   y = x (SiLU(z) first, with gate_first);  a = norm(y) norm_w;  (a SiLU(z), without)
-//   t = residual + scale a;   out = norm(t) out_w;   norm(r) = r / sqrt(mean(r^2) + eps)
-// every part optional; a grouped norm is the same with each group a row.
-//
-// Bound by memory: each row is read once into registers (kChunk = 8 values per
-// lane and access), its sums taken across the TPR lanes that share it, and the
-// results written once; t is normalised from its 32-bit value, not from the
-// residual as stored.  The backward pass recomputes a and t from the inputs (it
-// needs no saved statistics) and takes the three sums of its formulas (sum y^2;
-// sum t^2 with sum dout out_w t; sum dn n) in that order.  Its weight gradients
-// are column sums: every workgroup keeps running sums in registers over the rows
-// it walks and writes one partial row, and a second kernel adds the partials in
-// a fixed order (no atomics, the same result every time).
-#include "delta.h"
-#include "ssm_device.h"
+// Bound by memory: a row's tensors are read once, the next row's while this one is
+// computed.  The weights' gradients are column sums: every workgroup keeps running
+// sums in registers over the rows it walks and writes one partial row, and a second
+// kernel adds the partials in a fixed order (no atomics, the same result every time).
+#include "block_norm_device.h"
 
 namespace ssm {
 namespace {
-
-constexpr int kChunk = 8;
-
-// 8 values from element i0 of a row of n, as loaded (vec: elements per aligned
-// access).  Types and alignment are uniform branches; widening is kept apart from
-// loading, so that a row's loads are all in flight before the first is waited for.
-struct Raw {
-  uint4 a, b;
-};
-__device__ __forceinline__ Raw raw8(const void* base, size_t row, int i0, int n, int dtype, int vec) {
-  Raw r;
-  r.a = r.b = make_uint4(0u, 0u, 0u, 0u);
-  if (dtype == kBF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + row + i0;
-    if (vec == 8) {
-      if (i0 < n) r.a = *reinterpret_cast<const uint4*>(p);
-    } else if (vec == 4) {
-      uint2 x = make_uint2(0u, 0u), y = x;
-      if (i0 < n) x = *reinterpret_cast<const uint2*>(p);
-      if (i0 + 4 < n) y = *reinterpret_cast<const uint2*>(p + 4);
-      r.a = make_uint4(x.x, x.y, y.x, y.y);
-    } else {
-      uint32_t v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = 0u;
-        if (i0 + i < n) v[i] = p[i];
-      }
-      r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-    }
-  } else {
-    const float* p = static_cast<const float*>(base) + row + i0;
-    if (vec >= 4) {
-      if (i0 < n) r.a = *reinterpret_cast<const uint4*>(p);
-      if (i0 + 4 < n) r.b = *reinterpret_cast<const uint4*>(p + 4);
-    } else {
-      uint32_t v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = 0u;
-        if (i0 + i < n) v[i] = __float_as_uint(p[i]);
-      }
-      r.a = make_uint4(v[0], v[1], v[2], v[3]);
-      r.b = make_uint4(v[4], v[5], v[6], v[7]);
-    }
-  }
-  return r;
-}
-__device__ __forceinline__ void widen(const Raw& r, int dtype, float (&v)[8]) {
-  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w}, x[4] = {r.b.x, r.b.y, r.b.z, r.b.w};
-  const bool bf = dtype == kBF16;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = __uint_as_float(bf ? (i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16) : w[i]);
-    v[4 + i] = __uint_as_float(bf ? (i & 1 ? w[2 + (i >> 1)] & 0xffff0000u : w[2 + (i >> 1)] << 16) : x[i]);
-  }
-}
-__device__ __forceinline__ void get8(const void* base, size_t row, int i0, int n, int dtype, int vec, float (&v)[8]) {
-  widen(raw8(base, row, i0, n, dtype, vec), dtype, v);
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 v = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
-  return __builtin_bit_cast(uint32_t, v);
-}
-
-__device__ __forceinline__ void put8(void* base, size_t row, int i0, int n, int dtype, int vec, const float (&v)[8]) {
-  if (dtype == kBF16) {
-    uint16_t* p = static_cast<uint16_t*>(base) + row + i0;
-    const uint32_t w[4] = {pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
-    if (vec == 8) {
-      if (i0 < n) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if (vec == 4) {
-      if (i0 < n) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-      if (i0 + 4 < n) *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i0 + i < n) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-    }
-  } else {
-    float* p = static_cast<float*>(base) + row + i0;
-    if (vec >= 4) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (i0 + 4 * h < n)
-          *reinterpret_cast<float4*>(p + 4 * h) = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i0 + i < n) p[i] = v[i];
-    }
-  }
-}
-
-// Sums of NS values over the TPR lanes of a row.  sh: per row of the workgroup two
-// copies of NS x waves floats used in turn, so a copy is rewritten only after a
-// barrier has passed.
-template <int TPR, int NS>
-__device__ __forceinline__ void row_sums(float (&x)[NS], float* sh, int& turn) {
-#pragma unroll
-  for (int o = 1; o < (TPR < 64 ? TPR : 64); o <<= 1)
-#pragma unroll
-    for (int k = 0; k < NS; ++k) x[k] += __shfl_xor(x[k], o);
-  if (TPR > 64) {
-    constexpr int W = TPR / 64;
-    float* s = sh + (threadIdx.x / TPR) * 4 * W + (turn & 1) * 2 * W;
-    ++turn;
-    const int w = (threadIdx.x % TPR) >> 6;
-    if ((threadIdx.x & 63) == 0)
-#pragma unroll
-      for (int k = 0; k < NS; ++k) s[k * W + w] = x[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < NS; ++k) {
-      float t = s[k * W];
-#pragma unroll
-      for (int i = 1; i < W; ++i) t += s[k * W + i];
-      x[k] = t;
-    }
-  }
-}
-
-__device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.0f + exp2_fast(-z * kLog2e)); }
-
-// XD, RD: the dtypes of x, z and out, and of the residual, where every row takes
-// 16-byte accesses; -1: types and accesses as a says (then a lane holds twice the
-// registers for its raw values and every pointer's alternatives)
-template <int TPR, int NCH, int XD, int RD>
-__global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
-  __shared__ float sh[16];
-  int turn = 0;
-  constexpr bool kKnown = XD >= 0;
-  const int vec = kKnown ? 8 : a.vec, xd = kKnown ? XD : a.x_dtype, rd = kKnown ? RD : a.res_dtype;
-  const int od = kKnown ? XD : a.out_dtype;
-  constexpr int RPB = 256 / TPR;  // rows per workgroup
-  const int l = threadIdx.x % TPR;
-  const long row_raw = static_cast<long>(blockIdx.x) * RPB + threadIdx.x / TPR;
-  const bool act = row_raw < a.rows;  // (whole teams; with TPR 256 every row is there)
-  const long row = act ? row_raw : a.rows - 1;
-  const long call_row = row / a.groups;
-  const int grp = static_cast<int>(row - call_row * a.groups);
-  const size_t xo = call_row * a.x_stride + static_cast<size_t>(grp) * a.n;
-  const size_t zo = call_row * a.z_stride + static_cast<size_t>(grp) * a.n;
-  const size_t dense = static_cast<size_t>(row) * a.n;
-  const size_t wo = static_cast<size_t>(row % a.w_period) * a.n;
-
-  Raw rx[NCH], rz[NCH], rr[NCH];
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int i0 = (l + c * TPR) * kChunk;
-    rx[c] = raw8(a.x, xo, i0, a.n, xd, vec);
-    if (a.z) rz[c] = raw8(a.z, zo, i0, a.n, xd, vec);
-    if (a.res) rr[c] = raw8(a.res, dense, i0, a.n, rd, vec);
-  }
-  float y[NCH][8], g[NCH][8], t[NCH][8];
-  float sum[1] = {0.0f};
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    widen(rx[c], xd, y[c]);
-    if (a.z) widen(rz[c], xd, g[c]);
-    if (a.res) widen(rr[c], rd, t[c]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (a.z) {
-        g[c][i] *= sigmoid(g[c][i]);
-        if (a.gate_first) y[c][i] *= g[c][i];
-      }
-      sum[0] = fmaf(y[c][i], y[c][i], sum[0]);
-    }
-  }
-  float inv = 1.0f;
-  if (a.norm_w) {
-    row_sums<TPR, 1>(sum, sh, turn);
-    inv = 1.0f / sqrtf(sum[0] / static_cast<float>(a.n) + a.eps);
-  }
-  sum[0] = 0.0f;
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int i0 = (l + c * TPR) * kChunk;
-    float w[8], sc[8];
-    if (a.norm_w) get8(a.norm_w, wo, i0, a.n, kF32, vec, w);
-    if (a.scale) get8(a.scale, 0, i0, a.n, kF32, vec, sc);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = y[c][i];
-      if (a.norm_w) v *= inv * w[i];
-      if (a.z && !a.gate_first) v *= g[c][i];
-      if (a.scale) v *= sc[i];
-      if (a.res) v += t[c][i];
-      t[c][i] = v;
-      sum[0] = fmaf(v, v, sum[0]);
-    }
-    if (act && a.res_out) put8(a.res_out, dense, i0, a.n, rd, vec, t[c]);
-  }
-  if (!a.out) return;
-  if (a.out_w) {
-    row_sums<TPR, 1>(sum, sh, turn);
-    inv = 1.0f / sqrtf(sum[0] / static_cast<float>(a.n) + a.eps);
-  }
-  if (!act) return;
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int i0 = (l + c * TPR) * kChunk;
-    if (a.out_w) {
-      float w[8];
-      get8(a.out_w, 0, i0, a.n, kF32, vec, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[c][i] *= inv * w[i];
-    }
-    put8(a.out, dense, i0, a.n, od, vec, t[c]);
-  }
-}
 
 // GF: gate_first.  Parts that are missing cost no branch per element: an absent weight
 // is held as ones, an absent gate as z sigmoid = 1.
@@ -570,29 +348,6 @@ __global__ __launch_bounds__(256) void norm_reduce_kernel(NormArgs a) {
   }
 }
 
-// The type combinations that have kernels of their own (same: the other tensors
-// have the types of x and the residual), or -1
-int known_types(const NormArgs& a, bool same) {
-  if (a.vec != 8 || !same) return -1;
-  const int rd = a.res || a.dres ? a.res_dtype : a.x_dtype;
-  if (a.x_dtype == kBF16) return rd == kBF16 ? 2 : 1;
-  return rd == kF32 ? 0 : -1;
-}
-
-template <int TPR, int NCH>
-hipError_t fwd(const NormArgs& a, hipStream_t s) {
-  constexpr int RPB = 256 / TPR;
-  return timed_launch(s, [&] {
-    const dim3 grid(static_cast<unsigned>((a.rows + RPB - 1) / RPB));
-    switch (known_types(a, !a.out || a.out_dtype == a.x_dtype)) {
-      case 0: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kF32, kF32>), grid, dim3(256), 0, s, a); break;
-      case 1: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kBF16, kF32>), grid, dim3(256), 0, s, a); break;
-      case 2: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kBF16, kBF16>), grid, dim3(256), 0, s, a); break;
-      default: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, -1, -1>), grid, dim3(256), 0, s, a);
-    }
-  });
-}
-
 long gcd(long a, long b) { return b == 0 ? a : gcd(b, a % b); }
 
 struct BwdShape {
@@ -628,10 +383,11 @@ hipError_t bwd(const NormArgs& a, long blocks, hipStream_t s) {
     };
     const bool same = (!a.dout || a.dout_dtype == a.x_dtype) && (!a.dres || a.dres_dtype == a.res_dtype) &&
                       a.grad_dtype == a.x_dtype;
-    switch (known_types(a, same)) {
-      case 0: run(norm_bwd_kernel<TPR, NCH, kF32, kF32, false>, norm_bwd_kernel<TPR, NCH, kF32, kF32, true>); break;
-      case 1: run(norm_bwd_kernel<TPR, NCH, kBF16, kF32, false>, norm_bwd_kernel<TPR, NCH, kBF16, kF32, true>); break;
-      case 2: run(norm_bwd_kernel<TPR, NCH, kBF16, kBF16, false>, norm_bwd_kernel<TPR, NCH, kBF16, kBF16, true>); break;
+    // (rows of more than two accesses per lane spill in every variant: one serves all types)
+    switch (NCH <= 2 ? known_types(a, same) : -1) {
+      case 0: run(norm_bwd_kernel<TPR, (NCH <= 2 ? NCH : 1), kF32, kF32, false>, norm_bwd_kernel<TPR, (NCH <= 2 ? NCH : 1), kF32, kF32, true>); break;
+      case 1: run(norm_bwd_kernel<TPR, (NCH <= 2 ? NCH : 1), kBF16, kF32, false>, norm_bwd_kernel<TPR, (NCH <= 2 ? NCH : 1), kBF16, kF32, true>); break;
+      case 2: run(norm_bwd_kernel<TPR, (NCH <= 2 ? NCH : 1), kBF16, kBF16, false>, norm_bwd_kernel<TPR, (NCH <= 2 ? NCH : 1), kBF16, kBF16, true>); break;
       default: run(norm_bwd_kernel<TPR, NCH, -1, -1, false>, norm_bwd_kernel<TPR, NCH, -1, -1, true>);
     }
   });
@@ -642,29 +398,6 @@ hipError_t bwd(const NormArgs& a, long blocks, hipStream_t s) {
 int norm_bwd_parts(long rows, int n, int period) {
   const BwdShape b = bwd_shape(rows, n, period);
   return static_cast<int>(period == 1 ? b.blocks : b.blocks * (256 / b.tpr));
-}
-
-hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
-  if (a.rows == 0) return hipSuccess;
-  const int chunks = (a.n + kChunk - 1) / kChunk;
-  if (chunks <= 16) return fwd<16, 1>(a, s);
-  if (chunks <= 32) return fwd<32, 1>(a, s);
-  // a wave per row needs no barrier; with few rows four waves share one
-  if (a.rows >= 1024 && chunks <= 512) {
-    switch ((chunks + 63) / 64) {
-      case 1: return fwd<64, 1>(a, s);
-      case 2: return fwd<64, 2>(a, s);
-      case 3: return fwd<64, 3>(a, s);
-      case 4: return fwd<64, 4>(a, s);
-      case 5: return fwd<64, 5>(a, s);
-      case 6: return fwd<64, 6>(a, s);
-      default: return fwd<64, 8>(a, s);
-    }
-  }
-  if (chunks <= 256) return fwd<256, 1>(a, s);
-  if (chunks <= 512) return fwd<256, 2>(a, s);
-  if (chunks <= 1024) return fwd<256, 4>(a, s);
-  return fwd<256, 8>(a, s);
 }
 
 // (without rows the kernels still run: the weight gradients are then zeros)

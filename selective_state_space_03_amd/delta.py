@@ -23,6 +23,25 @@ from .binding import (
 )
 
 _F32 = torch.float32
+_byref = ctypes.byref
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(device, stream):
+    """The stream's handle, without building a Stream object for the current one."""
+    if stream is None and _raw_stream is not None and device.index is not None:
+        return ctypes.c_void_p(_raw_stream(device.index))
+    return _stream(device, stream)
+
+
+def _arg(t, name, shape, dtype, device):
+    """_ptr, with its checks in the fewest calls for a tensor that passes them (a decode step's
+    launch is bound by the host)."""
+    if t is None:
+        return None
+    if type(t) is torch.Tensor and t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.device == device:
+        return t.data_ptr() or None
+    return _ptr(t, name, shape, dtype, device)
 
 
 def _dtype(d, name):
@@ -35,7 +54,7 @@ def _rows(t, name, shape, dtype, device):
     """Pointer and row stride of a tensor whose rows (its last two dimensions) are dense and whose
     leading dimensions step evenly from row to row, as a slice of a wider projection does."""
     if t.is_contiguous():
-        return _ptr(t, name, shape, dtype, device), 0
+        return _arg(t, name, shape, dtype, device), 0
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError(f"{name} must be a GPU tensor")
     if t.device != device:
@@ -85,8 +104,8 @@ def _delta_inputs(p, q, k, v, g, beta, scale, qk_norm, eps, cu_seqlens, state_in
     p.x_dtype = _code(q, "q")
     p.k, p.k_stride = _rows(k, "k", (batch, seqlen, hk, dk), q.dtype, dev)
     p.v, p.v_stride = _rows(v, "v", (batch, seqlen, h, dv), q.dtype, dev)
-    p.g = _ptr(g, "g", (batch, seqlen, h), _F32, dev)
-    p.beta = _ptr(beta, "beta", (batch, seqlen, h), _F32, dev)
+    p.g = _arg(g, "g", (batch, seqlen, h), _F32, dev)
+    p.beta = _arg(beta, "beta", (batch, seqlen, h), _F32, dev)
     p.scale = 1.0 / math.sqrt(dk) if scale is None else scale
     p.qk_norm = 1 if qk_norm else 0
     p.eps = eps
@@ -98,7 +117,7 @@ def _delta_inputs(p, q, k, v, g, beta, scale, qk_norm, eps, cu_seqlens, state_in
     else:
         p.num_seqs = batch
     shape = (p.num_seqs, h, dv, dk)
-    p.state_in = _ptr(state_in, "state_in", shape, _F32, dev)
+    p.state_in = _arg(state_in, "state_in", shape, _F32, dev)
     return shape
 
 
@@ -115,12 +134,12 @@ def delta_chunk_fwd(q, k, v, g, beta, *, scale=None, qk_norm=False, eps=1e-6, cu
     p = DeltaChunkParams()
     shape = _delta_inputs(p, q, k, v, g, beta, scale, qk_norm, eps, cu_seqlens, state_in)
     if o is None:
-        o = _empty(tuple(v.shape), o_dtype or q.dtype, dev, stream)
-    p.state_out = _ptr(state_out, "state_out", shape, _F32, dev)
-    p.o = _ptr(o, "o", tuple(v.shape), device=dev)
+        o = _empty(v.shape, o_dtype or q.dtype, dev, stream)
+    p.state_out = _arg(state_out, "state_out", shape, _F32, dev)
+    p.o = _arg(o, "o", v.shape, o.dtype, dev)
     p.o_dtype = _code(o, "o")
-    workspace = _workspace(p, L_.ssm_delta_chunk_workspace_size(ctypes.byref(p)), workspace, dev, stream)
-    call = Call(L_.ssm_delta_chunk_fwd, p, _stream(dev, stream), o, (q, k, v, g, beta, cu_seqlens, state_in, state_out,
+    workspace = _workspace(p, L_.ssm_delta_chunk_workspace_size(_byref(p)), workspace, dev, stream)
+    call = Call(L_.ssm_delta_chunk_fwd, p, _on(dev, stream), o, (q, k, v, g, beta, cu_seqlens, state_in, state_out,
                                                                     workspace))
     return call if prepare else call.run()
 
@@ -135,8 +154,8 @@ def delta_chunk_bwd(q, k, v, g, beta, dout, *, scale=None, qk_norm=False, eps=1e
     dev = q.device
     p = DeltaChunkBwdParams()
     shape = _delta_inputs(p, q, k, v, g, beta, scale, qk_norm, eps, cu_seqlens, state_in)
-    p.dout = _ptr(dout, "dout", tuple(v.shape), q.dtype, dev)
-    p.dstate_out = _ptr(dstate_out, "dstate_out", shape, _F32, dev)
+    p.dout = _arg(dout, "dout", v.shape, q.dtype, dev)
+    p.dstate_out = _arg(dstate_out, "dstate_out", shape, _F32, dev)
     gd = grad_dtype or _F32
     p.grad_dtype = _dtype(gd, "grad_dtype")
     # tokens outside every packed sequence are not written: they start as zeros
@@ -149,8 +168,8 @@ def delta_chunk_bwd(q, k, v, g, beta, dout, *, scale=None, qk_norm=False, eps=1e
     for name, field in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("beta", "dbeta"), ("state_in", "dstate_in")):
         if name in out and out[name].numel() > 0:
             setattr(p, field, out[name].data_ptr())
-    workspace = _workspace(p, L_.ssm_delta_chunk_bwd_workspace_size(ctypes.byref(p)), workspace, dev, stream)
-    call = Call(L_.ssm_delta_chunk_bwd, p, _stream(dev, stream), out, (q, k, v, g, beta, dout, cu_seqlens, state_in,
+    workspace = _workspace(p, L_.ssm_delta_chunk_bwd_workspace_size(_byref(p)), workspace, dev, stream)
+    call = Call(L_.ssm_delta_chunk_bwd, p, _on(dev, stream), out, (q, k, v, g, beta, dout, cu_seqlens, state_in,
                                                                       dstate_out, workspace))
     return call if prepare else call.run()
 
@@ -171,24 +190,24 @@ def delta_decode_step(q, k, v, g, beta, state, *, scale=None, qk_norm=False, eps
     p.x_dtype = _code(q, "q")
     p.k, p.k_stride = _rows(k, "k", (batch, hk, dk), q.dtype, dev)
     p.v, p.v_stride = _rows(v, "v", (batch, h, dv), q.dtype, dev)
-    p.g = _ptr(g, "g", (batch, h), _F32, dev)
-    p.beta = _ptr(beta, "beta", (batch, h), _F32, dev)
+    p.g = _arg(g, "g", (batch, h), _F32, dev)
+    p.beta = _arg(beta, "beta", (batch, h), _F32, dev)
     p.scale = 1.0 / math.sqrt(dk) if scale is None else scale
     p.qk_norm = 1 if qk_norm else 0
     p.eps = eps
-    p.state = _ptr(state, "state", (batch, h, dv, dk), _F32, dev)
+    p.state = _arg(state, "state", (batch, h, dv, dk), _F32, dev)
     if o is None:
         o = _empty((batch, h, dv), o_dtype or q.dtype, dev, stream)
-    p.o = _ptr(o, "o", (batch, h, dv), device=dev)
+    p.o = _arg(o, "o", (batch, h, dv), o.dtype, dev)
     p.o_dtype = _code(o, "o")
-    call = Call(L_.ssm_delta_decode_step, p, _stream(dev, stream), o, (q, k, v, g, beta, state))
+    call = Call(L_.ssm_delta_decode_step, p, _on(dev, stream), o, (q, k, v, g, beta, state))
     return call if prepare else call.run()
 
 
 def _norm_inputs(p, x, norm_w, z, gate_first, residual, scale, out_norm_w, group_size, eps):
     dev, width = x.device, x.shape[-1]
     shape = tuple(x.shape)
-    rows = math.prod(shape[:-1])
+    rows = shape[0] if len(shape) == 2 else math.prod(shape[:-1])
     p.struct_size = ctypes.sizeof(type(p))
     p.rows, p.width = rows, width
     if group_size is None:
@@ -198,7 +217,7 @@ def _norm_inputs(p, x, norm_w, z, gate_first, residual, scale, out_norm_w, group
 
     def lines(t, name):  # rows of the last dimension at an even stride
         if t is None or t.is_contiguous():
-            return _ptr(t, name, shape, x.dtype, dev), 0
+            return _arg(t, name, shape, x.dtype, dev), 0
         return _rows(t.unsqueeze(-2), name, shape[:-1] + (1, width), x.dtype, dev)
 
     p.x, p.x_stride = lines(x, "x")
@@ -206,12 +225,12 @@ def _norm_inputs(p, x, norm_w, z, gate_first, residual, scale, out_norm_w, group
     p.z, p.z_stride = lines(z, "z")
     p.gate_first = 1 if gate_first else 0
     if norm_w is not None:
-        p.norm_w = _ptr(norm_w, "norm_w", (norm_w.numel(),), _F32, dev)
+        p.norm_w = _arg(norm_w, "norm_w", (norm_w.numel(),), _F32, dev)
         p.norm_w_len = norm_w.numel()
-    p.residual = _ptr(residual, "residual", shape, None, dev)
+    p.residual = _arg(residual, "residual", shape, residual.dtype, dev) if residual is not None else None
     p.res_dtype = _code(residual, "residual") if residual is not None else 0
-    p.scale = _ptr(scale, "scale", (width,), _F32, dev)
-    p.out_norm_w = _ptr(out_norm_w, "out_norm_w", (width,), _F32, dev)
+    p.scale = _arg(scale, "scale", (width,), _F32, dev)
+    p.out_norm_w = _arg(out_norm_w, "out_norm_w", (width,), _F32, dev)
     p.eps = eps
     return shape
 
@@ -231,10 +250,12 @@ def block_norm_fwd(x, *, norm_w=None, z=None, gate_first=False, residual=None, s
         residual_out = _empty(shape, residual.dtype, dev, stream)
     if out is None and (residual is None or out_norm_w is not None):
         out = _empty(shape, out_dtype or x.dtype, dev, stream)
-    p.residual_out = _ptr(residual_out, "residual_out", shape, residual.dtype if residual is not None else None, dev)
-    p.out = _ptr(out, "out", shape, None, dev)
+    if residual_out is not None:
+        p.residual_out = _arg(residual_out, "residual_out", shape, (residual if residual is not None else residual_out).dtype, dev)
+    if out is not None:
+        p.out = _arg(out, "out", shape, out.dtype, dev)
     p.out_dtype = _code(out, "out") if out is not None else 0
-    call = Call(L_.ssm_block_norm_fwd, p, _stream(dev, stream), (out, residual_out),
+    call = Call(L_.ssm_block_norm_fwd, p, _on(dev, stream), (out, residual_out),
                 (x, norm_w, z, residual, scale, out_norm_w))
     return call if prepare else call.run()
 
@@ -249,10 +270,11 @@ def block_norm_bwd(x, *, norm_w=None, z=None, gate_first=False, residual=None, s
     dev = x.device
     p = BlockNormBwdParams()
     shape = _norm_inputs(p, x, norm_w, z, gate_first, residual, scale, out_norm_w, group_size, eps)
-    p.dout = _ptr(dout, "dout", shape, None, dev)
-    p.dout_dtype = _code(dout, "dout") if dout is not None else 0
-    p.dresidual_out = _ptr(dresidual, "dresidual", shape, None, dev)
-    p.dres_dtype = _code(dresidual, "dresidual") if dresidual is not None else 0
+    if dout is not None:
+        p.dout, p.dout_dtype = _arg(dout, "dout", shape, dout.dtype, dev), _code(dout, "dout")
+    if dresidual is not None:
+        p.dresidual_out = _arg(dresidual, "dresidual", shape, dresidual.dtype, dev)
+        p.dres_dtype = _code(dresidual, "dresidual")
     gd = grad_dtype or _F32
     p.grad_dtype = _dtype(gd, "grad_dtype")
     out = {"x": _empty(shape, gd, dev, stream)}
@@ -270,7 +292,7 @@ def block_norm_bwd(x, *, norm_w=None, z=None, gate_first=False, residual=None, s
                         ("out_norm_w", "dout_norm_w")):
         if name in out and out[name].numel() > 0:
             setattr(p, field, out[name].data_ptr())
-    workspace = _workspace(p, L_.ssm_block_norm_bwd_workspace_size(ctypes.byref(p)), workspace, dev, stream)
-    call = Call(L_.ssm_block_norm_bwd, p, _stream(dev, stream), out,
+    workspace = _workspace(p, L_.ssm_block_norm_bwd_workspace_size(_byref(p)), workspace, dev, stream)
+    call = Call(L_.ssm_block_norm_bwd, p, _on(dev, stream), out,
                 (x, norm_w, z, residual, scale, out_norm_w, dout, dresidual, workspace))
     return call if prepare else call.run()
