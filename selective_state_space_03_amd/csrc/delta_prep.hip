@@ -17,6 +17,7 @@ namespace ssm {
 namespace {
 
 constexpr int kLP = 68;  // floats per LDS row of a 64 x 64 matrix
+constexpr int kHeads = 8;  // value heads of a workgroup at most
 
 // 8 values of an LDS tile as an operand: `lo` and `hi` point at 4 consecutive ones each
 __device__ __forceinline__ Frag<1> frag44(const bf16s* lo, const bf16s* hi) {
@@ -81,8 +82,8 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
   constexpr int mat = kDeltaC * kLP * 4;
   __shared__ __align__(16) unsigned char qk_raw[2 * tile > mat ? 2 * tile : mat];
   __shared__ __align__(16) float Lm[kDeltaC * kLP];
-  __shared__ double Gs[kDeltaC];
-  __shared__ float bs[kDeltaC], rks[kDeltaC], rqs[kDeltaC];
+  __shared__ double Gs[kHeads][kDeltaC];
+  __shared__ float bs[kHeads][kDeltaC], rks[kDeltaC], rqs[kDeltaC];
   IN* const Ks = reinterpret_cast<IN*>(qk_raw);
   IN* const Qs = reinterpret_cast<IN*>(qk_raw + tile);
   // after the last use of Ks and Qs their room holds a head's P, then its T
@@ -101,10 +102,21 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
   if (n == 0) return;
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6), r = lane & 15, q = lane >> 4;
 
-  // the chunk's q and k rows, zeros past its end and past K; wave 0 also holds the
-  // next head's g and beta
+  // the heads' running sums of g, in 64 bits, a head per wave at a time
   const size_t grow = static_cast<size_t>(t0 + (lane < n ? lane : 0)) * a.h;
-  float gl = a.g[grow + h0], bl = a.beta[grow + h0];
+  for (int head = h0 + w; head < h1; head += 4) {
+    const float gl = a.g[grow + head], bl = a.beta[grow + head];
+    double g = lane < n ? static_cast<double>(gl) : 0.0;
+    g = g < -1e4 ? -1e4 : g;  // e^-10000 is 0 in 32 bits already; -inf would make differences NaN
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const double up = __shfl_up(g, o);
+      if (lane >= o) g += up;
+    }
+    Gs[head - h0][lane] = g;
+    bs[head - h0][lane] = lane < n ? bl : 0.0f;
+  }
+  // the chunk's q and k rows, zeros past its end and past K
   {
     constexpr int per = KP / 8, each = kDeltaC * per / 256;
     Row8<IN> rk[each], rq[each];
@@ -141,33 +153,36 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
   }
   __syncthreads();
 
-  // k k^T and q k^T, row tile w
-  f32x4 kk[4], qk[4];
+  // k k^T and q k^T on the ten 16 x 16 tiles of the lower triangle: three for waves 0
+  // and 1, two for waves 2 and 3 (whose third repeats their first, unused: no branch
+  // among the products)
+  const int nt = w < 2 ? 3 : 2;
+  const int ti[3] = {w, w < 3 ? w + 1 : 2, w < 2 ? 3 : w}, tj[3] = {w, w < 3 ? w : 0, w};
+  f32x4 kk[3], qk[3];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j = 0; j < 3; ++j) kk[j] = qk[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int c = 0; c < ND; ++c) {
     const int off = 32 * c + 8 * q;
-    const Frag<NI> fk = frag44(Ks + (16 * w + r) * pitch + off, Ks + (16 * w + r) * pitch + off + 4);
-    const Frag<NI> fq = frag44(Qs + (16 * w + r) * pitch + off, Qs + (16 * w + r) * pitch + off + 4);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {  // (the tiles above the diagonal too: no branch among the products)
-      const Frag<NI> b = frag44(Ks + (16 * j + r) * pitch + off, Ks + (16 * j + r) * pitch + off + 4);
-      kk[j] = mma(fk, b, kk[j]);
-      qk[j] = mma(fq, b, qk[j]);
+    for (int j = 0; j < 3; ++j) {
+      const IN* rk = Ks + (16 * ti[j] + r) * pitch + off;
+      const IN* rq = Qs + (16 * ti[j] + r) * pitch + off;
+      const IN* rb = Ks + (16 * tj[j] + r) * pitch + off;
+      const Frag<NI> b = frag44(rb, rb + 4);
+      kk[j] = mma(frag44(rk, rk + 4), b, kk[j]);
+      qk[j] = mma(frag44(rq, rq + 4), b, qk[j]);
     }
   }
   // norms and the readout scale go into the products, which every head shares
-  float rkt[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = 16 * w + 4 * q + i;
-    rkt[i] = rks[t];
-    const float rqt = a.scale * rqs[t];
+  for (int j = 0; j < 3; ++j) {
+    const float rs = rks[16 * tj[j] + r];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      kk[j][i] *= rkt[i] * rks[16 * j + r];
-      qk[j][i] *= rqt * rks[16 * j + r];
+    for (int i = 0; i < 4; ++i) {
+      const int t = 16 * ti[j] + 4 * q + i;
+      kk[j][i] *= rks[t] * rs;
+      qk[j][i] *= a.scale * rqs[t] * rs;
     }
   }
   // operands shared by the key head's value heads
@@ -193,23 +208,12 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
 #pragma unroll 1
   for (int head = h0; head < h1; ++head) {
     const size_t at = static_cast<size_t>(slot) * a.h + head;
-    float* const sc = a.sc + at * kDeltaSc;
-    if (w == 0) {  // the running sum of g, in 64 bits
-      double g = lane < n ? static_cast<double>(gl) : 0.0;
-      g = g < -1e4 ? -1e4 : g;  // e^-10000 is 0 in 32 bits already; -inf would make differences NaN
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double up = __shfl_up(g, o);
-        if (lane >= o) g += up;
-      }
-      const float b = lane < n ? bl : 0.0f;
-      Gs[lane] = g;
-      bs[lane] = b;
-      const int next = min(head + 1, h1 - 1);
-      gl = a.g[grow + next];
-      bl = a.beta[grow + next];
-      const double GC = __shfl(g, 63);
-      const float eg = exp_of(g), el = exp_of(GC - g), rk = rks[lane], rq = rqs[lane];
+    const double* const Gh = Gs[head - h0];
+    const float* const bh = bs[head - h0];
+    if (w == 3) {
+      float* const sc = a.sc + at * kDeltaSc;
+      const double g = Gh[lane], GC = Gh[kDeltaC - 1];
+      const float eg = exp_of(g), el = exp_of(GC - g), rk = rks[lane], rq = rqs[lane], b = bh[lane];
       sc[kScBeta * kDeltaC + lane] = b;
       sc[kScR * kDeltaC + lane] = b * eg * rk;
       sc[kScO * kDeltaC + lane] = a.scale * eg * rq;
@@ -221,21 +225,25 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
       reinterpret_cast<double*>(sc + kScG * kDeltaC)[lane] = g;
       if (lane == 0) sc[kScGamma * kDeltaC] = exp_of(GC);
     }
-    __syncthreads();  // G; the room of q and k (or of the head before) is free
+    __syncthreads();  // the room of q and k (or of the head before) is free
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 16 * w + 4 * q + i;
-      const double Gt = Gs[t];
-      const float bt = bs[t];
+    for (int j = 0; j < 3; ++j)
+      if (j < nt) {
+        const int s = 16 * tj[j] + r;
+        const double Gsv = Gh[s];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int s = 16 * j + r;
-        // 0 above the diagonal, where the decay may overflow
-        const float dec = exp_of(s <= t ? Gt - Gs[s] : -1e4);
-        Lm[t * kLP + s] = s < t ? bt * dec * kk[j][i] : 0.0f;
-        Pm[t * kLP + s] = s <= t ? dec * qk[j][i] : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          const int t = 16 * ti[j] + 4 * q + i;
+          // 0 above the diagonal, where the decay may overflow
+          const float dec = exp_of(s <= t ? Gh[t] - Gsv : -1e4);
+          Lm[t * kLP + s] = s < t ? bh[t] * dec * kk[j][i] : 0.0f;
+          Pm[t * kLP + s] = s <= t ? dec * qk[j][i] : 0.0f;
+        }
       }
-    }
+    // tiles above the diagonal that an operand's step spans: (0, 1) and (2, 3)
+    if (w >= 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) Pm[(32 * (w - 2) + 4 * q + i) * kLP + 32 * (w - 2) + 16 + r] = 0.0f;
     __syncthreads();
     if (!BWD) {
       unsigned char* pf = a.pf + at * (kDeltaTri * NO * kDeltaFrag);
@@ -323,11 +331,12 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
 }
 
 // Workgroups per (chunk, key head): the value heads share the rows and their
-// products, so a workgroup takes as many as leave the GPU's CUs eight each.
+// products, so a workgroup takes as many (up to kHeads) as leave the GPU's CUs eight
+// workgroups each.
 int head_parts(const DeltaArgs& a) {
   const long rep = a.h / a.hk, want = 8L * 256, have = a.slots * a.hk;
-  const long parts = (want + have - 1) / have;
-  return static_cast<int>(parts < rep ? parts : rep);
+  const long parts = (want + have - 1) / have, least = (rep + kHeads - 1) / kHeads;
+  return static_cast<int>(parts > rep ? rep : parts < least ? least : parts);
 }
 
 template <typename IN, int KP>
