@@ -19,7 +19,7 @@
 namespace ssm {
 namespace {
 
-constexpr int kPitch = 72;  // tokens per LDS row of an exchanged [channel][token] tile (144 bytes: no bank conflicts)
+constexpr int kTile = 16 * kDeltaC;  // 16-bit words of an exchanged tile's part in LDS
 
 // 4 consecutive outputs of a row, any dtype; vec: they are all inside and aligned
 __device__ __forceinline__ void store4(void* p, size_t i, bool bf16, bool vec, int left, f32x4 v) {
@@ -72,15 +72,17 @@ __device__ __forceinline__ void store_state4(float* s, long row, int d, int K, b
   }
 }
 
-// A wave's tile (tokens 16 w + 4 q + i, channel r) as NP parts into [channel][token]
+// A wave's tile (tokens t .. t + 3 = 16 w + 4 q .., channel r) as NP parts into the
+// operands' order, [part][step][lane] 16 bytes: reads are whole lines without bank
+// conflicts
 template <int NP>
 __device__ __forceinline__ void put_tile(uint16_t* dst, int r, int t, f32x4 v) {
   uint32_t a[NP], b[NP];
   split2<NP>(v[0], v[1], a);
   split2<NP>(v[2], v[3], b);
+  uint16_t* at = dst + ((t >> 5) * 64 + ((t >> 3) & 3) * 16 + r) * 8 + (t & 4);
 #pragma unroll
-  for (int p = 0; p < NP; ++p)
-    *reinterpret_cast<uint2*>(dst + (p * 16 + r) * kPitch + t) = make_uint2(a[p], b[p]);
+  for (int p = 0; p < NP; ++p) *reinterpret_cast<uint2*>(at + p * kTile) = make_uint2(a[p], b[p]);
 }
 // The operand of token step s from such a tile
 template <int NP>
@@ -88,7 +90,7 @@ __device__ __forceinline__ Frag<NP> get_tile(const uint16_t* src, int r, int q, 
   Frag<NP> f;
 #pragma unroll
   for (int p = 0; p < NP; ++p)
-    f.p[p] = *reinterpret_cast<const uint4*>(src + (p * 16 + r) * kPitch + 32 * s + 8 * q);
+    f.p[p] = *reinterpret_cast<const uint4*>(src + p * kTile + (s * 64 + q * 16 + r) * 8);
   return f;
 }
 
@@ -133,9 +135,9 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
   constexpr int ND = KP / 32, CT = KP / 64;
   constexpr int kState = ND * NS * kDeltaFrag;
   __shared__ __align__(16) unsigned char Ssh[NV * kState];
-  __shared__ __align__(16) uint16_t Rsh[NV][NS * 16 * kPitch];
-  __shared__ __align__(16) uint16_t Ush[NV][NS * 16 * kPitch];
-  __shared__ __align__(16) uint16_t Wsh[SAVE ? 1 : NV][SAVE ? 8 : NO * 16 * kPitch];
+  __shared__ __align__(16) uint16_t Rsh[NV][NS * kTile];
+  __shared__ __align__(16) uint16_t Ush[NV][NS * kTile];
+  __shared__ __align__(16) uint16_t Wsh[SAVE ? 1 : NV][SAVE ? 8 : NO * kTile];
 
   long group;
   unsigned slice;
@@ -341,10 +343,10 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
   constexpr int ND = KP / 32, CT = KP / 64;
   constexpr int kState = ND * NS * kDeltaFrag;
   __shared__ __align__(16) unsigned char Ssh[NV * kState];
-  __shared__ __align__(16) uint16_t Rsh[NV][NS * 16 * kPitch];
-  __shared__ __align__(16) uint16_t Ush[NV][NS * 16 * kPitch];
-  __shared__ __align__(16) uint16_t Dsh[NV][NI * 16 * kPitch];   // do
-  __shared__ __align__(16) uint16_t Csh[NV][NS * 16 * kPitch];   // scale e^G rq do
+  __shared__ __align__(16) uint16_t Rsh[NV][NS * kTile];
+  __shared__ __align__(16) uint16_t Ush[NV][NS * kTile];
+  __shared__ __align__(16) uint16_t Dsh[NV][NI * kTile];   // do
+  __shared__ __align__(16) uint16_t Csh[NV][NS * kTile];   // scale e^G rq do
 
   long group;
   unsigned slice;
