@@ -95,8 +95,10 @@ __device__ __forceinline__ void store8(void* p, size_t i, int dtype, bool vec, i
   }
 }
 
-// VEC: rows of q, k, v, do, dq, dk and dv take 16-byte accesses (else element by element)
-template <typename IN, int KP, bool VEC>
+// VEC: rows of q, k, v, do, dq, dk and dv take 16-byte accesses (else element by element).
+// SHARED: several value heads per key head; with one, dq and dk need no registers
+// through the walk over the value channels.
+template <typename IN, int KP, bool VEC, bool SHARED>
 __global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs a, int grad_dtype) {
   using Parts = DeltaParts<IN>;
   constexpr int NI = Parts::in, NS = Parts::state;
@@ -120,7 +122,7 @@ __global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs 
 
   const long slot = blockIdx.x / a.hk;
   const int kh = static_cast<int>(blockIdx.x - slot * a.hk);
-  const int rep = a.h / a.hk;
+  const int rep = SHARED ? a.h / a.hk : 1;
   long t0 = 0;
   const int n = delta_chunk(a, slot, &t0);
   if (n == 0) return;
@@ -497,8 +499,12 @@ hipError_t go(const DeltaLaunch& l, hipStream_t s) {
                    al16(a.dq) && al16(a.dk);
   const dim3 grid(static_cast<unsigned>(a.slots * a.hk)), block(KP * 4);
   return timed_launch(s, [&] {
-    if (vec) hipLaunchKernelGGL((delta_grads_kernel<IN, KP, true>), grid, block, 0, s, a, l.grad_dtype);
-    else hipLaunchKernelGGL((delta_grads_kernel<IN, KP, false>), grid, block, 0, s, a, l.grad_dtype);
+    auto run = [&](auto one, auto shared) {
+      if (a.h == a.hk) hipLaunchKernelGGL(one, grid, block, 0, s, a, l.grad_dtype);
+      else hipLaunchKernelGGL(shared, grid, block, 0, s, a, l.grad_dtype);
+    };
+    if (vec) run(delta_grads_kernel<IN, KP, true, false>, delta_grads_kernel<IN, KP, true, true>);
+    else run(delta_grads_kernel<IN, KP, false, false>, delta_grads_kernel<IN, KP, false, true>);
   });
 }
 
