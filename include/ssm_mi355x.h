@@ -529,7 +529,8 @@ ssm_status_t ssm_delta_chunk_check(const ssm_delta_chunk_params_t *p);
  * Key heads shared by several value heads receive the sum over them, in a fixed
  * order (no atomics: results repeat bit for bit).  The other fields are those of
  * the forward.  Workspace: ssm_delta_chunk_bwd_workspace_size() bytes (the
- * forward's, and two (K, V) states and two (64, V) tiles in f32 per chunk and head).
+ * forward's, two (K, V) states and two (64, V) tiles in f32 per chunk and head, and
+ * where value heads share key heads two (K) rows in f32 per token and value head).
  * ---------------------------------------------------------------------- */
 typedef struct ssm_delta_chunk_bwd_params {
   uint32_t struct_size; /* = sizeof(ssm_delta_chunk_bwd_params_t) */

@@ -69,6 +69,7 @@ struct DeltaArgs {
   const float* dstate_out;         // (nseq, h, V, K) or null
   void *dq, *dk, *dv;              // dense, or null
   float *dg, *dbeta, *dstate_in;   // or null
+  float *dq_part, *dk_part;        // (tokens, h, delta_kp) where heads share q and k
 };
 
 struct DeltaLaunch {

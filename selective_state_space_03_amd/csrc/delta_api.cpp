@@ -77,7 +77,7 @@ Range rows_of(const P* p, const void* ptr, int64_t stride, int64_t width, long t
 }
 
 struct DeltaWs {
-  size_t kf, qf, ktf, qtf, tf, pf, ttf, ptf, sc, s_chunk, ds_chunk, u_chunk, dr_chunk, total;
+  size_t kf, qf, ktf, qtf, tf, pf, ttf, ptf, sc, s_chunk, ds_chunk, u_chunk, dr_chunk, dq_part, dk_part, total;
 };
 
 template <typename P>
@@ -116,6 +116,11 @@ DeltaWs delta_ws(const P* p, bool bwd) {
     w.ds_chunk = take(state);
     w.u_chunk = take(rows64);
     w.dr_chunk = take(rows64);
+    if (p->nheads != p->nkheads) {
+      const size_t part = static_cast<size_t>(p->batch) * p->seqlen * p->nheads * ssm::delta_kp(p->d_key) * sizeof(float);
+      w.dq_part = take(part);
+      w.dk_part = take(part);
+    }
   }
   w.total = at;
   return w;
@@ -233,6 +238,8 @@ void delta_plan(const P* p, bool bwd, ssm::DeltaLaunch& l) {
     a.ds_chunk = reinterpret_cast<float*>(ws + w.ds_chunk);
     a.u_chunk = reinterpret_cast<float*>(ws + w.u_chunk);
     a.dr_chunk = reinterpret_cast<float*>(ws + w.dr_chunk);
+    a.dq_part = reinterpret_cast<float*>(ws + w.dq_part);
+    a.dk_part = reinterpret_cast<float*>(ws + w.dk_part);
   }
   l.in_dtype = p->x_dtype;
 }

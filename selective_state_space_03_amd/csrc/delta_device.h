@@ -221,6 +221,19 @@ __device__ __forceinline__ int delta_chunk(const DeltaArgs& a, long slot, long* 
   return left < kDeltaC ? static_cast<int>(left) : kDeltaC;
 }
 
+// Whether a token lies in one of the packed sequences.
+__device__ __forceinline__ bool delta_inside(const DeltaArgs& a, long t) {
+  int lo = 0, hi = a.nseq - 1;
+  if (hi < 0) return false;
+  while (lo < hi) {  // the last sequence that begins at or before it
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.cu[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  const DeltaSeq q = delta_seq(a, lo);
+  return t >= q.t0 && t < q.t0 + q.len;
+}
+
 // Workgroup b's (group, slice) for `slices` workgroups per group: the slices of
 // a group go to one XCD (blocks are dealt round the 8 XCDs), whose L2 then
 // serves the group's shared operands.  The grid holds 8 ceil(groups / 8) slices

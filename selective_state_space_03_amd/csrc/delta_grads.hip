@@ -10,8 +10,10 @@
 //   dG_t = every term's part of the exponent; dg_t = sum of dG from t to the chunk's end
 // and through the norm, dq = scale rq (dq^ - q~ (q~.dq^)), q~ = rq q.
 //
-// One workgroup takes a (chunk, key head) and its value heads in turn, so the
-// shared heads' dq and dk are summed in registers in a fixed order.  Wave w owns
+// One workgroup takes a (chunk, value head); where value heads share a key head,
+// their dq and dk are added up by a second kernel in a fixed order (holding the sums
+// in registers over a workgroup's heads instead cost 212 bytes of scratch per lane
+// and left a third of the workgroups).  Wave w owns
 // the key channels 16 w .. 16 w + 15 for the products with S and D, so those are
 // read and split into bf16 parts once, and a share of the tokens of row tile
 // rt = w % 4 for everything else; the rows do, dR and u of 32 value channels at a
@@ -96,9 +98,7 @@ __device__ __forceinline__ void store8(void* p, size_t i, int dtype, bool vec, i
 }
 
 // VEC: rows of q, k, v, do, dq, dk and dv take 16-byte accesses (else element by element).
-// SHARED: several value heads per key head; with one, dq and dk need no registers
-// through the walk over the value channels.
-template <typename IN, int KP, bool VEC, bool SHARED>
+template <typename IN, int KP, bool VEC>
 __global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs a, int grad_dtype) {
   using Parts = DeltaParts<IN>;
   constexpr int NI = Parts::in, NS = Parts::state;
@@ -120,9 +120,9 @@ __global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs 
   unsigned char* const cf = stage + kDeltaTri * NS * kDeltaFrag;       // columns of W: upper triangle
   unsigned char* const nf = stage;                                     // M + M^T, all 8
 
-  const long slot = blockIdx.x / a.hk;
-  const int kh = static_cast<int>(blockIdx.x - slot * a.hk);
-  const int rep = SHARED ? a.h / a.hk : 1;
+  const long slot = blockIdx.x / a.h;
+  const int head = static_cast<int>(blockIdx.x - slot * a.h);
+  const int rep = a.h / a.hk, kh = head / rep;
   long t0 = 0;
   const int n = delta_chunk(a, slot, &t0);
   if (n == 0) return;
@@ -173,8 +173,8 @@ __global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs 
       kq[i][e].set(Ks[at], Qs[at]);
     }
   }
-  {  // the products of k and q with k, which every head uses, stay in LDS
-    const float* nrm = a.sc + (static_cast<size_t>(slot) * a.h + kh * rep) * kDeltaSc;
+  {  // the products of k and q with k wait in LDS for their use
+    const float* nrm = a.sc + (static_cast<size_t>(slot) * a.h + head) * kDeltaSc;
     f32x4 kk[JT], qk[JT];
 #pragma unroll
     for (int j = 0; j < JT; ++j) kk[j] = qk[j] = zero;
@@ -204,9 +204,7 @@ __global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs 
   }
   __syncthreads();
 
-#pragma unroll 1
-  for (int hr = 0; hr < rep; ++hr) {
-    const int head = kh * rep + hr;
+  {
     const size_t hc = static_cast<size_t>(slot) * a.h + head;
     constexpr int kScEach = (kDeltaSc + NT - 1) / NT;
     float scr[kScEach];
@@ -447,18 +445,21 @@ __global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs 
     __syncthreads();
   }
 
-  // through the norms (rk and rq are the same for every head), and out by whole rows
+  // through the norms, and out by whole rows; where heads share q and k, as they are
+  // (per value head) for the kernel that adds them up
+  if (rep == 1) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float dq = sum16(kq[i][e].q() * dqa[i][e]), dk = sum16(kq[i][e].k() * dka[i][e]);
-      if (r == 0) {
-        rowp[w][0][16 * i + 4 * q + e] = dq;
-        rowp[w][1][16 * i + 4 * q + e] = dk;
+      for (int e = 0; e < 4; ++e) {
+        const float dq = sum16(kq[i][e].q() * dqa[i][e]), dk = sum16(kq[i][e].k() * dka[i][e]);
+        if (r == 0) {
+          rowp[w][0][16 * i + 4 * q + e] = dq;
+          rowp[w][1][16 * i + 4 * q + e] = dk;
+        }
       }
-    }
-  __syncthreads();
+    __syncthreads();
+  }
   constexpr int opitch = KP + 4;
   static_assert(kDeltaC * opitch <= 2 * kDeltaC * kLP, "a gradient's rows fit W and M");
 #pragma unroll 1
@@ -468,16 +469,18 @@ __global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = 16 * i + 4 * q + e;
-        const float rr = sc[(which ? kScRk : kScRq) * kDeltaC + t];
-        float dot = 0.0f;
+        float g = which ? dka[i][e] : dqa[i][e];
+        if (rep == 1) {
+          const float rr = sc[(which ? kScRk : kScRq) * kDeltaC + t];
+          float dot = 0.0f;
 #pragma unroll
-        for (int x = 0; x < NW; ++x) dot += rowp[x][which][t];
-        dot = a.qk_norm ? dot * rr * rr : 0.0f;
-        const float g = which ? dka[i][e] - kq[i][e].k() * dot : dqa[i][e] - kq[i][e].q() * dot;
-        WM[t * opitch + 16 * w + r] = (which ? 1.0f : a.scale) * rr * g;
+          for (int x = 0; x < NW; ++x) dot += rowp[x][which][t];
+          dot = a.qk_norm ? dot * rr * rr : 0.0f;
+          g = (which ? 1.0f : a.scale) * rr * (g - (which ? kq[i][e].k() : kq[i][e].q()) * dot);
+        }
+        WM[t * opitch + 16 * w + r] = g;
       }
     __syncthreads();
-    void* const dst = which ? a.dk : a.dq;
     constexpr int per = KP / 8;
 #pragma unroll
     for (int p = tid; p < kDeltaC * per; p += NT) {
@@ -485,10 +488,70 @@ __global__ __launch_bounds__(KP * 4, KP / 64) void delta_grads_kernel(DeltaArgs 
       const float4 x = *reinterpret_cast<const float4*>(WM + t * opitch + d);
       const float4 y = *reinterpret_cast<const float4*>(WM + t * opitch + d + 4);
       const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      if (dst && t < n && d < a.K) store8(dst, (static_cast<size_t>(t0 + t) * a.hk + kh) * a.K + d, grad_dtype, VEC, a.K - d, v);
+      if (t < n && d < a.K) {
+        if (rep == 1) {
+          void* const dst = which ? a.dk : a.dq;
+          if (dst) store8(dst, (static_cast<size_t>(t0 + t) * a.hk + kh) * a.K + d, grad_dtype, VEC, a.K - d, v);
+        } else {
+          float* const dst = which ? a.dk_part : a.dq_part;  // rows padded to KP
+          store8(dst, (static_cast<size_t>(t0 + t) * a.h + head) * KP + d, kF32, true, 8, v);
+        }
+      }
     }
     __syncthreads();
   }
+}
+
+// dq and dk of heads that share them: the sum over a key head's value heads, in their
+// order, and through the norms.  KP / 8 lanes per row, q's rows and then k's.
+template <typename IN, int KP>
+__global__ __launch_bounds__(256) void delta_heads_kernel(DeltaArgs a, int grad_dtype) {
+  constexpr int LPR = KP / 8;
+  const long row = (static_cast<long>(blockIdx.x) * 256 + threadIdx.x) / LPR;  // (token, key head)
+  if (row >= a.tokens * a.hk) return;  // whole rows leave together
+  const bool of_k = blockIdx.y != 0;
+  void* const dst = of_k ? a.dk : a.dq;
+  if (!dst) return;
+  const long t = row / a.hk;
+  if (a.cu && !delta_inside(a, t)) return;
+  const int kh = static_cast<int>(row - t * a.hk), rep = a.h / a.hk, d = (threadIdx.x % LPR) * 8;
+  const float* part = (of_k ? a.dk_part : a.dq_part) + (t * a.h + static_cast<long>(kh) * rep) * KP + d;
+  float g[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (d < a.K)
+    for (int h = 0; h < rep; ++h) {
+      const float4 x = reinterpret_cast<const float4*>(part + static_cast<long>(h) * KP)[0];
+      const float4 y = reinterpret_cast<const float4*>(part + static_cast<long>(h) * KP)[1];
+      g[0] += x.x; g[1] += x.y; g[2] += x.z; g[3] += x.w;
+      g[4] += y.x; g[5] += y.y; g[6] += y.z; g[7] += y.w;
+    }
+  float rr = 1.0f;
+  if (a.qk_norm) {
+    const IN* src = static_cast<const IN*>(of_k ? a.k : a.q) + t * (of_k ? a.k_stride : a.q_stride) + static_cast<long>(kh) * a.K;
+    Row8<IN> raw;
+    raw.load(src, d, a.K, a.vec_qk);
+    float x[8], ss = 0.0f, dot = 0.0f;
+    raw.get(a.K - d, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (d + i >= a.K) g[i] = 0.0f;  // (the padded columns hold zeros, or nothing)
+      ss = fmaf(x[i], x[i], ss);
+      dot = fmaf(x[i], g[i], dot);
+    }
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) {
+      ss += __shfl_xor(ss, o);
+      dot += __shfl_xor(dot, o);
+    }
+    rr = 1.0f / sqrtf(ss + a.eps);
+    dot *= rr * rr;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = fmaf(-x[i], dot, g[i]);
+  }
+  const float f = of_k ? rr : a.scale * rr;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] *= f;
+  const bool vec = a.K % 8 == 0 && (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
+  if (d < a.K) store8(dst, static_cast<size_t>(row) * a.K + d, grad_dtype, vec, a.K - d, g);
 }
 
 template <typename IN, int KP>
@@ -497,15 +560,16 @@ hipError_t go(const DeltaLaunch& l, hipStream_t s) {
   auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   const bool vec = a.vec_qk && a.V % 8 == 0 && a.v_stride % 8 == 0 && al16(a.v) && al16(a.dout) && al16(a.dv) &&
                    al16(a.dq) && al16(a.dk);
-  const dim3 grid(static_cast<unsigned>(a.slots * a.hk)), block(KP * 4);
-  return timed_launch(s, [&] {
-    auto run = [&](auto one, auto shared) {
-      if (a.h == a.hk) hipLaunchKernelGGL(one, grid, block, 0, s, a, l.grad_dtype);
-      else hipLaunchKernelGGL(shared, grid, block, 0, s, a, l.grad_dtype);
-    };
-    if (vec) run(delta_grads_kernel<IN, KP, true, false>, delta_grads_kernel<IN, KP, true, true>);
-    else run(delta_grads_kernel<IN, KP, false, false>, delta_grads_kernel<IN, KP, false, true>);
+  const dim3 grid(static_cast<unsigned>(a.slots * a.h)), block(KP * 4);
+  const hipError_t e = timed_launch(s, [&] {
+    if (vec) hipLaunchKernelGGL((delta_grads_kernel<IN, KP, true>), grid, block, 0, s, a, l.grad_dtype);
+    else hipLaunchKernelGGL((delta_grads_kernel<IN, KP, false>), grid, block, 0, s, a, l.grad_dtype);
   });
+  if (e != hipSuccess || a.h == a.hk || (!a.dq && !a.dk)) return e;
+  const long rows = 256 / (KP / 8);
+  hipLaunchKernelGGL((delta_heads_kernel<IN, KP>), dim3(static_cast<unsigned>((a.tokens * a.hk + rows - 1) / rows), 2),
+                     dim3(256), 0, s, a, l.grad_dtype);
+  return hipGetLastError();
 }
 
 }  // namespace
