@@ -23,6 +23,11 @@
  *                              + e^{dA[l]} C[l] prev_states + D x[l],
  *                       with the chunk-final state carried to the next chunk.
  *
+ * Next to them: the multi-head scan's decode step, the scan's backward, the
+ * layer's projections and the whole layer; the gated delta rule
+ * (ssm_delta_chunk_fwd, ssm_delta_chunk_bwd, ssm_delta_decode_step) and the
+ * norms before and after a block (ssm_block_norm_fwd, ssm_block_norm_bwd).
+ *
  * Conventions shared by every entry point
  *  - Every tensor pointer is a DEVICE pointer owned by the caller.  The scan,
  *    chunked-scan, decode and backward entry points allocate nothing, keep no

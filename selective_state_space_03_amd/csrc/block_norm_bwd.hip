@@ -7,6 +7,9 @@
 // computed.  The weights' gradients are column sums: every workgroup keeps running
 // sums in registers over the rows it walks and writes one partial row, and a second
 // kernel adds the partials in a fixed order (no atomics, the same result every time).
+// 8192 x 2560, every part, f32 residual (461 MB): 141 us, 3.3 TB/s, and 6 us for the
+// sums; what is left is the three sums in turn at two waves per SIMD (260 us with the
+// weights read among the rows' loads, which return in order; 410 us one load at a time).
 #include "block_norm_device.h"
 
 namespace ssm {

@@ -11,6 +11,10 @@
 // instructions, first within the two halves, then between them.  q and k enter the products
 // unscaled (bf16 rows are exact operands); the reciprocal norms, decays, gates
 // and the readout scale are folded into L, P and per-token coefficients.
+//
+// Bound by latency (seven barriers and two substitutions' lengths a head) and by what
+// it writes, 33 KB per chunk and head.  12289 packed tokens, 80 heads on 8 key heads,
+// K 64: 211 us (573 MB written, 2.7 TB/s); 8192 tokens, 32 heads on 16, K 128: 80 us.
 #include "delta_device.h"
 
 namespace ssm {
@@ -332,7 +336,8 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
 
 // Workgroups per (chunk, key head): the value heads share the rows and their
 // products, so a workgroup takes as many (up to kHeads) as leave the GPU's CUs eight
-// workgroups each.
+// workgroups each (five heads each at the packed call above 211 us, one 344 us; two
+// at the prompt 80 us, one 102 us).
 int head_parts(const DeltaArgs& a) {
   const long rep = a.h / a.hk, want = 8L * 256, have = a.slots * a.hk;
   const long parts = (want + have - 1) / have, least = (rep + kHeads - 1) / kHeads;

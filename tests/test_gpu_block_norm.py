@@ -98,7 +98,7 @@ def test_widths(d, dtype):
 
 @pytest.mark.parametrize("d", [264, 640, 1111, 1600, 2000, 2560, 2700, 4096])
 def test_many_rows(d):
-    """From 1024 rows on a wave takes a row by itself in the forward."""
+    """More rows than the backward has workgroups: each walks several."""
     opt = OPTS["all"]
     _check(_inputs(d, 1027, d, BF, opt), opt, what=f"d={d}")
 

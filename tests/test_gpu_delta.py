@@ -298,7 +298,7 @@ def test_step(K, V, dtype, batch):
 
 
 def test_step_wide_rows_and_strides():
-    """Enough rows for four per lane group, token rows taken from a wider projection."""
+    """Many rows, token rows taken from a wider projection."""
     n, Hk, H, K, V = 64, 4, 16, 64, 50
     c, st = _case(60, n, 1, Hk, H, K, V, torch.bfloat16)
     wide = torch.full((n, 2 * Hk * K + H * V + 8), float("nan"), device=DEV, dtype=torch.bfloat16)
