@@ -216,7 +216,7 @@ void delta_plan(const P* p, bool bwd, ssm::DeltaLaunch& l) {
   a.K = p->d_key;
   a.V = p->d_value;
   a.tokens = static_cast<long>(p->batch) * p->seqlen;
-  a.slots = a.tokens > 0 ? delta_slots(p) : 0;
+  a.slots = a.tokens > 0 && p->num_seqs > 0 ? delta_slots(p) : 0;  // (no sequence: no chunk, and cu[1] is not there)
   a.scale = p->scale;
   a.eps = p->eps;
   a.qk_norm = p->qk_norm != 0;
@@ -282,8 +282,8 @@ ssm_status_t norm_check_common(const P* p) {
   const int64_t most = static_cast<int64_t>(1) << 40;
   if ((p->x_stride && (p->x_stride < p->width || p->x_stride > most)) || (p->z_stride && (p->z_stride < p->width || p->z_stride > most)))
     return fail(SSM_ERR_INVALID_ARG, "x_stride or z_stride is shorter than a row (or beyond 2^40)");
-  if (p->rows > (static_cast<int64_t>(1) << 31) / (p->width / p->group_size))
-    return fail(SSM_ERR_UNSUPPORTED, "rows * (width / group_size) must be at most 2^31");
+  if (p->rows > 0x7fffffffLL / (p->width / p->group_size))
+    return fail(SSM_ERR_UNSUPPORTED, "rows * (width / group_size) must be below 2^31");
   if (p->rows > 0 && !p->x) return fail(SSM_ERR_INVALID_ARG, "x is NULL");
   if (!aligned({p->x, p->z}, esize(p->x_dtype)) || !aligned({p->residual}, esize(p->res_dtype)) ||
       !aligned({p->norm_w, p->scale, p->out_norm_w}, 4))

@@ -85,6 +85,12 @@ def _rows(t, name, shape, dtype, device):
     return t.data_ptr(), row
 
 
+def _zeros(shape, dtype, device, stream):
+    t = _empty(shape, dtype, device, stream)
+    with torch.cuda.stream(stream):  # (None: the current one)
+        return t.zero_()
+
+
 def _workspace(p, need, workspace, dev, stream):
     if workspace is None and need > 0:
         workspace = _empty(need, torch.uint8, dev, stream)
@@ -125,7 +131,8 @@ def delta_chunk_fwd(q, k, v, g, beta, *, scale=None, qk_norm=False, eps=1e-6, cu
                     state_out=None, o=None, o_dtype=None, workspace=None, stream=None, prepare=False):
     """The gated delta rule over whole sequences (ssm_delta_chunk_fwd): q, k (batch, L, Hk, K),
     v (batch, L, H, V), g and beta (batch, L, H) fp32; head h reads key head h // (H // Hk).
-    cu_seqlens: int32 offsets on the GPU of sequences packed into one batch row.  scale defaults to
+    cu_seqlens: int32 offsets on the GPU of sequences packed into one batch row (tokens of no sequence
+    are not written).  scale defaults to
     1 / sqrt(K); qk_norm scales q and k to unit length first.  state_in / state_out
     (sequences, H, V, K) fp32.  q, k and v may be slices of a wider tensor along the token's row.
     Returns o (batch, L, H, V), or with prepare=True a Call that enqueues this same call again."""
@@ -158,8 +165,8 @@ def delta_chunk_bwd(q, k, v, g, beta, dout, *, scale=None, qk_norm=False, eps=1e
     p.dstate_out = _arg(dstate_out, "dstate_out", shape, _F32, dev)
     gd = grad_dtype or _F32
     p.grad_dtype = _dtype(gd, "grad_dtype")
-    # tokens outside every packed sequence are not written: they start as zeros
-    make = _empty if cu_seqlens is None else lambda s, d, v_, st: _empty(s, d, v_, st).zero_()
+    # tokens outside every packed sequence are not written: they start as zeros (on the call's stream)
+    make = _empty if cu_seqlens is None else _zeros
     out = {"q": make(tuple(q.shape), gd, dev, stream), "k": make(tuple(k.shape), gd, dev, stream),
            "v": make(tuple(v.shape), gd, dev, stream), "g": make(tuple(g.shape), _F32, dev, stream),
            "beta": make(tuple(g.shape), _F32, dev, stream)}

@@ -348,6 +348,39 @@ def test_on_another_stream():
     assert all(torch.equal(g[x], gw[x]) for x in gw)
 
 
+def test_packed_gradients_on_another_stream():
+    """The zeros that tokens outside the sequences get are written on the call's stream too."""
+    cu = [3, 70, 190]
+    c, st = _case(73, 1, 200, 2, 4, 48, 40, torch.bfloat16, cu=cu)
+    do = torch.randn_like(c["v"])
+    want = ssm.delta_chunk_bwd(c["q"], c["k"], c["v"], c["g"], c["beta"], do, qk_norm=True, cu_seqlens=_cu(cu), state_in=st)
+    for x in ("q", "k", "v", "g", "beta"):
+        assert not want[x][:, :3].any() and not want[x][:, 190:].any() and want[x][:, 3:190].any()
+    offsets = _cu(cu)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    spin = torch.randn(4096, 4096, device=DEV)
+    for _ in range(4):
+        for _ in range(8):
+            spin = torch.tanh(spin @ spin)  # work that keeps the current stream behind
+        got = ssm.delta_chunk_bwd(c["q"], c["k"], c["v"], c["g"], c["beta"], do, qk_norm=True, cu_seqlens=offsets,
+                                  state_in=st, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[x], want[x]) for x in want)
+
+
+def test_no_sequence_at_all():
+    """One offset, no sequence: nothing is read or written, gradients are zeros."""
+    c, _ = _case(74, 1, 100, 1, 2, 32, 16, state=False)
+    o = torch.full_like(c["v"], 5.0)
+    cu = _cu([0])
+    out = torch.empty((0, 2, 16, 32), device=DEV)
+    ssm.delta_chunk_fwd(c["q"], c["k"], c["v"], c["g"], c["beta"], cu_seqlens=cu, o=o, state_out=out)
+    g = ssm.delta_chunk_bwd(c["q"], c["k"], c["v"], c["g"], c["beta"], c["v"], cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert (o == 5).all() and not any(t.any() for t in g.values())
+
+
 def test_graph_replays():
     """Prefill, backward and a decode step recorded in one graph, replayed with eager work between."""
     c, st = _case(71, 1, 200, 2, 4, 64, 32, torch.bfloat16)
