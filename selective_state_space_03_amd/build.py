@@ -18,7 +18,7 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libssm_mi355x_debug.so")
 SOURCES = ["api.cpp", "scan_fused.hip", "scan_xy_bb.hip", "scan_xy_bf.hip", "scan_xy_fb.hip", "scan_xy_ff.hip",
            "decode_step.hip", "ssd_chunk.hip", "ssd_generic.hip", "ssd_decode.hip", "gemm.hip", "layer.hip", "scan_bwd.hip",
            "scan_blocked.hip", "delta_api.cpp", "delta_prep.hip", "delta_pass.hip", "delta_grads.hip", "delta_step.hip",
-           "block_norm_fwd.hip", "block_norm_bwd.hip"]
+           "block_norm_fwd.hip", "block_norm_bwd.hip", "block_norm_bwd_first.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU forms are kept out of the generated code: the compiler

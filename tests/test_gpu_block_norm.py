@@ -103,6 +103,14 @@ def test_many_rows(d):
     _check(_inputs(d, 1027, d, BF, opt), opt, what=f"d={d}")
 
 
+@pytest.mark.parametrize("d", [4104, 5120, 8192, 9001])
+@pytest.mark.parametrize("dtype,grads", [(F32, F32), (BF, F32), (BF, BF)])
+@pytest.mark.parametrize("name", ["all", "all_first"])
+def test_many_long_rows(d, dtype, grads, name):
+    """Rows long enough for the widest team, more of them than workgroups."""
+    _check(_inputs(d, 519, d, dtype, OPTS[name], dtype), OPTS[name], grad_dtype=grads, what=f"{name} d={d}")
+
+
 @pytest.mark.parametrize("group,groups", [(1, 5), (8, 3), (96, 10), (100, 3), (128, 32), (257, 3), (600, 2)])
 @pytest.mark.parametrize("whole", [False, True])
 def test_groups(group, groups, whole):
