@@ -498,9 +498,10 @@ ssm_status_t ssm_layer_check(const ssm_layer_params_t *p);
  * The sequence is taken in chunks of 64 tokens whose corrections u solve one
  * triangular system each, with matrix products throughout.  bf16 operands are
  * exact; 32-bit operands (f32 inputs, the state, u) enter the matrix cores as
- * two or three bf16 parts, so an f32 result carries f32 accuracy.
- * Workspace: ssm_delta_chunk_workspace_size() bytes, 256-byte aligned (about
- * 31 KB per chunk and head and 48 KB per chunk and key head at K = 128 in bf16).
+ * three bf16 parts, so an f32 result carries f32 accuracy and a bf16 one is that
+ * rounded once.
+ * Workspace: ssm_delta_chunk_workspace_size() bytes, 256-byte aligned (39.7 kB per
+ * chunk and head and 49.2 kB per chunk and key head at K = 128 in bf16).
  * Supported: K <= 128, any V, x_dtype f32 or bf16, L == 0 copies the state.
  * ---------------------------------------------------------------------- */
 typedef struct ssm_delta_chunk_params {

@@ -29,21 +29,21 @@ constexpr int kDeltaTri = 6;       // fragments of a triangular 64 x 64 operand 
 constexpr int kDeltaSc = 11 * kDeltaC;
 enum DeltaScRow { kScBeta = 0, kScR, kScO, kScU, kScGamma, kScRk, kScRq, kScEg, kScG, kScEl = kScG + 2 };
 
-// bf16 parts that stand for a 32-bit operand of a matrix product (its leading
-// 8, 16 or 24 bits): the inputs (bf16 inputs are exact in one); the state chain T, S,
-// u and the gradients, which keep all 24 bits, as sums and states are held in 32 (two
-// parts would leave f32 results 3e-6 to 1e-5 off instead of 2e-7); and the operands
-// that only reach o, where two parts of bf16 inputs are far below o's own rounding.
+// bf16 parts that stand for a 32-bit operand of a matrix product: the inputs (bf16
+// inputs are exact in one), and everything formed from them, T, P, S, u and the
+// gradients, which keep all 24 bits, as sums and states are held in 32.  Two parts of
+// the operands that only reach o left it 3e-5 of its largest value off instead of 2e-7:
+// small outputs of a bf16 o were then off by more than its own rounding.
 template <typename IN>
 struct DeltaParts;
 struct bf16s;
 template <>
 struct DeltaParts<bf16s> {
-  static constexpr int in = 1, state = 3, out = 2;
+  static constexpr int in = 1, state = 3;
 };
 template <>
 struct DeltaParts<float> {
-  static constexpr int in = 3, state = 3, out = 3;
+  static constexpr int in = 3, state = 3;
 };
 
 struct DeltaArgs {

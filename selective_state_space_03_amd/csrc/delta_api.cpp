@@ -90,7 +90,7 @@ template <typename P>
 DeltaWs delta_ws(const P* p, bool bwd) {
   const size_t slots = delta_slots(p), kc = slots * p->nkheads, hc = slots * p->nheads;
   const size_t nd = ssm::delta_kp(p->d_key) / 32;
-  const size_t ni = p->x_dtype == SSM_BF16 ? 1 : 3, ns = 3, no = p->x_dtype == SSM_BF16 ? 2 : 3;
+  const size_t ni = p->x_dtype == SSM_BF16 ? 1 : 3, ns = 3;
   DeltaWs w{};
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -105,7 +105,7 @@ DeltaWs delta_ws(const P* p, bool bwd) {
   w.tf = take(hc * ssm::kDeltaTri * ns * ssm::kDeltaFrag);
   w.sc = take(hc * ssm::kDeltaSc * sizeof(float));
   if (!bwd) {
-    w.pf = take(hc * ssm::kDeltaTri * no * ssm::kDeltaFrag);
+    w.pf = take(hc * ssm::kDeltaTri * ns * ssm::kDeltaFrag);
   } else {
     w.qtf = take(rows);
     w.ttf = take(hc * ssm::kDeltaTri * ns * ssm::kDeltaFrag);

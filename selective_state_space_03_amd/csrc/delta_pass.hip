@@ -137,13 +137,13 @@ __device__ __forceinline__ void put_states(unsigned char* dst, int w, int lane, 
 template <typename IN, int KP, int NV, bool SAVE>
 __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices, int o_bf16, int vec_o) {
   using Parts = DeltaParts<IN>;
-  constexpr int NI = Parts::in, NS = Parts::state, NO = Parts::out;
+  constexpr int NI = Parts::in, NS = Parts::state;
   constexpr int ND = KP / 32, CT = KP / 64;
   constexpr int kState = ND * NS * kDeltaFrag;
   __shared__ __align__(16) unsigned char Ssh[NV * kState];
   __shared__ __align__(16) uint16_t Rsh[NV][NS * kTile];
   __shared__ __align__(16) uint16_t Ush[NV][NS * kTile];
-  __shared__ __align__(16) uint16_t Wsh[SAVE ? 1 : NV][SAVE ? 8 : NO * kTile];
+  __shared__ __align__(16) uint16_t Wsh[SAVE ? 1 : NV][SAVE ? 8 : NS * kTile];
 
   long group;
   unsigned slice;
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
   // after its last use, so a chunk's loads have the rest of the chunk before to arrive
   Frag<NI> fk[ND], fq[SAVE ? 1 : ND], fkt[CT][2];
   Frag<NS> ft[2];
-  Frag<NO> fp[2];
+  Frag<NS> fp[2];
   // Waves 0 and 1 have no second step of the triangles: theirs stays zero, which costs
   // nothing beside waves 2 and 3 (skipping it measured the same) and keeps the products
   // free of branches: between a matrix instruction and the first use of its result the
@@ -222,9 +222,9 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
       for (int s = 0; s < 2; ++s) fkt[i][s] = load_frag<NI>(a.ktf + khead + c * kstep, 2 * (w * CT + i) + s, lane);
     gamma = sc[kScGamma * kDeltaC];
     if (!SAVE) {
-      const unsigned char* pf = a.pf + hc * (kDeltaTri * NO * kDeltaFrag);
-      fp[0] = load_frag<NO>(pf, low_frag(w, 0), lane);
-      if (w >= 2) fp[1] = load_frag<NO>(pf, low_frag(w, 1), lane);
+      const unsigned char* pf = a.pf + hc * (kDeltaTri * NS * kDeltaFrag);
+      fp[0] = load_frag<NS>(pf, low_frag(w, 0), lane);
+      if (w >= 2) fp[1] = load_frag<NS>(pf, low_frag(w, 1), lane);
       co = sc[kScO * kDeltaC + 16 * w + r];
     }
   };
@@ -262,12 +262,7 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
       for (int s = 0; s < ND; ++s) {
         const Frag<NS> st = load_frag<NS>(Ssh + e * kState, s, lane);
         ks = mma(fk[s], st, ks);
-        if (!SAVE) {
-          Frag<NO> so;
-#pragma unroll
-          for (int p = 0; p < NO; ++p) so.p[p] = st.p[p];
-          ot[e] = mma(so, fq[s], ot[e]);
-        }
+        if (!SAVE) ot[e] = mma(st, fq[s], ot[e]);
       }
       f32x4 rr;
 #pragma unroll
@@ -290,7 +285,7 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
       }
       put_tile<NS>(Ush[e], r, 16 * w + 4 * q, us);
       if (!SAVE) {
-        put_tile<NO>(Wsh[e], r, 16 * w + 4 * q, u);
+        put_tile<NS>(Wsh[e], r, 16 * w + 4 * q, u);
       } else {
         const int v = v0 + 16 * e + r;
         float* dst = a.u_chunk + (hc * kDeltaC + 16 * w + 4 * q) * vp + v;
@@ -317,8 +312,8 @@ __global__ __launch_bounds__(256) void delta_pass_kernel(DeltaArgs a, int slices
         f32x4 o = ot[e];
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[x] *= co;
-        o = mma(get_tile<NO>(Wsh[e], r, q, 0), fp[0], o);
-        o = mma(get_tile<NO>(Wsh[e], r, q, 1), fp[1], o);
+        o = mma(get_tile<NS>(Wsh[e], r, q, 0), fp[0], o);
+        o = mma(get_tile<NS>(Wsh[e], r, q, 1), fp[1], o);
         const int t = 16 * w + r, v = v0 + 16 * e + 4 * q, left = a.V - v;
         if (t < n && left > 0)
           store4(a.o, (static_cast<size_t>(t0 + t) * a.h + head) * a.V + v, o_bf16, vec_o && left >= 4, left, o);

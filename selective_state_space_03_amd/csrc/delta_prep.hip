@@ -13,7 +13,7 @@
 // and the readout scale are folded into L, P and per-token coefficients.
 //
 // Bound by latency (seven barriers and two substitutions' lengths a head) and by what
-// it writes, 33 KB per chunk and head.  12289 packed tokens, 80 heads on 8 key heads,
+// it writes, 39.7 kB per chunk and head.  12289 packed tokens, 80 heads on 8 key heads,
 // K 64: 211 us (573 MB written, 2.7 TB/s); 8192 tokens, 32 heads on 16, K 128: 80 us.
 #include "delta_device.h"
 
@@ -79,7 +79,7 @@ __device__ __forceinline__ float exp_of(double x) { return exp2_fast(static_cast
 template <typename IN, int KP, bool BWD>
 __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int parts) {
   using Parts = DeltaParts<IN>;
-  constexpr int NI = Parts::in, NS = Parts::state, NO = Parts::out;
+  constexpr int NI = Parts::in, NS = Parts::state;
   constexpr int ND = KP / 32;                              // 32-channel steps
   constexpr int pitch = KP + 16 / static_cast<int>(sizeof(IN));
   constexpr int tile = kDeltaC * pitch * static_cast<int>(sizeof(IN));
@@ -250,9 +250,9 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
       for (int i = 0; i < 4; ++i) Pm[(32 * (w - 2) + 4 * q + i) * kLP + 32 * (w - 2) + 16 + r] = 0.0f;
     __syncthreads();
     if (!BWD) {
-      unsigned char* pf = a.pf + at * (kDeltaTri * NO * kDeltaFrag);
+      unsigned char* pf = a.pf + at * (kDeltaTri * NS * kDeltaFrag);
       for (int s = 0; s <= (w >> 1); ++s)
-        store_frag<NO>(pf, low_frag(w, s), lane, frag_row<NO>(Pm + (16 * w + r) * kLP + 32 * s + 8 * q));
+        store_frag<NS>(pf, low_frag(w, s), lane, frag_row<NS>(Pm + (16 * w + r) * kLP + 32 * s + 8 * q));
     } else {
       unsigned char* ptf = a.ptf + at * (kDeltaTri * NS * kDeltaFrag);
       for (int s = w >> 1; s < 2; ++s)

@@ -1,0 +1,45 @@
+"""GPU parity of the gated delta rule at its edges, against the float64 oracle, through the C ABI.
+
+Bounds, set before the first run: the operands of every matrix product keep 24 bits and sums are 32-bit, so a
+result before its rounding is off by a few times 2^-23 per product of the longest chain, 1e-5 of the result's
+largest value, whatever the inputs' type.  A bf16 result adds its own rounding, 2^-8 of each value."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_03_amd as ssm
+from gpu_util import DEV, check, np64
+from oracle import delta_oracle as D
+
+pytestmark = pytest.mark.gpu
+TOL = 1e-5
+BF, F32 = torch.bfloat16, torch.float32
+NAMES = ("q", "k", "v", "g", "beta")
+
+
+def _case(seed, n, L, Hk, H, K, V, dtype, seqs=None):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731
+    c = dict(q=rnd(n, L, Hk, K).to(dtype), k=rnd(n, L, Hk, K).to(dtype), v=rnd(n, L, H, V).to(dtype),
+             g=-torch.rand((n, L, H), generator=gen, device=DEV), beta=torch.sigmoid(rnd(n, L, H)))
+    return c, rnd(seqs or n, H, V, K), rnd(n, L, H, V).to(dtype), rnd(seqs or n, H, V, K)
+
+
+def _args(c):
+    return [c[x] for x in NAMES]
+
+
+def _ref(c):
+    return [np64(c[x]) for x in NAMES]
+
+
+@pytest.mark.parametrize("K,V,L", [(128, 128, 700), (64, 96, 700), (100, 40, 300)])
+def test_o_of_bf16_inputs_keeps_32_bits(K, V, L):
+    """An f32 o carries f32 accuracy, and a bf16 o is that o rounded once."""
+    c, st, _, _ = _case(K, 1, L, 1, 2, K, V, BF)
+    o = ssm.delta_chunk_fwd(*_args(c), qk_norm=True, state_in=st, o_dtype=F32)
+    ob = ssm.delta_chunk_fwd(*_args(c), qk_norm=True, state_in=st)
+    torch.cuda.synchronize()
+    ro, _ = D.delta_rule(*_ref(c), qk_norm=True, state=np64(st))
+    check(np64(o), ro, TOL, "f32 o")
+    assert ob.dtype == BF and torch.equal(ob, o.to(BF))
