@@ -150,8 +150,9 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
         sq += __shfl_xor(sq, o);
       }
       if (d == 0) {
-        rks[t] = a.qk_norm ? 1.0f / sqrtf(sk + a.eps) : 1.0f;
-        rqs[t] = a.qk_norm ? 1.0f / sqrtf(sq + a.eps) : 1.0f;
+        // (0 past the chunk's end: with eps = 0 a row of zeros has no reciprocal norm)
+        rks[t] = t >= n ? 0.0f : a.qk_norm ? 1.0f / sqrtf(sk + a.eps) : 1.0f;
+        rqs[t] = t >= n ? 0.0f : a.qk_norm ? 1.0f / sqrtf(sq + a.eps) : 1.0f;
       }
     }
   }

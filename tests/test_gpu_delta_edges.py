@@ -43,3 +43,30 @@ def test_o_of_bf16_inputs_keeps_32_bits(K, V, L):
     ro, _ = D.delta_rule(*_ref(c), qk_norm=True, state=np64(st))
     check(np64(o), ro, TOL, "f32 o")
     assert ob.dtype == BF and torch.equal(ob, o.to(BF))
+
+
+def _grads(c, do, st, ds, cu=None, **kw):
+    off = None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV)
+    g = ssm.delta_chunk_bwd(*_args(c), do, cu_seqlens=off, state_in=st, dstate_out=ds, **kw)
+    torch.cuda.synchronize()
+    return g, D.delta_rule_backward(*_ref(c), np64(do), cu=cu, state=np64(st), dstate=np64(ds), **kw)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("L,cu,Hk", [(1, None, 2), (63, None, 2), (64, None, 4), (65, None, 4), (77, None, 2),
+                                     (200, [0, 1, 64, 64, 200], 2)])
+def test_unit_rows_without_epsilon(dtype, L, cu, Hk):
+    """qk_norm with eps = 0 is x / |x|: the rows that fill a sequence's last chunk have no length to divide by, and
+    reach neither its results nor its gradients."""
+    n = 2 if cu is None else 1
+    c, st, do, ds = _case(L, n, L, Hk, 4, 48, 40, dtype, None if cu is None else len(cu) - 1)
+    off = None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV)
+    end = torch.empty_like(st)
+    o = ssm.delta_chunk_fwd(*_args(c), qk_norm=True, eps=0.0, cu_seqlens=off, state_in=st, state_out=end)
+    torch.cuda.synchronize()
+    ro, rs = D.delta_rule(*_ref(c), qk_norm=True, eps=0.0, cu=cu, state=np64(st))
+    check(np64(o), ro, TOL, "o", out_bf16=dtype == BF)
+    check(np64(end), rs, TOL, "state")
+    g, r = _grads(c, do, st, ds, cu, qk_norm=True, eps=0.0)
+    for x in g:
+        check(np64(g[x]), r[x], TOL, "d" + x)
