@@ -137,7 +137,8 @@ __device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.0f + exp2_
 // have the types of x and the residual), or -1
 int known_types(const NormArgs& a, bool same) {
   if (a.vec != 8 || !same) return -1;
-  const int rd = a.res || a.dres ? a.res_dtype : a.x_dtype;
+  const bool stream = a.res || a.res_out || a.dres || a.dresidual;  // a residual stream, in or out
+  const int rd = stream ? a.res_dtype : a.x_dtype;
   if (a.x_dtype == kBF16) return rd == kBF16 ? 2 : 1;
   return rd == kF32 ? 0 : -1;
 }

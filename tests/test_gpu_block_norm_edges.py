@@ -1,0 +1,48 @@
+"""GPU parity of the block norm at its edges, against the float64 oracle, through the C ABI.
+
+Bounds, set before the first run: all arithmetic is f32 on exact inputs, 1e-5 of the result's largest value; a
+bf16 result adds its own rounding, 2^-8 of each value."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_03_amd as ssm
+from gpu_util import DEV, check, np64
+from oracle import delta_oracle as D
+
+pytestmark = pytest.mark.gpu
+TOL = 1e-5
+BF, F32 = torch.bfloat16, torch.float32
+CODE = {F32: 0, BF: 1}
+
+
+def _inputs(seed, rows, d, dtype):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731
+    return {"x": rnd(rows, d).to(dtype), "z": rnd(rows, d).to(dtype), "norm_w": 1.0 + 0.3 * rnd(d), "scale": rnd(d),
+            "out_norm_w": 1.0 + 0.3 * rnd(d)}
+
+
+def _guarded(shape, dtype):
+    """A NaN-filled tensor and the elements behind it in the same allocation, twice its bytes and more."""
+    n = shape[0] * shape[1]
+    whole = torch.full((4 * n + 64,), 7.0, dtype=dtype, device=DEV)
+    whole[:n] = float("nan")
+    return whole[:n].view(shape), whole[n:]
+
+
+@pytest.mark.parametrize("d", [96, 100, 97, 2560])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("res", [F32, BF])
+def test_residual_out_without_residual_takes_res_dtype(d, dtype, res):
+    """t goes out in res_dtype, whatever the type of x, also where no residual comes in."""
+    c = _inputs(d, 5, d, dtype)
+    t, guard = _guarded((5, d), res)
+    call = ssm.block_norm_fwd(**c, residual_out=t, prepare=True)
+    call._p.res_dtype = CODE[res]
+    out, got = call.run()
+    torch.cuda.synchronize()
+    ro, rt = D.block_norm(**{k: np64(v) for k, v in c.items()})
+    assert got is t and (guard == 7).all()
+    check(np64(got), rt, TOL, "t", out_bf16=res == BF)
+    check(np64(out), ro, TOL, "out", out_bf16=dtype == BF)
