@@ -259,6 +259,7 @@ def block_norm_fwd(x, *, norm_w=None, z=None, gate_first=False, residual=None, s
         out = _empty(shape, out_dtype or x.dtype, dev, stream)
     if residual_out is not None:
         p.residual_out = _arg(residual_out, "residual_out", shape, (residual if residual is not None else residual_out).dtype, dev)
+        p.res_dtype = _code(residual_out, "residual_out")
     if out is not None:
         p.out = _arg(out, "out", shape, out.dtype, dev)
     p.out_dtype = _code(out, "out") if out is not None else 0

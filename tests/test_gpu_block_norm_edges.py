@@ -46,3 +46,22 @@ def test_residual_out_without_residual_takes_res_dtype(d, dtype, res):
     assert got is t and (guard == 7).all()
     check(np64(got), rt, TOL, "t", out_bf16=res == BF)
     check(np64(out), ro, TOL, "out", out_bf16=dtype == BF)
+
+
+@pytest.mark.parametrize("d", [96, 100, 97])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("res", [F32, BF])
+def test_binding_passes_residual_outs_type(d, dtype, res):
+    """The type of a residual_out given by the caller is the one the kernel writes."""
+    c = _inputs(d, 5, d, dtype)
+    t, guard = _guarded((5, d), res)
+    call = ssm.block_norm_fwd(**c, residual_out=t, prepare=True)
+    assert call._p.res_dtype == CODE[res]
+    call.run()
+    torch.cuda.synchronize()
+    assert (guard == 7).all()
+    check(np64(t), D.block_norm(**{k: np64(v) for k, v in c.items()})[1], TOL, "t", out_bf16=res == BF)
+    with pytest.raises(TypeError):
+        ssm.block_norm_fwd(**c, residual_out=torch.empty(5, d, dtype=torch.float16, device=DEV))
+    with pytest.raises(TypeError):
+        ssm.block_norm_fwd(**c, residual=torch.empty(5, d, dtype=F32 if res == BF else BF, device=DEV), residual_out=t)
