@@ -44,6 +44,15 @@ def _arg(t, name, shape, dtype, device):
     return _ptr(t, name, shape, dtype, device)
 
 
+def _gpu(t, name):
+    """The device that every other argument is compared with, which has to be a GPU."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
 def _dtype(d, name):
     if d not in _DT:
         raise TypeError(f"{name}: dtype {d} not supported (float32 or bfloat16)")
@@ -137,7 +146,7 @@ def delta_chunk_fwd(q, k, v, g, beta, *, scale=None, qk_norm=False, eps=1e-6, cu
     (sequences, H, V, K) fp32.  q, k and v may be slices of a wider tensor along the token's row.
     Returns o (batch, L, H, V), or with prepare=True a Call that enqueues this same call again."""
     L_ = lib()
-    dev = q.device
+    dev = _gpu(q, "q")
     p = DeltaChunkParams()
     shape = _delta_inputs(p, q, k, v, g, beta, scale, qk_norm, eps, cu_seqlens, state_in)
     if o is None:
@@ -158,7 +167,7 @@ def delta_chunk_bwd(q, k, v, g, beta, dout, *, scale=None, qk_norm=False, eps=1e
     grad_dtype (fp32 unless given), g, beta and, where a state was given, state_in in fp32; or with
     prepare=True a Call whose run() enqueues it again (its .out is that dict)."""
     L_ = lib()
-    dev = q.device
+    dev = _gpu(q, "q")
     p = DeltaChunkBwdParams()
     shape = _delta_inputs(p, q, k, v, g, beta, scale, qk_norm, eps, cu_seqlens, state_in)
     p.dout = _arg(dout, "dout", v.shape, q.dtype, dev)
@@ -187,7 +196,7 @@ def delta_decode_step(q, k, v, g, beta, state, *, scale=None, qk_norm=False, eps
     g and beta (batch, H) fp32, state (batch, H, V, K) fp32 updated in place.  Returns o (batch, H, V),
     or with prepare=True a Call that enqueues this same step again on each run()."""
     L_ = lib()
-    dev = q.device
+    dev = _gpu(q, "q")
     batch, hk, dk = q.shape
     h, dv = v.shape[1], v.shape[2]
     p = DeltaDecodeParams()
@@ -250,7 +259,7 @@ def block_norm_fwd(x, *, norm_w=None, z=None, gate_first=False, residual=None, s
     (out, residual_out): out is None where a residual but no out_norm_w is given (t is residual_out
     then), residual_out is None without a residual; with prepare=True a Call whose .out is that pair."""
     L_ = lib()
-    dev = x.device
+    dev = _gpu(x, "x")
     p = BlockNormParams()
     shape = _norm_inputs(p, x, norm_w, z, gate_first, residual, scale, out_norm_w, group_size, eps)
     if residual is not None and residual_out is None:
@@ -275,7 +284,7 @@ def block_norm_bwd(x, *, norm_w=None, z=None, gate_first=False, residual=None, s
     results.  Returns a dict of gradients for the inputs that were given: x and z in grad_dtype (fp32
     unless given), residual in the residual's dtype, norm_w, scale and out_norm_w in fp32."""
     L_ = lib()
-    dev = x.device
+    dev = _gpu(x, "x")
     p = BlockNormBwdParams()
     shape = _norm_inputs(p, x, norm_w, z, gate_first, residual, scale, out_norm_w, group_size, eps)
     if dout is not None:
