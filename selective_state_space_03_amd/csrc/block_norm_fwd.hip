@@ -20,7 +20,7 @@ namespace {
 // 16-byte accesses; -1: types and accesses as a says (then a lane holds twice the
 // registers for its raw values and every pointer's alternatives)
 template <int TPR, int NCH, int XD, int RD>
-__global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
+__global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a, long first) {
   __shared__ float sh[16];
   int turn = 0;
   constexpr bool kKnown = XD >= 0;
@@ -28,7 +28,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
   const int od = kKnown ? XD : a.out_dtype;
   constexpr int RPB = 256 / TPR;  // rows per workgroup
   const int l = threadIdx.x % TPR;
-  const long row_raw = static_cast<long>(blockIdx.x) * RPB + threadIdx.x / TPR;
+  const long row_raw = first + static_cast<long>(blockIdx.x) * RPB + threadIdx.x / TPR;
   const bool act = row_raw < a.rows;  // (whole teams; with TPR 256 every row is there)
   const long row = act ? row_raw : a.rows - 1;
   const long call_row = row / a.groups;
@@ -105,16 +105,22 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
   }
 }
 
+// A launch holds fewer than 2^32 threads: calls of more rows take several.
+constexpr long kMostBlocks = 1L << 23;
+
 template <int TPR, int NCH>
 hipError_t fwd(const NormArgs& a, hipStream_t s) {
   constexpr int RPB = 256 / TPR;
   return timed_launch(s, [&] {
-    const dim3 grid(static_cast<unsigned>((a.rows + RPB - 1) / RPB));
-    switch (known_types(a, !a.out || a.out_dtype == a.x_dtype)) {
-      case 0: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kF32, kF32>), grid, dim3(256), 0, s, a); break;
-      case 1: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kBF16, kF32>), grid, dim3(256), 0, s, a); break;
-      case 2: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kBF16, kBF16>), grid, dim3(256), 0, s, a); break;
-      default: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, -1, -1>), grid, dim3(256), 0, s, a);
+    for (long first = 0; first < a.rows; first += kMostBlocks * RPB) {
+      const long blocks = (a.rows - first + RPB - 1) / RPB;
+      const dim3 grid(static_cast<unsigned>(blocks < kMostBlocks ? blocks : kMostBlocks));
+      switch (known_types(a, !a.out || a.out_dtype == a.x_dtype)) {
+        case 0: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kF32, kF32>), grid, dim3(256), 0, s, a, first); break;
+        case 1: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kBF16, kF32>), grid, dim3(256), 0, s, a, first); break;
+        case 2: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, kBF16, kBF16>), grid, dim3(256), 0, s, a, first); break;
+        default: hipLaunchKernelGGL((norm_fwd_kernel<TPR, NCH, -1, -1>), grid, dim3(256), 0, s, a, first);
+      }
     }
   });
 }

@@ -65,3 +65,19 @@ def test_binding_passes_residual_outs_type(d, dtype, res):
         ssm.block_norm_fwd(**c, residual_out=torch.empty(5, d, dtype=torch.float16, device=DEV))
     with pytest.raises(TypeError):
         ssm.block_norm_fwd(**c, residual=torch.empty(5, d, dtype=F32 if res == BF else BF, device=DEV), residual_out=t)
+
+
+def test_more_rows_than_a_launch_holds():
+    """2^28 groups and some, 16 lanes each: the threads of one launch would be 2^32.  Every row equals that of a
+    call on a part of the rows."""
+    rows, d, n = (1 << 25) + 9, 64, 8
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.randn(rows, d, generator=gen, device=DEV, dtype=BF)
+    w = 1.0 + 0.3 * torch.randn(n, generator=gen, device=DEV)
+    out, _ = ssm.block_norm_fwd(x, norm_w=w)
+    for a, b in ((0, 1 << 23), (1 << 23, 1 << 24), (1 << 24, 3 << 23), (3 << 23, rows)):
+        part, _ = ssm.block_norm_fwd(x[a:b], norm_w=w)
+        torch.cuda.synchronize()
+        assert torch.equal(part, out[a:b]), (a, b)
+    last = slice(rows - 20, rows)
+    check(np64(out[last]), D.block_norm(np64(x[last]), norm_w=np64(w), group_size=n)[0], TOL, "last rows", out_bf16=True)
