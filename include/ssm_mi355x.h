@@ -503,6 +503,8 @@ ssm_status_t ssm_layer_check(const ssm_layer_params_t *p);
  * Workspace: ssm_delta_chunk_workspace_size() bytes, 256-byte aligned (39.7 kB per
  * chunk and head and 49.2 kB per chunk and key head at K = 128 in bf16).
  * Supported: K <= 128, any V, x_dtype f32 or bf16, L == 0 copies the state.
+ * A launch's 2^32 threads bound num_seqs * H * ceil(V / 32) and the chunks times H
+ * to below 2^24 (2^23 chunks times H in the backward with K > 64).
  * ---------------------------------------------------------------------- */
 typedef struct ssm_delta_chunk_params {
   uint32_t struct_size; /* = sizeof(ssm_delta_chunk_params_t) */

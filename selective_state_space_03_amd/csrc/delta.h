@@ -81,6 +81,21 @@ struct DeltaLaunch {
 
 inline int delta_kp(int K) { return K <= 64 ? 64 : 128; }
 __host__ __device__ inline int delta_vp(int V) { return (V + 31) / 32 * 32; }
+// Value channels per workgroup of the walks, in slices of 16: 32 once that still leaves
+// every CU a workgroup (the operands of T, P and the keys are then read half as often
+// and a chunk's three exchanges serve twice the work), else 16.  With 256 workgroups or
+// more at 32: packed call 415 us against 561, training walks 122 and 153 against 144
+// and 180; with fewer: prompt 268 us at 16 against 368.
+inline int delta_nv(long groups, int V) { return groups * ((V + 31) / 32) >= 256 && V > 16 ? 2 : 1; }
+// Workgroups per (sequence, head), and of a walk (backward: the kept tiles are padded,
+// the slices cover delta_vp channels)
+inline long delta_slices(long groups, int V, bool backward) {
+  const int width = 16 * delta_nv(groups, V);
+  return ((backward ? delta_vp(V) : V) + width - 1) / width;
+}
+inline long delta_walk_blocks(long groups, int V, bool backward) {
+  return (groups + 7) / 8 * 8 * delta_slices(groups, V, backward);
+}
 hipError_t launch_delta_prep(const DeltaLaunch& l, bool backward, hipStream_t s);
 // The forward walk; save: also writes s_chunk and u_chunk, and no output.
 hipError_t launch_delta_pass(const DeltaLaunch& l, bool save, hipStream_t s);

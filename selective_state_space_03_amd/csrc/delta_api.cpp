@@ -143,8 +143,10 @@ ssm_status_t delta_seq_check(const P* p, bool bwd) {
     return fail(SSM_ERR_INVALID_ARG, "packed sequences need batch 1; without cu_seqlens num_seqs must equal batch");
   if (!aligned({p->cu_seqlens, p->state_in}, 4)) return fail(SSM_ERR_INVALID_ARG, "cu_seqlens or state_in is not 4-byte aligned");
   const long slots = delta_slots(p);
-  const long slices = ssm::delta_vp(p->d_value) / 16;
-  if (slots * p->nheads > 0x7fffffffL || (static_cast<long>(p->num_seqs) * p->nheads + 7) * slices > 0x7fffffffL)
+  const long groups = static_cast<long>(p->num_seqs) * p->nheads;
+  // a launch holds fewer than 2^32 threads: workgroups of 256, of 512 in the gradients of K > 64
+  if (slots * p->nheads >= (bwd && p->d_key > 64 ? 1L << 23 : 1L << 24) ||
+      ssm::delta_walk_blocks(groups, p->d_value, bwd) >= 1L << 24)
     return fail(SSM_ERR_UNSUPPORTED, "too many chunks, sequences and heads for one launch");
   const size_t need = delta_ws(p, bwd).total;
   if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return fail(SSM_ERR_WORKSPACE, "workspace is missing or too small");

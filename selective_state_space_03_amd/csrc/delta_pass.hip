@@ -524,25 +524,11 @@ __global__ __launch_bounds__(256) void delta_reverse_kernel(DeltaArgs a, int sli
       }
 }
 
-unsigned grid_of(const DeltaArgs& a, int slices) {
-  const long groups = static_cast<long>(a.nseq) * a.h;
-  return static_cast<unsigned>((groups + 7) / 8 * 8 * slices);
-}
-
-// Value channels per workgroup: 32 once that still leaves every CU a workgroup
-// (the operands of T, P and the keys are then read half as often and a chunk's
-// three exchanges serve twice the work), else 16.  With 256 workgroups or more at 32:
-// packed call 415 us against 561, training walks 122 and 153 against 144 and 180;
-// with fewer: prompt 268 us at 16 against 368.
-bool wide(const DeltaArgs& a) {
-  return static_cast<long>(a.nseq) * a.h * ((a.V + 31) / 32) >= 256 && a.V > 16;
-}
-
 template <typename IN, int KP, int NV>
 hipError_t go(const DeltaLaunch& l, int what, hipStream_t s) {
-  // (the kept tiles are padded: their slices cover delta_vp channels)
-  const int slices = ((what == 0 ? l.a.V : delta_vp(l.a.V)) + 16 * NV - 1) / (16 * NV);
-  const dim3 grid(grid_of(l.a, slices));
+  const long groups = static_cast<long>(l.a.nseq) * l.a.h;
+  const int slices = static_cast<int>(delta_slices(groups, l.a.V, what != 0));
+  const dim3 grid(static_cast<unsigned>(delta_walk_blocks(groups, l.a.V, what != 0)));
   const int ob = l.o_dtype == kBF16;
   const int vec_o = l.a.V % 4 == 0 && (reinterpret_cast<uintptr_t>(l.a.o) & (ob ? 7 : 15)) == 0;
   if (what == 0)
@@ -558,7 +544,8 @@ hipError_t go(const DeltaLaunch& l, int what, hipStream_t s) {
 
 template <typename IN, int KP>
 hipError_t pick_nv(const DeltaLaunch& l, int what, hipStream_t s) {
-  return wide(l.a) ? go<IN, KP, 2>(l, what, s) : go<IN, KP, 1>(l, what, s);
+  return delta_nv(static_cast<long>(l.a.nseq) * l.a.h, l.a.V) == 2 ? go<IN, KP, 2>(l, what, s)
+                                                                   : go<IN, KP, 1>(l, what, s);
 }
 
 template <typename IN>

@@ -1,0 +1,37 @@
+"""The bounds that one launch's threads set on the gated delta rule's and the block norm's calls: the checks refuse
+what could not be launched (CPU only, pointers are compared and never dereferenced)."""
+import ctypes
+
+import pytest
+
+from selective_state_space_03_amd import binding as b
+from test_delta_abi import L, _bwd, _fwd  # noqa: F401
+
+MANY = dict(batch=1, cu_seqlens=1 << 50, workspace_bytes=1 << 62, workspace=1 << 55)
+
+
+def _check(L, p):  # noqa: F811
+    name = {b.DeltaChunkParams: "ssm_delta_chunk", b.DeltaChunkBwdParams: "ssm_delta_chunk_bwd"}[type(p)]
+    return getattr(L, name + "_check")(ctypes.byref(p))
+
+
+@pytest.mark.parametrize("seqs,heads,V,status", [
+    (1 << 16, 64, 128, 2), ((1 << 16) - 1, 64, 128, 0),  # 4 slices of 32 channels each: 2^24 workgroups of 256
+    (1 << 15, 64, 256, 2), ((1 << 15) - 1, 64, 256, 0), ((1 << 15) - 1, 64, 257, 2)])
+def test_many_short_sequences(L, seqs, heads, V, status):  # noqa: F811
+    assert _check(L, _fwd(**MANY, num_seqs=seqs, seqlen=seqs, nheads=heads, d_value=V, q=1 << 41, k=1 << 42, v=1 << 43,
+                          g=1 << 44, beta=1 << 45, o=1 << 46)) == status, L.ssm_last_error()
+    if status:
+        assert b"one launch" in L.ssm_last_error()
+
+
+def test_many_chunks(L):  # noqa: F811
+    """Chunks times heads: below 2^24 forward, below 2^23 where the gradients take 512 lanes a workgroup."""
+    far = dict(q=1 << 41, k=1 << 42, v=1 << 43, g=1 << 44, beta=1 << 45, batch=1, num_seqs=1, workspace_bytes=1 << 62,
+               workspace=1 << 55, nheads=64)
+    for make, K, log in ((_fwd, 128, 24), (_bwd, 64, 24), (_bwd, 128, 23)):
+        out = dict(o=1 << 46) if make is _fwd else dict(dout=1 << 46, dq=1 << 47, dk=1 << 48, dv=1 << 49, dg=1 << 50,
+                                                        dbeta=1 << 51)
+        chunks = 1 << (log - 6)
+        assert _check(L, make(**far, **out, d_key=K, seqlen=64 * chunks)) == 2
+        assert _check(L, make(**far, **out, d_key=K, seqlen=64 * (chunks - 1))) == 0, L.ssm_last_error()
