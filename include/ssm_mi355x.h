@@ -643,7 +643,8 @@ ssm_status_t ssm_block_norm_check(const ssm_block_norm_params_t *p);
  * dresidual in res_dtype, and dnorm_w (norm_w_len), dscale, dout_norm_w (width) in
  * f32; any may be NULL.  Column sums are taken in a fixed order (results repeat
  * bit for bit).  The workspace holds ssm_block_norm_bwd_workspace_size(p) bytes
- * (256-byte aligned).  The other fields are those of the forward.
+ * (256-byte aligned).  The other fields are those of the forward; a norm_w of the
+ * whole width may hold at most 2^22 groups.
  * ---------------------------------------------------------------------- */
 typedef struct ssm_block_norm_bwd_params {
   uint32_t struct_size; /* = sizeof(ssm_block_norm_bwd_params_t) */

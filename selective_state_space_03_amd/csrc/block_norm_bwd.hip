@@ -19,34 +19,37 @@ namespace {
 // eight loads of a run in flight
 __global__ __launch_bounds__(256) void norm_reduce_kernel(NormArgs a) {
   __shared__ float sh[8][33];
-  const int which = blockIdx.z, wr = blockIdx.y;
+  const int which = blockIdx.z;
   float* out = which == 0 ? a.dnorm_w : which == 1 ? a.dscale : a.dout_w;
   if (!out) return;
   const int c = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + c;
-  float s = 0.0f;
-  if (col < a.n) {
-    const float* src = a.part + static_cast<size_t>(which) * a.n + col;
-    const int step = 8 * a.w_period;
-    for (int p = wr + run * a.w_period; p < a.parts; p += 8 * step) {
-      float v[8];
+  const float* src = a.part + static_cast<size_t>(which) * a.n + (col < a.n ? col : 0);
+  const int step = 8 * a.w_period;
+  for (int wr = blockIdx.y; wr < a.w_period; wr += gridDim.y) {
+    float s = 0.0f;
+    if (col < a.n) {
+      for (int p = wr + run * a.w_period; p < a.parts; p += 8 * step) {
+        float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int q = p + i * step;
-        v[i] = src[static_cast<size_t>(q < a.parts ? q : p) * 3 * a.n];
-        if (q >= a.parts) v[i] = 0.0f;
+        for (int i = 0; i < 8; ++i) {
+          const int q = p + i * step;
+          v[i] = src[static_cast<size_t>(q < a.parts ? q : p) * 3 * a.n];
+          if (q >= a.parts) v[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += v[i];
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += v[i];
     }
-  }
-  sh[run][c] = s;
-  __syncthreads();
-  if (run == 0 && col < a.n) {
-    float t = sh[0][c];
+    sh[run][c] = s;
+    __syncthreads();
+    if (run == 0 && col < a.n) {
+      float t = sh[0][c];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += sh[i][c];
-    out[static_cast<size_t>(wr) * a.n + col] = t;
+      for (int i = 1; i < 8; ++i) t += sh[i][c];
+      out[static_cast<size_t>(wr) * a.n + col] = t;
+    }
+    __syncthreads();
   }
 }
 
@@ -86,7 +89,8 @@ hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
   const NormBwdShape b = bwd_shape(a.rows, a.n, a.w_period);
   const hipError_t e = a.gate_first ? run_norm_bwd<true>(a, b, s) : run_norm_bwd<false>(a, b, s);
   if (e != hipSuccess || (!a.dnorm_w && !a.dscale && !a.dout_w)) return e;
-  hipLaunchKernelGGL(norm_reduce_kernel, dim3((a.n + 31) / 32, a.w_period, 3), dim3(256), 0, s, a);
+  const int wrows = a.w_period < 65535 ? a.w_period : 65535;  // (the most workgroups along y)
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((a.n + 31) / 32, wrows, 3), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

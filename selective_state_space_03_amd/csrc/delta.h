@@ -134,12 +134,15 @@ struct NormArgs {
   int dout_dtype, dres_dtype, grad_dtype;
   void *dx, *dz, *dresidual;
   float *dnorm_w, *dscale, *dout_w;
-  float* part;    // (parts, 3, n * w_period) partial column sums
+  float* part;    // (parts, 3, n) partial column sums, part p of weight row p % w_period
   int parts;
 };
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
 int norm_bwd_parts(long rows, int n, int period);
 constexpr int kNormMax = 16384;  // longest normalised row
+// most weight rows of the backward: workgroups and partial rows are whole turns round
+// them, which keeps both and the steps between a weight row's partials in 31 bits
+constexpr int kNormMaxPeriod = 1 << 22;
 
 }  // namespace ssm

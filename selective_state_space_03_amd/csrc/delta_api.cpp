@@ -340,6 +340,8 @@ ssm_status_t norm_bwd_check(const ssm_block_norm_bwd_params_t* p) {
       !aligned({p->dout}, esize(p->dout_dtype)) || !aligned({p->dresidual_out}, esize(p->dres_dtype)) ||
       !aligned({p->dnorm_w, p->dscale, p->dout_norm_w}, 4))
     return fail(SSM_ERR_INVALID_ARG, "a gradient is not aligned to its element size");
+  if (norm_period(p) > ssm::kNormMaxPeriod)
+    return fail(SSM_ERR_UNSUPPORTED, "norm_w of the whole width must hold at most 2^22 groups");
   const size_t need = norm_bwd_ws(p);
   if (!p->workspace || p->workspace_bytes < need) return fail(SSM_ERR_WORKSPACE, "workspace is missing or too small");
   if (!aligned({p->workspace}, 256)) return fail(SSM_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
@@ -506,7 +508,7 @@ ssm_status_t ssm_block_norm_bwd_check(const ssm_block_norm_bwd_params_t* p) {
 
 size_t ssm_block_norm_bwd_workspace_size(const ssm_block_norm_bwd_params_t* p) {
   if (!p || p->struct_size != sizeof(*p) || p->rows < 0 || p->width <= 0 || p->group_size <= 0 ||
-      p->width % p->group_size != 0 || p->group_size > ssm::kNormMax)
+      p->width % p->group_size != 0 || p->group_size > ssm::kNormMax || norm_period(p) > ssm::kNormMaxPeriod)
     return 0;
   return norm_bwd_ws(p);
 }

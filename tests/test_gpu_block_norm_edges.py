@@ -81,3 +81,17 @@ def test_more_rows_than_a_launch_holds():
         assert torch.equal(part, out[a:b]), (a, b)
     last = slice(rows - 20, rows)
     check(np64(out[last]), D.block_norm(np64(x[last]), norm_w=np64(w), group_size=n)[0], TOL, "last rows", out_bf16=True)
+
+
+@pytest.mark.parametrize("groups,n", [(65535, 2), (65536, 2), (70001, 3)])
+def test_gradients_of_many_weight_rows(groups, n):
+    """A weight per channel in more groups than a launch holds workgroups along y."""
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731
+    x, w, do = rnd(3, groups * n), 1.0 + 0.3 * rnd(groups * n), rnd(3, groups * n)
+    g = ssm.block_norm_bwd(x, norm_w=w, group_size=n, dout=do)
+    torch.cuda.synchronize()
+    r = D.block_norm_backward(np64(x), norm_w=np64(w), group_size=n, dout=np64(do))
+    assert set(g) == {"x", "norm_w"}
+    check(np64(g["norm_w"]), r["norm_w"], TOL, "dnorm_w")
+    check(np64(g["x"]), r["x"], TOL, "dx")
