@@ -265,8 +265,8 @@ __global__ __launch_bounds__(norm_block(TPR), NCH == 1 ? 3 : TPR * NCH <= 512 ? 
       for (int i = 0; i < 8; ++i) {
         const float n = GF ? x[c][i] * g[c][i] * inv : x[c][i] * inv;
         const float e = GF ? d[c][i] * w[i] : d[c][i] * w[i] * g[c][i];
-        // (one value: as above)
-        const float dy = TPR == 16 && a.norm_w && a.n == 1 ? inv * inv * inv * a.eps * e : inv * fmaf(-n, k, e);
+        // (one value: as above; the epsilon first, as the cube of inv may overflow where it is 0)
+        const float dy = TPR == 16 && a.norm_w && a.n == 1 ? a.eps * inv * inv * inv * e : inv * fmaf(-n, k, e);
         dz[i] = (GF ? dy * x[c][i] : d[c][i] * w[i] * n) * h[c][i];
         x[c][i] = GF ? dy * g[c][i] : dy;
       }

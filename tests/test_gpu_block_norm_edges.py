@@ -95,3 +95,18 @@ def test_gradients_of_many_weight_rows(groups, n):
     assert set(g) == {"x", "norm_w"}
     check(np64(g["norm_w"]), r["norm_w"], TOL, "dnorm_w")
     check(np64(g["x"]), r["x"], TOL, "dx")
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_gradients_of_single_values(eps):
+    """A row of one value is normalised to its sign: without an epsilon its gradient is 0 at every size of value, and
+    with one eps / (y^2 + eps)^1.5."""
+    x = torch.tensor([3.0, -1e-3, 1e-14, -1e-18, 1e15], device=DEV).view(5, 1)
+    w, do = torch.full((1,), 1.5, device=DEV), torch.tensor([1.0, -2.0, 0.5, 1.0, 1.0], device=DEV).view(5, 1)
+    g = ssm.block_norm_bwd(x, norm_w=w, dout=do, eps=eps)
+    torch.cuda.synchronize()
+    y = np64(x)
+    # (eps as the kernel holds it, in 32 bits)
+    e = float(np.float32(eps))
+    check(np64(g["x"]), 1.5 * np64(do) * e / (y * y + e) ** 1.5 if eps else np.zeros((5, 1)), TOL, "dx")
+    check(np64(g["norm_w"]), (np64(do) * y / np.sqrt(y * y + e)).sum(0), TOL, "dnorm_w")
