@@ -499,7 +499,9 @@ ssm_status_t ssm_layer_check(const ssm_layer_params_t *p);
  * triangular system each, with matrix products throughout.  bf16 operands are
  * exact; 32-bit operands (f32 inputs, the state, u) enter the matrix cores as
  * three bf16 parts, so an f32 result carries f32 accuracy and a bf16 one is that
- * rounded once.
+ * rounded once.  A NaN or infinity in k, v, g (g = -inf apart) or beta of a token may
+ * reach the outputs of its whole chunk, earlier tokens included; other sequences are
+ * never reached.
  * Workspace: ssm_delta_chunk_workspace_size() bytes, 256-byte aligned (39.7 kB per
  * chunk and head and 49.2 kB per chunk and key head at K = 128 in bf16).
  * Supported: K <= 128, any V, x_dtype f32 or bf16, L == 0 copies the state.
@@ -692,10 +694,14 @@ size_t ssm_params_sizeof(int32_t which);
 /* Kernel timing for measurement tools.  start and stop are hipEvent_t handles
  * owned by the caller (both NULL switches timing off).  While set, each entry
  * point called on this thread records start on its stream right before the
- * launch of its main kernel (the full-segment scan kernel of ssm_scan_fwd, the
- * only kernel of the others) and stop right after it, so
- * hipEventElapsedTime(start, stop) is that kernel's duration.  The events are
- * only recorded, never created, synchronised or destroyed by the library. */
+ * launch of its main kernel and stop right after it, so
+ * hipEventElapsedTime(start, stop) is that kernel's duration.  Main kernels: the
+ * full-segment scan kernel of ssm_scan_fwd; the walk over the chunks of
+ * ssm_delta_chunk_fwd, without the kernel that forms its operands; the gradients'
+ * kernel of ssm_delta_chunk_bwd, without operands, walks and the sums of shared
+ * heads; the row kernel of ssm_block_norm_bwd, without the column sums; all of
+ * ssm_layer_fwd; the main or only kernel of the others.  The events are only
+ * recorded, never created, synchronised or destroyed by the library. */
 void ssm_set_timing_events(void *start, void *stop);
 
 /* ---- debug builds (SSM_DEBUG) ---------------------------------------------

@@ -84,8 +84,8 @@ __host__ __device__ inline int delta_vp(int V) { return (V + 31) / 32 * 32; }
 // Value channels per workgroup of the walks, in slices of 16: 32 once that still leaves
 // every CU a workgroup (the operands of T, P and the keys are then read half as often
 // and a chunk's three exchanges serve twice the work), else 16.  With 256 workgroups or
-// more at 32: packed call 415 us against 561, training walks 122 and 153 against 144
-// and 180; with fewer: prompt 268 us at 16 against 368.
+// more at 32: packed call 480 us against 609, training walks 120 and 154 against 140
+// and 179; with fewer: prompt 295 us at 16 against 443.
 inline int delta_nv(long groups, int V) { return groups * ((V + 31) / 32) >= 256 && V > 16 ? 2 : 1; }
 // Workgroups per (sequence, head), and of a walk (backward: the kept tiles are padded,
 // the slices cover delta_vp channels)

@@ -16,10 +16,11 @@
 // registers are free of the chunk before.
 //
 // Bound by a chunk's length in time where there is one workgroup per CU (8192 tokens,
-// 32 heads of 128: 128 chunks in 268 us, 2.1 us each; 510 us without reading ahead),
-// and by LDS (70 % busy) beside vector ALU and matrix cores (73 % of issue) where
-// there are many (12289 packed tokens, 80 heads, K 64, V 96: 415 us).  Training, 4 x
-// 2048 tokens, 16 heads of 128: 122 us forward, 153 us in reverse.
+// 32 heads of 128: 128 chunks in 295 us, 2.3 us each; reading ahead halved it), and by
+// vector ALU (43 % of the SIMD cycles) and matrix cores (29 %) at two waves per SIMD
+// where there are many (12289 packed tokens, 80 heads, K 64, V 96: 480 us; LDS 34 %
+// busy, 9 % more in bank conflicts).  Training, 4 x 2048 tokens, 16 heads of 128: 120 us
+// forward, 154 us in reverse.
 #include "delta_device.h"
 
 namespace ssm {
@@ -79,8 +80,7 @@ __device__ __forceinline__ void store_state4(float* s, long row, int d, int K, b
 }
 
 // A wave's tile (tokens t .. t + 3 = 16 w + 4 q .., channel r) as NP parts into the
-// operands' order, [part][step][lane] 16 bytes: reads are whole lines without bank
-// conflicts
+// operands' order, [part][step][lane] 16 bytes: reads are whole lines
 template <int NP>
 __device__ __forceinline__ void put_tile(uint16_t* dst, int r, int t, f32x4 v) {
   uint32_t a[NP], b[NP];

@@ -14,7 +14,7 @@
 //
 // Bound by latency (seven barriers and two substitutions' lengths a head) and by what
 // it writes, 39.7 kB per chunk and head.  12289 packed tokens, 80 heads on 8 key heads,
-// K 64: 211 us (573 MB written, 2.7 TB/s); 8192 tokens, 32 heads on 16, K 128: 80 us.
+// K 64: 222 us (671 MB written, 3.0 TB/s); 8192 tokens, 32 heads on 16, K 128: 83 us.
 #include "delta_device.h"
 
 namespace ssm {
@@ -337,8 +337,8 @@ __global__ __launch_bounds__(256, 2) void delta_prep_kernel(DeltaArgs a, int par
 
 // Workgroups per (chunk, key head): the value heads share the rows and their
 // products, so a workgroup takes as many (up to kHeads) as leave the GPU's CUs eight
-// workgroups each (five heads each at the packed call above 211 us, one 344 us; two
-// at the prompt 80 us, one 102 us).
+// workgroups each (five heads each at the packed call above 222 us, one 351 us; two
+// at the prompt 83 us, one 107 us).
 int head_parts(const DeltaArgs& a) {
   const long rep = a.h / a.hk, want = 8L * 256, have = a.slots * a.hk;
   const long parts = (want + have - 1) / have, least = (rep + kHeads - 1) / kHeads;
