@@ -45,6 +45,14 @@ ssm_status_t check_overlap(std::initializer_list<Range> outs, std::initializer_l
   return SSM_OK;
 }
 
+// Whether the last of `rows` rows lies past every address: no range is formed of such a
+// call, as its offsets would leave 63 bits.
+bool far_rows(int64_t rows, std::initializer_list<int64_t> strides) {
+  for (int64_t s : strides)
+    if (rows > 0 && s > (static_cast<int64_t>(1) << 58) / rows) return true;
+  return false;
+}
+
 // ---------------------------------------------------------------- gated delta rule
 
 // Sizes and strides shared by the three entry points; tokens: rows of q, k, v.
@@ -59,10 +67,12 @@ ssm_status_t delta_sizes(const P* p, long tokens) {
   if (!std::isfinite(p->scale)) return fail(SSM_ERR_INVALID_ARG, "scale must be finite");
   if (p->qk_norm && !(p->eps >= 0.0f && p->eps < INFINITY)) return fail(SSM_ERR_INVALID_ARG, "eps must be finite and not negative");
   const int64_t kw = static_cast<int64_t>(p->nkheads) * p->d_key, vw = static_cast<int64_t>(p->nheads) * p->d_value;
-  const int64_t most = static_cast<int64_t>(1) << 40;  // keeps every offset inside 63 bits
+  const int64_t most = static_cast<int64_t>(1) << 40;
   if ((p->q_stride && (p->q_stride < kw || p->q_stride > most)) || (p->k_stride && (p->k_stride < kw || p->k_stride > most)) ||
       (p->v_stride && (p->v_stride < vw || p->v_stride > most)))
     return fail(SSM_ERR_INVALID_ARG, "q_stride, k_stride or v_stride is shorter than a token's row (or beyond 2^40)");
+  if (far_rows(tokens, {p->q_stride, p->k_stride, p->v_stride}))
+    return fail(SSM_ERR_INVALID_ARG, "q_stride, k_stride or v_stride times the tokens is beyond 2^58");
   if (tokens > 0 && (!p->q || !p->k || !p->v || !p->g || !p->beta))
     return fail(SSM_ERR_INVALID_ARG, "q, k, v, g or beta is NULL");
   if (!aligned({p->q, p->k, p->v}, esize(p->x_dtype)) || !aligned({p->g, p->beta}, 4))
@@ -126,10 +136,19 @@ DeltaWs delta_ws(const P* p, bool bwd) {
   return w;
 }
 
+// A launch holds fewer than 2^32 threads: workgroups of 256, of 512 in the gradients of K > 64.
 template <typename P>
-bool delta_ws_fields(const P* p) {  // the fields the workspace size depends on are usable
-  return p->batch >= 0 && p->seqlen >= 0 && p->num_seqs >= 0 && p->nkheads > 0 && p->nheads > 0 && p->d_key > 0 &&
-         p->d_key <= ssm::kDeltaMaxK && p->d_value > 0 && valid_dtype(p->x_dtype);
+bool delta_too_many(const P* p, bool bwd) {
+  const long most = bwd && p->d_key > 64 ? 1L << 23 : 1L << 24;
+  const long groups = static_cast<long>(p->num_seqs) * p->nheads;
+  return delta_slots(p) > (most - 1) / p->nheads || ssm::delta_walk_blocks(groups, p->d_value, bwd) >= 1L << 24;
+}
+
+template <typename P>
+bool delta_ws_fields(const P* p, bool bwd) {  // the fields the workspace size depends on are usable
+  return p->batch >= 0 && p->seqlen >= 0 && p->num_seqs >= 0 && p->nkheads > 0 && p->nheads > 0 && p->nheads <= 65536 &&
+         p->d_key > 0 && p->d_key <= ssm::kDeltaMaxK && p->d_value > 0 && p->d_value <= 65536 && valid_dtype(p->x_dtype) &&
+         !delta_too_many(p, bwd);
 }
 
 // Everything but the outputs, common to forward and backward.
@@ -142,11 +161,7 @@ ssm_status_t delta_seq_check(const P* p, bool bwd) {
   if (p->cu_seqlens ? p->batch != 1 : p->num_seqs != p->batch)
     return fail(SSM_ERR_INVALID_ARG, "packed sequences need batch 1; without cu_seqlens num_seqs must equal batch");
   if (!aligned({p->cu_seqlens, p->state_in}, 4)) return fail(SSM_ERR_INVALID_ARG, "cu_seqlens or state_in is not 4-byte aligned");
-  const long slots = delta_slots(p);
-  const long groups = static_cast<long>(p->num_seqs) * p->nheads;
-  // a launch holds fewer than 2^32 threads: workgroups of 256, of 512 in the gradients of K > 64
-  if (slots * p->nheads >= (bwd && p->d_key > 64 ? 1L << 23 : 1L << 24) ||
-      ssm::delta_walk_blocks(groups, p->d_value, bwd) >= 1L << 24)
+  if (delta_too_many(p, bwd))
     return fail(SSM_ERR_UNSUPPORTED, "too many chunks, sequences and heads for one launch");
   const size_t need = delta_ws(p, bwd).total;
   if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return fail(SSM_ERR_WORKSPACE, "workspace is missing or too small");
@@ -270,6 +285,11 @@ ssm_status_t delta_step_check(const ssm_delta_decode_params_t* p) {
 // ---------------------------------------------------------------- block norm
 
 template <typename P>
+bool norm_too_many(const P* p) {  // rows of all groups
+  return p->rows > 0x7fffffffLL / (p->width / p->group_size);
+}
+
+template <typename P>
 ssm_status_t norm_check_common(const P* p) {
   if (p->rows < 0 || p->width <= 0 || p->group_size <= 0) return fail(SSM_ERR_INVALID_ARG, "rows is negative, or width or group_size not positive");
   if (p->width % p->group_size != 0) return fail(SSM_ERR_INVALID_ARG, "group_size must divide width");
@@ -284,7 +304,9 @@ ssm_status_t norm_check_common(const P* p) {
   const int64_t most = static_cast<int64_t>(1) << 40;
   if ((p->x_stride && (p->x_stride < p->width || p->x_stride > most)) || (p->z_stride && (p->z_stride < p->width || p->z_stride > most)))
     return fail(SSM_ERR_INVALID_ARG, "x_stride or z_stride is shorter than a row (or beyond 2^40)");
-  if (p->rows > 0x7fffffffLL / (p->width / p->group_size))
+  if (far_rows(p->rows, {p->x_stride, p->z_stride}))
+    return fail(SSM_ERR_INVALID_ARG, "x_stride or z_stride times the rows is beyond 2^58");
+  if (norm_too_many(p))
     return fail(SSM_ERR_UNSUPPORTED, "rows * (width / group_size) must be below 2^31");
   if (p->rows > 0 && !p->x) return fail(SSM_ERR_INVALID_ARG, "x is NULL");
   if (!aligned({p->x, p->z}, esize(p->x_dtype)) || !aligned({p->residual}, esize(p->res_dtype)) ||
@@ -398,7 +420,7 @@ ssm_status_t ssm_delta_chunk_check(const ssm_delta_chunk_params_t* p) {
 }
 
 size_t ssm_delta_chunk_workspace_size(const ssm_delta_chunk_params_t* p) {
-  if (!p || p->struct_size != sizeof(*p) || !delta_ws_fields(p)) return 0;
+  if (!p || p->struct_size != sizeof(*p) || !delta_ws_fields(p, false)) return 0;
   return delta_ws(p, false).total;
 }
 
@@ -423,7 +445,7 @@ ssm_status_t ssm_delta_chunk_bwd_check(const ssm_delta_chunk_bwd_params_t* p) {
 }
 
 size_t ssm_delta_chunk_bwd_workspace_size(const ssm_delta_chunk_bwd_params_t* p) {
-  if (!p || p->struct_size != sizeof(*p) || !delta_ws_fields(p)) return 0;
+  if (!p || p->struct_size != sizeof(*p) || !delta_ws_fields(p, true)) return 0;
   return delta_ws(p, true).total;
 }
 
@@ -508,7 +530,8 @@ ssm_status_t ssm_block_norm_bwd_check(const ssm_block_norm_bwd_params_t* p) {
 
 size_t ssm_block_norm_bwd_workspace_size(const ssm_block_norm_bwd_params_t* p) {
   if (!p || p->struct_size != sizeof(*p) || p->rows < 0 || p->width <= 0 || p->group_size <= 0 ||
-      p->width % p->group_size != 0 || p->group_size > ssm::kNormMax || norm_period(p) > ssm::kNormMaxPeriod)
+      p->width % p->group_size != 0 || p->group_size > ssm::kNormMax || norm_too_many(p) ||
+      norm_period(p) > ssm::kNormMaxPeriod)
     return 0;
   return norm_bwd_ws(p);
 }

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 from selective_state_space_03_amd import binding as b
-from test_delta_abi import L, _bwd, _fwd, _norm_bwd  # noqa: F401
+from test_delta_abi import L, _bwd, _fwd, _norm, _norm_bwd, _step  # noqa: F401
 
 MANY = dict(batch=1, cu_seqlens=1 << 50, workspace_bytes=1 << 62, workspace=1 << 55)
 
@@ -48,3 +48,42 @@ def test_weight_rows_of_the_norms_gradients(L):  # noqa: F811
         assert (L.ssm_block_norm_bwd_workspace_size(ctypes.byref(p)) > 0) == (status == 0)
         p.norm_w_len = 1  # one row shared by the groups
         assert L.ssm_block_norm_bwd_check(ctypes.byref(p)) == 0, L.ssm_last_error()
+
+
+BIG, FAR, LONG = (1 << 31) - 1, 1 << 40, (1 << 63) - 1
+
+
+def _sizes(L, p):  # noqa: F811
+    """Every function of the C ABI that only looks at the params."""
+    name = {b.DeltaChunkParams: "ssm_delta_chunk", b.DeltaChunkBwdParams: "ssm_delta_chunk_bwd",
+            b.DeltaDecodeParams: "ssm_delta_decode", b.BlockNormParams: "ssm_block_norm",
+            b.BlockNormBwdParams: "ssm_block_norm_bwd"}[type(p)]
+    size = getattr(L, name + "_workspace_size", None)
+    return getattr(L, name + "_check")(ctypes.byref(p)), size(ctypes.byref(p)) if size else None
+
+
+@pytest.mark.parametrize("make,kw", [
+    (_step, dict(batch=1 << 20, q_stride=FAR)), (_step, dict(batch=1 << 20, v_stride=FAR)),
+    (_fwd, dict(batch=1 << 10, num_seqs=1 << 10, seqlen=1 << 14, k_stride=FAR, workspace_bytes=1 << 62)),
+    (_bwd, dict(batch=1 << 10, num_seqs=1 << 10, seqlen=1 << 12, v_stride=FAR, workspace_bytes=1 << 62)),
+    (_norm, dict(rows=BIG, x_stride=FAR)), (_norm_bwd, dict(rows=BIG, z_stride=FAR))])
+def test_rows_past_the_address_space(L, make, kw):  # noqa: F811
+    """Rows whose last element no 64-bit offset reaches are refused before their range is formed."""
+    assert _sizes(L, make(**kw))[0] == 1
+    assert b"stride" in L.ssm_last_error()
+
+
+@pytest.mark.parametrize("make,kw", [
+    *[(m, kw) for m in (_fwd, _bwd) for kw in (
+        dict(d_value=BIG), dict(nheads=BIG - 1, nkheads=1), dict(batch=BIG, num_seqs=BIG, seqlen=BIG),
+        dict(batch=BIG, num_seqs=BIG, seqlen=BIG, nheads=65536, nkheads=65536, d_value=65536),
+        dict(batch=1, cu_seqlens=1 << 50, num_seqs=BIG, seqlen=BIG))],
+    (_step, dict(batch=BIG, nheads=65536, nkheads=65536, d_value=65536)), (_step, dict(nheads=BIG - 1, d_value=BIG)),
+    (_norm, dict(rows=LONG)), (_norm_bwd, dict(rows=LONG)),
+    (_norm_bwd, dict(rows=LONG, width=BIG, group_size=1, norm_w_len=BIG, residual=None, scale=None, out_norm_w=None)),
+    (_norm_bwd, dict(rows=1 << 31, width=2, group_size=1, norm_w_len=1, residual=None, scale=None, out_norm_w=None))])
+def test_extreme_sizes_are_refused_without_overflow(L, make, kw):  # noqa: F811
+    """The largest values of the fields: the checks refuse, and a workspace size for what they refuse is 0."""
+    status, size = _sizes(L, make(**kw))
+    assert status in (1, 2), L.ssm_last_error()
+    assert not size
