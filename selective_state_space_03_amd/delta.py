@@ -94,10 +94,16 @@ def _rows(t, name, shape, dtype, device):
     return t.data_ptr(), row
 
 
-def _zeros(shape, dtype, device, stream):
-    t = _empty(shape, dtype, device, stream)
-    with torch.cuda.stream(stream):  # (None: the current one)
-        return t.zero_()
+class _PackedGrads(Call):
+    """A backward call of packed sequences: tokens outside every one of them are not written by the library, so
+    each run clears their gradients first, on the call's stream (the offsets may have changed since the last)."""
+
+    def run(self):
+        clear = [self.out[name] for name in ("q", "k", "v", "g", "beta")]
+        with torch.cuda.stream(torch.cuda.ExternalStream(self._stream.value or 0, device=clear[0].device)):
+            for t in clear:
+                t.zero_()
+        return super().run()
 
 
 def _workspace(p, need, workspace, dev, stream):
@@ -164,7 +170,8 @@ def delta_chunk_bwd(q, k, v, g, beta, dout, *, scale=None, qk_norm=False, eps=1e
                     dstate_out=None, grad_dtype=None, workspace=None, stream=None, prepare=False):
     """Backward of delta_chunk_fwd (ssm_delta_chunk_bwd): the forward's inputs, dout (batch, L, H, V) in
     q's dtype and optionally the final state's gradient.  Returns a dict of gradients: q, k, v in
-    grad_dtype (fp32 unless given), g, beta and, where a state was given, state_in in fp32; or with
+    grad_dtype (fp32 unless given), g, beta and, where a state was given, state_in in fp32 (zeros for
+    tokens of no sequence); or with
     prepare=True a Call whose run() enqueues it again (its .out is that dict)."""
     L_ = lib()
     dev = _gpu(q, "q")
@@ -174,19 +181,18 @@ def delta_chunk_bwd(q, k, v, g, beta, dout, *, scale=None, qk_norm=False, eps=1e
     p.dstate_out = _arg(dstate_out, "dstate_out", shape, _F32, dev)
     gd = grad_dtype or _F32
     p.grad_dtype = _dtype(gd, "grad_dtype")
-    # tokens outside every packed sequence are not written: they start as zeros (on the call's stream)
-    make = _empty if cu_seqlens is None else _zeros
-    out = {"q": make(tuple(q.shape), gd, dev, stream), "k": make(tuple(k.shape), gd, dev, stream),
-           "v": make(tuple(v.shape), gd, dev, stream), "g": make(tuple(g.shape), _F32, dev, stream),
-           "beta": make(tuple(g.shape), _F32, dev, stream)}
+    out = {"q": _empty(tuple(q.shape), gd, dev, stream), "k": _empty(tuple(k.shape), gd, dev, stream),
+           "v": _empty(tuple(v.shape), gd, dev, stream), "g": _empty(tuple(g.shape), _F32, dev, stream),
+           "beta": _empty(tuple(g.shape), _F32, dev, stream)}
     if state_in is not None:
         out["state_in"] = _empty(shape, _F32, dev, stream)
     for name, field in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("beta", "dbeta"), ("state_in", "dstate_in")):
         if name in out and out[name].numel() > 0:
             setattr(p, field, out[name].data_ptr())
     workspace = _workspace(p, L_.ssm_delta_chunk_bwd_workspace_size(_byref(p)), workspace, dev, stream)
-    call = Call(L_.ssm_delta_chunk_bwd, p, _on(dev, stream), out, (q, k, v, g, beta, dout, cu_seqlens, state_in,
-                                                                      dstate_out, workspace))
+    kind = Call if cu_seqlens is None else _PackedGrads
+    call = kind(L_.ssm_delta_chunk_bwd, p, _on(dev, stream), out, (q, k, v, g, beta, dout, cu_seqlens, state_in,
+                                                                   dstate_out, workspace))
     return call if prepare else call.run()
 
 

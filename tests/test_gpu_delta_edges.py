@@ -70,3 +70,26 @@ def test_unit_rows_without_epsilon(dtype, L, cu, Hk):
     g, r = _grads(c, do, st, ds, cu, qk_norm=True, eps=0.0)
     for x in g:
         check(np64(g[x]), r[x], TOL, "d" + x)
+
+
+def test_prepared_packed_gradients_follow_the_offsets():
+    """A prepared backward call run again with other offsets in the same buffer: tokens that left the sequences have
+    zeros, not the gradients of the run before; so too in a graph that records the call."""
+    c, st, do, _ = _case(21, 1, 130, 1, 2, 32, 24, F32, seqs=2)
+    cu = torch.tensor([0, 50, 130], dtype=torch.int32, device=DEV)
+    call = ssm.delta_chunk_bwd(*_args(c), do, qk_norm=True, cu_seqlens=cu, state_in=st, prepare=True)
+    torch.cuda.synchronize()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=s):
+        rec = ssm.delta_chunk_bwd(*_args(c), do, qk_norm=True, cu_seqlens=cu, state_in=st, stream=s)
+    for off in ([0, 50, 130], [20, 60, 100], [0, 1, 64], [5, 5, 130]):
+        cu.copy_(torch.tensor(off, dtype=torch.int32))
+        graph.replay()
+        got = call.run()
+        want = ssm.delta_chunk_bwd(*_args(c), do, qk_norm=True, cu_seqlens=torch.tensor(off, dtype=torch.int32, device=DEV),
+                                   state_in=st)
+        torch.cuda.synchronize()
+        for x in want:
+            assert torch.equal(got[x], want[x]) and torch.equal(rec[x], want[x]), (off, x)
+        for x in NAMES:
+            assert not got[x][:, :off[0]].any() and not got[x][:, off[-1]:].any(), (off, x)
