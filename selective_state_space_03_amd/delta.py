@@ -53,6 +53,12 @@ def _gpu(t, name):
     return t.device
 
 
+def _fits(n, name, what):
+    """Sizes that the library holds in 31 bits: ctypes would cut a longer one without a word."""
+    if n > 0x7fffffff:
+        raise ValueError(f"{name} has {n} {what}, more than 2^31 - 1")
+
+
 def _dtype(d, name):
     if d not in _DT:
         raise TypeError(f"{name}: dtype {d} not supported (float32 or bfloat16)")
@@ -117,6 +123,7 @@ def _workspace(p, need, workspace, dev, stream):
 
 def _delta_inputs(p, q, k, v, g, beta, scale, qk_norm, eps, cu_seqlens, state_in):
     batch, seqlen, hk, dk = q.shape
+    _fits(max(batch, seqlen), "q", "sequences or tokens")
     h, dv = v.shape[2], v.shape[3]
     dev = q.device
     p.struct_size = ctypes.sizeof(type(p))
@@ -204,6 +211,7 @@ def delta_decode_step(q, k, v, g, beta, state, *, scale=None, qk_norm=False, eps
     L_ = lib()
     dev = _gpu(q, "q")
     batch, hk, dk = q.shape
+    _fits(batch, "q", "sequences")
     h, dv = v.shape[1], v.shape[2]
     p = DeltaDecodeParams()
     p.struct_size = ctypes.sizeof(DeltaDecodeParams)
@@ -228,6 +236,7 @@ def delta_decode_step(q, k, v, g, beta, state, *, scale=None, qk_norm=False, eps
 
 def _norm_inputs(p, x, norm_w, z, gate_first, residual, scale, out_norm_w, group_size, eps):
     dev, width = x.device, x.shape[-1]
+    _fits(width, "x", "values a row")
     shape = tuple(x.shape)
     rows = shape[0] if len(shape) == 2 else math.prod(shape[:-1])
     p.struct_size = ctypes.sizeof(type(p))

@@ -110,3 +110,11 @@ def test_gradients_of_single_values(eps):
     e = float(np.float32(eps))
     check(np64(g["x"]), 1.5 * np64(do) * e / (y * y + e) ** 1.5 if eps else np.zeros((5, 1)), TOL, "dx")
     check(np64(g["norm_w"]), (np64(do) * y / np.sqrt(y * y + e)).sum(0), TOL, "dnorm_w")
+
+
+def test_rows_past_31_bits_are_refused():
+    """2^32 + 64 values a row (of no memory here) are not taken for 64."""
+    x = torch.empty(1, 1, dtype=BF, device=DEV).expand(1, (1 << 32) + 64)
+    for call in (ssm.block_norm_fwd, ssm.block_norm_bwd):
+        with pytest.raises(ValueError, match="values a row, more than"):
+            call(x, group_size=64)

@@ -93,3 +93,19 @@ def test_prepared_packed_gradients_follow_the_offsets():
             assert torch.equal(got[x], want[x]) and torch.equal(rec[x], want[x]), (off, x)
         for x in NAMES:
             assert not got[x][:, :off[0]].any() and not got[x][:, off[-1]:].any(), (off, x)
+
+
+def test_sizes_past_31_bits_are_refused():
+    """2^32 + 64 tokens or sequences (of no memory here) are not taken for 64."""
+    n = (1 << 32) + 64
+    q, v = torch.empty(1, 1, 1, 8, device=DEV), torch.empty(1, 1, 1, 4, device=DEV)
+    g = torch.empty(1, 1, 1, device=DEV)
+    for dims in ((1, n), (n, 1)):
+        args = [t.expand(*dims, *t.shape[2:]) for t in (q, q, v, g, g)]
+        with pytest.raises(ValueError, match="tokens, more than"):
+            ssm.delta_chunk_fwd(*args)
+        with pytest.raises(ValueError, match="tokens, more than"):
+            ssm.delta_chunk_bwd(*args, args[2])
+    one = [t[0].expand(n, *t.shape[2:]) for t in (q, q, v, g, g)]
+    with pytest.raises(ValueError, match="sequences, more than"):
+        ssm.delta_decode_step(*one, torch.empty(1, 1, 4, 8, device=DEV).expand(n, 1, 4, 8))
