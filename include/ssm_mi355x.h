@@ -25,8 +25,10 @@
  *
  * Next to them: the multi-head scan's decode step, the scan's backward, the
  * layer's projections and the whole layer; the gated delta rule
- * (ssm_delta_chunk_fwd, ssm_delta_chunk_bwd, ssm_delta_decode_step) and the
- * norms before and after a block (ssm_block_norm_fwd, ssm_block_norm_bwd).
+ * (ssm_delta_chunk_fwd, ssm_delta_chunk_bwd, ssm_delta_decode_step), the
+ * norms before and after a block (ssm_block_norm_fwd, ssm_block_norm_bwd) and
+ * attention with a sliding window and sinks with its paged cache (ssm_attn_fwd,
+ * ssm_attn_bwd, ssm_attn_cache_write, ssm_attn_decode_step).
  *
  * Conventions shared by every entry point
  *  - Every tensor pointer is a DEVICE pointer owned by the caller.  The scan,
@@ -64,8 +66,9 @@ extern "C" {
 
 #define SSM_ABI_VERSION 2
 
-/* element types (int32 fields in the structs below) */
-typedef enum { SSM_F32 = 0, SSM_BF16 = 1 } ssm_dtype_t;
+/* element types (int32 fields in the structs below).  SSM_E4M3 (8 bits: sign, 4 of
+ * exponent, 3 of fraction, largest 448, no infinity) only for the attention's cache. */
+typedef enum { SSM_F32 = 0, SSM_BF16 = 1, SSM_E4M3 = 2 } ssm_dtype_t;
 
 /* How B is discretized.  SSM_EULER: dB u = dt B u (the "dB * x_t" of the
  * Axon-SSM page's kernel section and the dt[s] x[s] of the velog page's chunk
@@ -681,6 +684,167 @@ ssm_status_t ssm_block_norm_bwd(const ssm_block_norm_bwd_params_t *p, void *stre
 size_t ssm_block_norm_bwd_workspace_size(const ssm_block_norm_bwd_params_t *p);
 ssm_status_t ssm_block_norm_bwd_check(const ssm_block_norm_bwd_params_t *p);
 
+/* ------------------------------------------------------------------------
+ * Causal attention with a sliding window and sinks, over whole sequences.  The query
+ * at position p of its sequence sees the keys j <= p with j > p - window or j < sinks:
+ *   s_pj = scale q_p.k_j,  lse_p = log sum_j e^{s_pj},  o_p = sum_j e^{s_pj - lse_p} v_j
+ *   q         (Bt, L, H, D), k, v (Bt, Lk, Hk, D) x_dtype; head h reads key head
+ *             h / (H / Hk).  *_stride: elements from one token to the next (the same
+ *             across sequences), 0 for a dense tensor
+ *   L, Lk     with more keys than queries the queries are the sequence's last positions
+ *             (query i is at i + Lk - L); with fewer, the first see nothing
+ *   window    keys that a query sees at most besides the sinks, itself among them; 0: all
+ *   sinks     first keys of the sequence that stay visible behind the window
+ *   scale     finite, not negative
+ *   cu_seqlens (num_seqs + 1) int32 in DEVICE memory or NULL: packed sequences, Bt = 1,
+ *             sequence i holds the queries [cu[i], cu[i+1]); offsets rise from 0 to L (empty
+ *             sequences allowed).  They are not read on the host; offsets out of range are
+ *             clamped, queries outside every sequence are not written.  NULL: num_seqs = Bt
+ *   cu_seqlens_k  the same for the keys; NULL with cu_seqlens: the same offsets (L = Lk)
+ *   lse       (Bt, L, H) f32 or NULL; -infinity where a query sees nothing (o is zero there)
+ *   o         (Bt, L, H, D) o_dtype, dense
+ * Sums and the softmax's statistics are f32.  Scores are products of the inputs as they
+ * are; their exponentials enter the product with v in f32 for f32 inputs, in three bf16
+ * parts (24 bits) for bf16 inputs and an f32 o, in two (16 bits) for a bf16 o.
+ * A NaN or infinity in a row of v that a query does not see may reach it where another
+ * query of its tile of 128 sees that row; rows of other sequences never do.
+ * Workspace: ssm_attn_workspace_size() bytes, 256-byte aligned.
+ * Supported: D <= 128, x_dtype and o_dtype f32 or bf16, L and Lk up to 2^30; a launch's
+ * 2^32 threads bound the tiles of 64 queries times H to below 2^24.
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_attn_params {
+  uint32_t struct_size; /* = sizeof(ssm_attn_params_t) */
+  int32_t batch, seqlen, seqlen_k, num_seqs, nkheads, nheads, d_head;
+  const void *q, *k, *v;
+  int32_t x_dtype;
+  int64_t q_stride, k_stride, v_stride;
+  float scale;
+  int32_t window, sinks;
+  const int32_t *cu_seqlens, *cu_seqlens_k;
+  float *lse;
+  void *o;
+  int32_t o_dtype;
+  void *workspace;
+  size_t workspace_bytes;
+} ssm_attn_params_t;
+
+ssm_status_t ssm_attn_fwd(const ssm_attn_params_t *p, void *stream);
+size_t ssm_attn_workspace_size(const ssm_attn_params_t *p);
+ssm_status_t ssm_attn_check(const ssm_attn_params_t *p);
+
+/* ------------------------------------------------------------------------
+ * Backward of ssm_attn_fwd from its inputs and its results o and lse: given dout = dL/do
+ * (Bt, L, H, D) x_dtype, dense, writes dq (Bt, L, H, D), dk and dv (Bt, Lk, Hk, D) in
+ * grad_dtype, dense; any may be NULL:
+ *   P_pj = e^{s_pj - lse_p},  dS_pj = P_pj (dout_p.v_j - dout_p.o_p),
+ *   dq_p = scale sum_j dS_pj k_j,  dk_j = scale sum_p dS_pj q_p,  dv_j = sum_p P_pj dout_p
+ * Key heads shared by several heads receive the sum over them.  Sums are taken in a
+ * fixed order, without atomics: results repeat bit for bit.  dout_p.o_p comes from o as
+ * it is given: an o in bf16 moves dS_pj by P_pj |dout_p||o_p| 2^-9 at most, one in f32
+ * does not.  P and dS enter their products as they do in the forward (grad_dtype in the
+ * place of o_dtype).  Queries and keys outside every sequence are not written.
+ * Workspace: ssm_attn_bwd_workspace_size() bytes, 256-byte aligned.
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_attn_bwd_params {
+  uint32_t struct_size; /* = sizeof(ssm_attn_bwd_params_t) */
+  int32_t batch, seqlen, seqlen_k, num_seqs, nkheads, nheads, d_head;
+  const void *q, *k, *v;
+  int32_t x_dtype;
+  int64_t q_stride, k_stride, v_stride;
+  float scale;
+  int32_t window, sinks;
+  const int32_t *cu_seqlens, *cu_seqlens_k;
+  const float *lse;
+  const void *o;
+  int32_t o_dtype;
+  const void *dout;
+  void *dq, *dk, *dv;
+  int32_t grad_dtype;
+  void *workspace;
+  size_t workspace_bytes;
+} ssm_attn_bwd_params_t;
+
+ssm_status_t ssm_attn_bwd(const ssm_attn_bwd_params_t *p, void *stream);
+size_t ssm_attn_bwd_workspace_size(const ssm_attn_bwd_params_t *p);
+ssm_status_t ssm_attn_bwd_check(const ssm_attn_bwd_params_t *p);
+
+/* ------------------------------------------------------------------------
+ * The attention's cache lies in pages, in a pool (pages, Hk, page_size, D) for the keys
+ * and one for the values, in f32, bf16 or SSM_E4M3; the token at position j of a sequence
+ * is row j % page_size of page page_table[sequence][j / page_size].  A cache in SSM_E4M3
+ * has a scale (pages, Hk) f32 beside each pool: a code c stands for c scale.
+ *
+ * ssm_attn_cache_write puts new tokens behind the lens[i] that sequence i holds:
+ *   k, v      (Bt, L, Hk, D) x_dtype; *_stride elements from one token to the next (0:
+ *             dense).  cu_seqlens as in ssm_attn_fwd, or NULL: L tokens of each of the
+ *             num_seqs = Bt sequences
+ *   lens      (num_seqs) int32 in DEVICE memory: tokens held before the call (not changed)
+ *   page_table (num_seqs, table_rows) int32 in DEVICE memory.  Tokens whose page is not in
+ *             [0, pages), or past the table, are not written: pages that no query sees any
+ *             more may be given back and their entries set to -1
+ *   cache_dtype  x_dtype, or SSM_E4M3
+ * Scales are powers of two: for a page and head the least s with |x| <= 448 s for every
+ * finite value put there (2^-100 at least); a page that holds tokens already keeps its
+ * scale or takes a larger one, and its codes are put to that (exactly, but for codes that
+ * become subnormal, which are rounded again).  Values are rounded to nearest even;
+ * infinities and NaN become NaN.  Rows that no token is put to keep their contents.
+ * Pages that the call writes to belong to one sequence.
+ * Supported: D <= 128; page_size up to 65536, table_rows * page_size up to 2^30; the pages
+ * met (at most tokens / page_size + 2 num_seqs) times Hk below 2^24.
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_attn_cache_params {
+  uint32_t struct_size; /* = sizeof(ssm_attn_cache_params_t) */
+  int32_t batch, seqlen, num_seqs, nkheads, d_head;
+  const void *k, *v;
+  int32_t x_dtype;
+  int64_t k_stride, v_stride;
+  const int32_t *cu_seqlens, *lens, *page_table;
+  int32_t table_rows, pages, page_size;
+  void *k_cache, *v_cache;
+  int32_t cache_dtype;
+  float *k_scale, *v_scale;
+} ssm_attn_cache_params_t;
+
+ssm_status_t ssm_attn_cache_write(const ssm_attn_cache_params_t *p, void *stream);
+ssm_status_t ssm_attn_cache_check(const ssm_attn_cache_params_t *p);
+
+/* ------------------------------------------------------------------------
+ * One query of each of Bt sequences over its pages (the cache as above):
+ *   q (Bt, H, D) x_dtype with q_stride elements from one sequence to the next (0: dense);
+ *   lens (Bt) int32: tokens that the sequence holds, the query's own among them (the query
+ *   is at position lens - 1; 0: o is zero); o (Bt, H, D) o_dtype, dense.
+ * window, sinks and scale as in ssm_attn_fwd.  Entries of page_table that no visible key
+ * needs are not read; keys whose page is not in [0, pages) are left out.  A lens past the
+ * table counts as table_rows * page_size.  The result equals the last row of ssm_attn_fwd
+ * over the values that the cache stands for.
+ * cache_dtype: x_dtype, or SSM_E4M3, or bf16 beside an f32 x_dtype.
+ * Workspace: ssm_attn_decode_workspace_size() bytes, 256-byte aligned.
+ * Supported: D <= 128; Bt * H below 2^24; page_size up to 65536, table_rows * page_size up
+ * to 2^30.
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_attn_decode_params {
+  uint32_t struct_size; /* = sizeof(ssm_attn_decode_params_t) */
+  int32_t batch, nkheads, nheads, d_head;
+  const void *q;
+  int32_t x_dtype;
+  int64_t q_stride;
+  const void *k_cache, *v_cache;
+  int32_t cache_dtype;
+  const float *k_scale, *v_scale;
+  const int32_t *page_table, *lens;
+  int32_t table_rows, pages, page_size;
+  float scale;
+  int32_t window, sinks;
+  void *o;
+  int32_t o_dtype;
+  void *workspace;
+  size_t workspace_bytes;
+} ssm_attn_decode_params_t;
+
+ssm_status_t ssm_attn_decode_step(const ssm_attn_decode_params_t *p, void *stream);
+size_t ssm_attn_decode_workspace_size(const ssm_attn_decode_params_t *p);
+ssm_status_t ssm_attn_decode_check(const ssm_attn_decode_params_t *p);
+
 /* ------------------------------------------------------------------------ */
 const char *ssm_status_string(int32_t status);
 /* Detail of the last non-OK return on the calling thread ("" if none). */
@@ -688,7 +852,8 @@ const char *ssm_last_error(void);
 int32_t ssm_abi_version(void);
 /* sizeof of a params struct: which = 0 scan, 1 decode, 2 chunk, 3 chunk
  * decode, 4 linear, 5 layer, 6 scan backward, 8 delta chunk, 9 delta chunk
- * backward, 10 delta decode, 11 block norm, 12 block norm backward; 0 otherwise. */
+ * backward, 10 delta decode, 11 block norm, 12 block norm backward, 13 attention,
+ * 14 attention backward, 15 attention cache, 16 attention decode; 0 otherwise. */
 size_t ssm_params_sizeof(int32_t which);
 
 /* Kernel timing for measurement tools.  start and stop are hipEvent_t handles

@@ -1,8 +1,15 @@
 """MI355X (gfx950) selective-scan hot path: fused prefill scan, in-place decode
 step, multi-head chunked scan and its in-place decode step, the gated delta rule
-(chunked, backward, decode step) and the block norm, as hand-written HIP kernels
-behind the C ABI of include/ssm_mi355x.h.  This package is the thin Python
+(chunked, backward, decode step), the block norm, and attention with a sliding
+window and sinks (whole sequences, backward, paged cache of 8, 16 or 32 bits,
+decode step), as hand-written HIP kernels behind the C ABI of include/ssm_mi355x.h.  This package is the thin Python
 binding."""
+from .attn import (  # noqa: F401
+    attn_bwd,
+    attn_cache_write,
+    attn_decode_step,
+    attn_fwd,
+)
 from .binding import (  # noqa: F401
     EXPORTED,
     Call,

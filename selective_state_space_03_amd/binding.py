@@ -18,7 +18,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # one of build_sanitized.py, for the CPU-side checks)
 LIB_PATH = os.environ.get("SSM_MI355X_LIB") or os.path.join(_HERE, "libssm_mi355x.so")
 
-SSM_F32, SSM_BF16 = 0, 1
+SSM_F32, SSM_BF16, SSM_E4M3 = 0, 1, 2
 # time_split value of the blocked single-pass scan (SSM_SCAN_BLOCKED in the header)
 SCAN_BLOCKED = -1
 STATUS = {0: "SSM_OK", 1: "SSM_ERR_INVALID_ARG", 2: "SSM_ERR_UNSUPPORTED", 3: "SSM_ERR_WORKSPACE", 4: "SSM_ERR_HIP",
@@ -159,6 +159,44 @@ class BlockNormBwdParams(ctypes.Structure):
     ]
 
 
+_ATTN_HEAD = [
+    ("struct_size", ctypes.c_uint32), ("batch", _i32), ("seqlen", _i32), ("seqlen_k", _i32), ("num_seqs", _i32),
+    ("nkheads", _i32), ("nheads", _i32), ("d_head", _i32), ("q", _vp), ("k", _vp), ("v", _vp), ("x_dtype", _i32),
+    ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("scale", _f32), ("window", _i32), ("sinks", _i32),
+    ("cu_seqlens", _vp), ("cu_seqlens_k", _vp), ("lse", _vp), ("o", _vp), ("o_dtype", _i32),
+]
+
+
+class AttnParams(ctypes.Structure):
+    _fields_ = _ATTN_HEAD + [("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class AttnBwdParams(ctypes.Structure):
+    _fields_ = _ATTN_HEAD + [
+        ("dout", _vp), ("dq", _vp), ("dk", _vp), ("dv", _vp), ("grad_dtype", _i32), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class AttnCacheParams(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("batch", _i32), ("seqlen", _i32), ("num_seqs", _i32), ("nkheads", _i32),
+        ("d_head", _i32), ("k", _vp), ("v", _vp), ("x_dtype", _i32), ("k_stride", _i64), ("v_stride", _i64),
+        ("cu_seqlens", _vp), ("lens", _vp), ("page_table", _vp), ("table_rows", _i32), ("pages", _i32),
+        ("page_size", _i32), ("k_cache", _vp), ("v_cache", _vp), ("cache_dtype", _i32), ("k_scale", _vp), ("v_scale", _vp),
+    ]
+
+
+class AttnDecodeParams(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("batch", _i32), ("nkheads", _i32), ("nheads", _i32), ("d_head", _i32),
+        ("q", _vp), ("x_dtype", _i32), ("q_stride", _i64), ("k_cache", _vp), ("v_cache", _vp), ("cache_dtype", _i32),
+        ("k_scale", _vp), ("v_scale", _vp), ("page_table", _vp), ("lens", _vp), ("table_rows", _i32), ("pages", _i32),
+        ("page_size", _i32), ("scale", _f32), ("window", _i32), ("sinks", _i32), ("o", _vp), ("o_dtype", _i32),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 # entry points of the gated delta rule and the block norm: (name, params, has a workspace size)
 _DELTA_ENTRIES = [
     ("ssm_delta_chunk_fwd", "ssm_delta_chunk", DeltaChunkParams, True),
@@ -166,6 +204,13 @@ _DELTA_ENTRIES = [
     ("ssm_delta_decode_step", "ssm_delta_decode", DeltaDecodeParams, False),
     ("ssm_block_norm_fwd", "ssm_block_norm", BlockNormParams, False),
     ("ssm_block_norm_bwd", "ssm_block_norm_bwd", BlockNormBwdParams, True),
+]
+# the same of the window attention and its cache
+_ATTN_ENTRIES = [
+    ("ssm_attn_fwd", "ssm_attn", AttnParams, True),
+    ("ssm_attn_bwd", "ssm_attn_bwd", AttnBwdParams, True),
+    ("ssm_attn_cache_write", "ssm_attn_cache", AttnCacheParams, False),
+    ("ssm_attn_decode_step", "ssm_attn_decode", AttnDecodeParams, True),
 ]
 
 EXPORTED = [
@@ -181,6 +226,10 @@ EXPORTED = [
     "ssm_delta_decode_step", "ssm_delta_decode_check",
     "ssm_block_norm_fwd", "ssm_block_norm_check",
     "ssm_block_norm_bwd", "ssm_block_norm_bwd_workspace_size", "ssm_block_norm_bwd_check",
+    "ssm_attn_fwd", "ssm_attn_workspace_size", "ssm_attn_check",
+    "ssm_attn_bwd", "ssm_attn_bwd_workspace_size", "ssm_attn_bwd_check",
+    "ssm_attn_cache_write", "ssm_attn_cache_check",
+    "ssm_attn_decode_step", "ssm_attn_decode_workspace_size", "ssm_attn_decode_check",
     "ssm_status_string", "ssm_last_error", "ssm_abi_version", "ssm_params_sizeof", "ssm_set_timing_events",
     "ssm_debug_checks", "ssm_debug_check_scan", "ssm_debug_check_chunk", "ssm_debug_check_scan_bwd",
 ]
@@ -243,7 +292,7 @@ def load(path) -> ctypes.CDLL:
     L.ssm_scan_bwd_workspace_size.restype = ctypes.c_size_t
     L.ssm_scan_bwd_check.argtypes = [ctypes.POINTER(ScanBwdParams)]
     L.ssm_scan_bwd_check.restype = _i32
-    for run, base, st, sized in _DELTA_ENTRIES:
+    for run, base, st, sized in _DELTA_ENTRIES + _ATTN_ENTRIES:
         ptr = ctypes.POINTER(st)
         getattr(L, run).argtypes, getattr(L, run).restype = [ptr, _vp], _i32
         getattr(L, base + "_check").argtypes, getattr(L, base + "_check").restype = [ptr], _i32
@@ -272,7 +321,7 @@ def load(path) -> ctypes.CDLL:
                             ScanBwdParams)):
         if L.ssm_params_sizeof(i) != ctypes.sizeof(st):
             raise RuntimeError(f"ctypes mirror of params struct {i} does not match the library")
-    for i, (_, _, st, _) in enumerate(_DELTA_ENTRIES):
+    for i, (_, _, st, _) in enumerate(_DELTA_ENTRIES + _ATTN_ENTRIES):
         if L.ssm_params_sizeof(8 + i) != ctypes.sizeof(st):
             raise RuntimeError(f"ctypes mirror of params struct {8 + i} does not match the library")
     return L

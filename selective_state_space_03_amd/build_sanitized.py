@@ -1,5 +1,5 @@
 """A host-sanitized build of the library for the CPU-side checks: the C-ABI
-layer (api.cpp and delta_api.cpp: argument validation, workspace sizing,
+layer (api.cpp, delta_api.cpp and attn_api.cpp: argument validation, workspace sizing,
 dispatch, and the SSM_DEBUG launch-plan checks) compiled with AddressSanitizer and
 UndefinedBehaviorSanitizer on the host side only, linked with the kernels'
 objects of the regular build (build.py, which must have run first).  Device
@@ -21,7 +21,7 @@ ASAN_DIR = os.path.join(b.BUILD, "asan")
 ASAN_LIB = os.path.join(ASAN_DIR, "libssm_mi355x_hostsan.so")
 LLVM_BIN = "/opt/rocm/lib/llvm/bin"
 HOST_SAN = ["address", "undefined"]
-HOST_SOURCES = ["api.cpp", "delta_api.cpp"]
+HOST_SOURCES = ["api.cpp", "delta_api.cpp", "attn_api.cpp"]
 
 
 def asan_runtime() -> str:

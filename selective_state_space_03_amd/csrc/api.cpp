@@ -1306,6 +1306,10 @@ size_t ssm_params_sizeof(int32_t which) {
     case 10: return sizeof(ssm_delta_decode_params_t);
     case 11: return sizeof(ssm_block_norm_params_t);
     case 12: return sizeof(ssm_block_norm_bwd_params_t);
+    case 13: return sizeof(ssm_attn_params_t);
+    case 14: return sizeof(ssm_attn_bwd_params_t);
+    case 15: return sizeof(ssm_attn_cache_params_t);
+    case 16: return sizeof(ssm_attn_decode_params_t);
     default: return 0;
   }
 }

@@ -1,0 +1,44 @@
+"""The window attention's binding on the CPU: what it refuses before the library is called.  The library is a stub
+here that fails the test when an entry point is reached."""
+import types
+
+import pytest
+import torch
+
+import selective_state_space_03_amd as ssm
+from selective_state_space_03_amd import attn
+
+
+class _Stub:
+    """Workspace sizes are answered, entry points must not be reached."""
+
+    def __getattr__(self, name):
+        if name.endswith("_workspace_size"):
+            return lambda p: 256
+        return lambda *a: pytest.fail(f"{name} reached with host tensors")
+
+
+STREAM = types.SimpleNamespace(cuda_stream=0)
+Q, K = torch.zeros(1, 3, 2, 8), torch.zeros(1, 3, 1, 8)
+CACHE, TABLE, LENS = torch.zeros(4, 1, 2, 8), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+CALLS = {
+    "fwd": lambda: ssm.attn_fwd(Q, K, K, o=Q.clone(), workspace=torch.zeros(256), stream=STREAM),
+    "bwd": lambda: ssm.attn_bwd(Q, K, K, Q, torch.zeros(1, 3, 2), Q, workspace=torch.zeros(256), stream=STREAM),
+    "write": lambda: ssm.attn_cache_write(K.transpose(0, 1), K.transpose(0, 1), CACHE, CACHE.clone(), TABLE, LENS, stream=STREAM),
+    "step": lambda: ssm.attn_decode_step(Q[0], CACHE, CACHE, TABLE, LENS, o=Q[0].clone(), workspace=torch.zeros(256), stream=STREAM),
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_host_tensors_are_refused(name, monkeypatch):
+    """Every argument on the host, with the outputs and the stream given: a ValueError, as from the other entry
+    points, and nothing is launched on host addresses."""
+    monkeypatch.setattr(attn, "lib", _Stub)
+    with pytest.raises(ValueError, match="must be a GPU tensor"):
+        CALLS[name]()
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (-3, 0), (5, -1), (2 ** 31, 0)])
+def test_masks_out_of_range_are_refused(window, sinks):
+    with pytest.raises(ValueError, match="window|sinks"):
+        attn._mask(ssm.binding.AttnParams(), window, sinks, None, 8)
