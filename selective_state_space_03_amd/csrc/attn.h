@@ -78,10 +78,12 @@ struct AttnStepArgs {
   int batch, h, hk, D, table_rows, pages, page;
   int window, sinks;
   float scale;
-  int vec;                            // rows of 16-byte groups of q, of 8 elements of the cache, aligned
+  int q_vec, vec;                     // rows of q and of the cache: 16-byte groups (2), 8-byte groups (1), any (0)
+  int page_shift;                     // log2(page), or -1
   int nsplit, chunk;                  // parts of a sequence's visible keys, keys in one
   void* o;                            // (batch, h, D)
-  float* part;                        // (batch, h, nsplit, D + 2): sums, then maximum and sum of the softmax
+  float* part;                        // (batch, h, nsplit, attn_dq(D)): the parts' sums of P v
+  float* part_stat;                   // (batch, h, nsplit, 2): maximum and sum of their softmax
 };
 struct AttnStepLaunch {
   AttnStepArgs a;
