@@ -78,7 +78,8 @@ int vec_of(int32_t d, int32_t dtype, std::initializer_list<int64_t> strides, std
   for (int v = 2; v > 0; --v) {
     const int64_t b = v == 2 ? 16 : 8, e = static_cast<int64_t>(esize(dtype));
     bool fits = d * e % b == 0 && aligned(ps, 16);
-    for (int64_t s : strides) fits = fits && s * e % b == 0;
+    // (a tile's rows are addressed in 31 bits)
+    for (int64_t s : strides) fits = fits && s * e % b == 0 && (v == 1 || s <= 1 << 22);
     if (fits) return v;
   }
   return 0;

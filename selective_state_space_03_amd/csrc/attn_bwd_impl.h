@@ -14,14 +14,13 @@ namespace ssm {
 
 __device__ __forceinline__ float attn_lse2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
-template <typename T, int DQ, int MT, int NP>
+template <typename T, int DQ, int MT, int NP, bool VEC>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
   using E = AttnEl<T>;
   constexpr int BN = E::kTile, KS = DQ / E::kUnit, NT = DQ / 16, BM = 64 * MT;
   constexpr int PU = sizeof(T) == 2 ? 2 : 1, UN = BN / 16 / PU;
-  using KTile = AttnTile<T, BN, DQ, 32>;
-  using VTile = AttnTile<T, BN, DQ, 16>;
-  __shared__ __align__(16) unsigned char lds[2][KTile::kBytes + VTile::kBytes];
+  using Tile = AttnTile<T, BN, DQ, VEC>;
+  __shared__ __align__(16) unsigned char lds[2][2 * Tile::kBytes];  // keys, values
 
   const AttnWork w = attn_work(a, blockIdx.x, BM, false, a.h / a.hk);
   if (w.tile < 0) return;
@@ -72,24 +71,35 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
   const int p0 = off + i0, p1 = p0 + 16 * MT - 1;
   const bool lone_all = a.window == 1 && a.sinks == 0;
 
-  uint4 kr[KTile::kPer], vr[VTile::kPer];
-  if (n > 0) {
-    const int j0 = ns > 0 ? 0 : first * BN;
-    KTile::fetch(kb, a.k_stride, j0, sq.nk, a.D, a.vec, kr);
-    VTile::fetch(vb, a.v_stride, j0, sq.nk, a.D, a.vec, vr);
-    KTile::put(lds[0], kr);
-    VTile::put(lds[0] + KTile::kBytes, vr);
-  }
-  lds_barrier();
-  for (int t = 0; t < n; ++t) {
-    const int j0 = (t < ns ? t : t - ns + first) * BN;
-    if (t + 1 < n) {
-      const int j1 = (t + 1 < ns ? t + 1 : t + 1 - ns + first) * BN;
-      KTile::fetch(kb, a.k_stride, j1, sq.nk, a.D, a.vec, kr);
-      VTile::fetch(vb, a.v_stride, j1, sq.nk, a.D, a.vec, vr);
+  uint4 kr[VEC ? 1 : Tile::kPer], vr[VEC ? 1 : Tile::kPer];
+  const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
+  const auto key = [&](int t) { return (t < ns ? t : t - ns + first) * BN; };  // first key of tile t
+  const auto load = [&](int t) {
+    if constexpr (VEC) {
+      Tile::load(lds[t & 1], ks, kb, a.k_stride, key(t), sq.nk, a.D);
+      Tile::load(lds[t & 1] + Tile::kBytes, vs, vb, a.v_stride, key(t), sq.nk, a.D);
+    } else {
+      Tile::fetch(kb, a.k_stride, key(t), sq.nk, a.D, a.vec, kr);
+      Tile::fetch(vb, a.v_stride, key(t), sq.nk, a.D, a.vec, vr);
     }
+  };
+  const auto put = [&](int t) {
+    if constexpr (!VEC) {
+      Tile::put(lds[t & 1], kr);
+      Tile::put(lds[t & 1] + Tile::kBytes, vr);
+    }
+  };
+  if (n > 0) {
+    load(0);
+    put(0);
+  }
+  for (int t = 0; t < n; ++t) {
+    if constexpr (VEC) loads_done();
+    lds_barrier();  // tile t is there, and nobody reads the tile before it any more
+    if (t + 1 < n) load(t + 1);
+    const int j0 = key(t);
     const unsigned char* const kl = lds[t & 1];
-    const unsigned char* const vl = kl + KTile::kBytes;
+    const unsigned char* const vl = kl + Tile::kBytes;
     const bool some = j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - a.window || j0 < a.sinks);
     if (some) {
       const bool whole = j0 + BN - 1 <= p0 && (j0 > p1 - a.window || j0 + BN <= a.sinks);
@@ -104,8 +114,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
         for (int x = 0; x < KS; ++x)
 #pragma unroll
           for (int e = 0; e < PU; ++e) {
-            const uint4 kf = KTile::rows(kl, 16 * (PU * u + e), x, lane);
-            const uint4 vf = VTile::rows(vl, 16 * (PU * u + e), x, lane);
+            const uint4 kf = Tile::rows(kl, 16 * (PU * u + e), x, lane);
+            const uint4 vf = Tile::rows(vl, 16 * (PU * u + e), x, lane);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
               s[m][e] = attn_mma<T>(kf, q[m][x], s[m][e]);
@@ -134,7 +144,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
         }
 #pragma unroll
         for (int d = 0; d < NT; ++d) {
-          const uint4 x = KTile::cols(kl, 16 * PU * u, 16 * d, lane);
+          const uint4 x = Tile::cols(kl, 16 * PU * u, 16 * d, lane);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -142,11 +152,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
         }
       }
     }
-    if (t + 1 < n) {
-      KTile::put(lds[(t + 1) & 1], kr);
-      VTile::put(lds[(t + 1) & 1] + KTile::kBytes, vr);
-    }
-    lds_barrier();
+    if (t + 1 < n) put(t + 1);
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -165,12 +171,12 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
 // The tiles that hold sinks are seen by every later query.  Where they are few (a.sink_tiles), the queries
 // are cut into pieces of a.span for them, the first workgroups of the launch, whose partial sums
 // attn_sink_kernel adds up.
-template <typename T, int DQ, int MT, int NP>
+template <typename T, int DQ, int MT, int NP, bool VEC>
 __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsigned sink_blocks) {
   using E = AttnEl<T>;
   constexpr int BN = E::kTile, KS = DQ / E::kUnit, NT = DQ / 16, BM = 64 * MT;
   constexpr int PU = sizeof(T) == 2 ? 2 : 1, UN = BN / 16 / PU;
-  using Tile = AttnTile<T, BN, DQ, 32>;
+  using Tile = AttnTile<T, BN, DQ, VEC>;
   __shared__ __align__(16) unsigned char lds[2][2 * Tile::kBytes + 8 * BN];
 
   const int heads = a.h / a.hk;
@@ -238,12 +244,21 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
   const float cs = a.scale * kLog2e;
   const bool lone_all = a.window == 1 && a.sinks == 0;
 
-  uint4 qr[Tile::kPer], dr[Tile::kPer];
+  uint4 qr[VEC ? 1 : Tile::kPer], dr[VEC ? 1 : Tile::kPer];
   float st = 0.0f;
-  const auto fetch = [&](int t) {
+  const long dstride = static_cast<long>(a.h) * a.D;
+  const typename Tile::Source qs = Tile::source(a.q_stride, a.D), ds = Tile::source(dstride, a.D);
+  const auto load = [&](int t) {
     const int head = kh * heads + t / per, i0 = (first + t % per) * BN;
-    Tile::fetch(static_cast<const T*>(a.q) + sq.q0 * a.q_stride + static_cast<long>(head) * a.D, a.q_stride, i0, sq.nq, a.D, a.vec, qr);
-    Tile::fetch(static_cast<const T*>(a.dout) + (sq.q0 * a.h + head) * a.D, static_cast<long>(a.h) * a.D, i0, sq.nq, a.D, a.vec, dr);
+    const T* const qb = static_cast<const T*>(a.q) + sq.q0 * a.q_stride + static_cast<long>(head) * a.D;
+    const T* const db = static_cast<const T*>(a.dout) + (sq.q0 * a.h + head) * a.D;
+    if constexpr (VEC) {
+      Tile::load(lds[t & 1], qs, qb, a.q_stride, i0, sq.nq, a.D);
+      Tile::load(lds[t & 1] + Tile::kBytes, ds, db, dstride, i0, sq.nq, a.D);
+    } else {
+      Tile::fetch(qb, a.q_stride, i0, sq.nq, a.D, a.vec, qr);
+      Tile::fetch(db, dstride, i0, sq.nq, a.D, a.vec, dr);
+    }
     if (threadIdx.x < 2 * BN) {  // lse, then delta
       const int i = i0 + threadIdx.x % BN;
       const long row = (sq.q0 + i) * a.h + head;
@@ -251,18 +266,22 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
       if (i < sq.nq) st = threadIdx.x < BN ? attn_lse2(a.lse[row]) : a.delta[row];
     }
   };
-  const auto put = [&](unsigned char* to) {
-    Tile::put(to, qr);
-    Tile::put(to + Tile::kBytes, dr);
+  const auto put = [&](int t) {
+    unsigned char* const to = lds[t & 1];
+    if constexpr (!VEC) {
+      Tile::put(to, qr);
+      Tile::put(to + Tile::kBytes, dr);
+    }
     if (threadIdx.x < 2 * BN) reinterpret_cast<float*>(to + 2 * Tile::kBytes)[threadIdx.x] = st;
   };
   if (n > 0) {
-    fetch(0);
-    put(lds[0]);
+    load(0);
+    put(0);
   }
-  lds_barrier();
   for (int t = 0; t < n; ++t) {
-    if (t + 1 < n) fetch(t + 1);
+    if constexpr (VEC) loads_done();
+    lds_barrier();
+    if (t + 1 < n) load(t + 1);
     const unsigned char* const ql = lds[t & 1];
     const unsigned char* const dl = ql + Tile::kBytes;
     const float* const sl = reinterpret_cast<const float*>(ql + 2 * Tile::kBytes);
@@ -332,8 +351,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
         }
       }
     }
-    if (t + 1 < n) put(lds[(t + 1) & 1]);
-    lds_barrier();
+    if (t + 1 < n) put(t + 1);
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -355,12 +373,12 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
   }
 }
 
-template <typename T, int DQ, int MT, int NP>
+template <typename T, int DQ, int MT, int NP, bool VEC>
 hipError_t attn_bwd_go(const AttnLaunch& l, hipStream_t s) {
   const AttnArgs& a = l.a;
   if (a.dq && a.rows_q > 0) {
     const long blocks = attn_tiles(a, 64 * MT, false) * a.h;
-    hipLaunchKernelGGL((attn_dq_kernel<T, DQ, MT, NP>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attn_dq_kernel<T, DQ, MT, NP, VEC>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -368,21 +386,25 @@ hipError_t attn_bwd_go(const AttnLaunch& l, hipStream_t s) {
   const long sinks = a.sink_tiles > 0 ? attn_pieces(a) * a.hk * a.sink_tiles : 0;
   const long blocks = sinks + attn_tiles(a, 64, true) * a.hk;
   hipError_t e = timed_launch(s, [&] {
-    hipLaunchKernelGGL((attn_dkv_kernel<T, DQ, 1, NP>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a,
+    hipLaunchKernelGGL((attn_dkv_kernel<T, DQ, 1, NP, VEC>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a,
                        static_cast<unsigned>(sinks));
   });
   if (e == hipSuccess && a.sink_tiles > 0) e = launch_attn_sinks(a, s);
   return e;
 }
 
+template <typename T, int MT, int NP, bool VEC>
+hipError_t attn_bwd_vec(const AttnLaunch& l, hipStream_t s) {
+  switch (attn_dq(l.a.D)) {
+    case 32: return attn_bwd_go<T, 32, MT, NP, VEC>(l, s);
+    case 64: return attn_bwd_go<T, 64, MT, NP, VEC>(l, s);
+    case 96: return attn_bwd_go<T, 96, MT, NP, VEC>(l, s);
+    default: return attn_bwd_go<T, 128, MT, NP, VEC>(l, s);
+  }
+}
 template <typename T, int MT, int NP>
 hipError_t attn_bwd_d(const AttnLaunch& l, hipStream_t s) {
-  switch (attn_dq(l.a.D)) {
-    case 32: return attn_bwd_go<T, 32, MT, NP>(l, s);
-    case 64: return attn_bwd_go<T, 64, MT, NP>(l, s);
-    case 96: return attn_bwd_go<T, 96, MT, NP>(l, s);
-    default: return attn_bwd_go<T, 128, MT, NP>(l, s);
-  }
+  return l.a.vec == 2 ? attn_bwd_vec<T, MT, NP, true>(l, s) : attn_bwd_vec<T, MT, NP, false>(l, s);
 }
 
 hipError_t attn_bwd_bf16(const AttnLaunch& l, hipStream_t s);

@@ -88,9 +88,17 @@ __device__ __forceinline__ uint4 step_cols(const unsigned char* lds, int c0, int
     const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_ptr)(lds + row * kStride + c0 + j % 2 * 8));
     const uint32_t w[2] = {static_cast<uint32_t>(v[0]), static_cast<uint32_t>(v[1])};
     return StepEl<CT>::op(w);
+  } else if constexpr (sizeof(CT) == 2) {  // the same with 4 values of a row
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+    const unsigned char* const p = lds + (4 * g + j / 4) * kStride + c0 * 2 + j % 4 * 8;
+    const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p)));
+    const uint2 y = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * kStride)));
+    return make_uint4(x.x, x.y, y.x, y.y);
   } else {
-    constexpr int D = (kStride - 16) / static_cast<int>(sizeof(CT));
-    return AttnTile<CT, 64, D, 16>::cols(lds, 0, c0, lane);
+    const unsigned char* const p = lds + 4 * g * kStride + (c0 + j) * 4;
+    return make_uint4(*reinterpret_cast<const uint32_t*>(p), *reinterpret_cast<const uint32_t*>(p + kStride),
+                      *reinterpret_cast<const uint32_t*>(p + 2 * kStride), *reinterpret_cast<const uint32_t*>(p + 3 * kStride));
   }
 }
 

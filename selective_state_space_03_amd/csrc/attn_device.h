@@ -80,35 +80,74 @@ __device__ __forceinline__ uint4 attn_chunk(const T* row, int c, int D, int vec)
   }
 }
 
-// A tile of kRows rows of kD channels (a multiple of 32) in LDS.  kPad bytes behind each row: 16 where
-// rows are read in 16-byte groups by 16 lanes of 16 rows, 32 where they are read transposed.
-template <typename T, int kRows, int kD, int kPad>
-struct AttnTile {
-  static constexpr int kStride = kD * static_cast<int>(sizeof(T)) + kPad;
-  static constexpr int kBytes = kRows * kStride;
-  static constexpr int kChunks = kD * static_cast<int>(sizeof(T)) / 16;
-  static constexpr int kPer = (kRows * kChunks + 255) / 256;  // chunks per lane of 256
-  static_assert(kRows * kChunks % 256 == 0, "whole accesses");
+// Global loads in flight of this wave, those into LDS among them, are done
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-  // rows j0 .. of `n` rows at `base` (of row 0) into registers; rows from n on are zeros and not read
+// A tile of kRows rows of kD channels (a multiple of 32) in LDS, in slots of 16 bytes: group c of row r lies
+// in slot c ^ swap(r) of its row.  So neither 16 lanes that read one group of 16 rows, nor the transposed
+// reads of two groups of four rows, meet in a bank.  96 channels take the room of 128.
+// kVecRows: rows of aligned 16-byte groups go straight to LDS (a wave's load fills 64 slots in order, each
+// lane fetches the group that belongs into its slot; the buffer's range check gives zeros for rows past
+// the last and groups past D).  Other rows go through registers.
+template <typename T, int kRows, int kD, bool kVecRows>
+struct AttnTile {
+  static constexpr int kSlots = (kD == 96 ? 128 : kD) * static_cast<int>(sizeof(T)) / 16;
+  static constexpr int kStride = kSlots * 16;
+  static constexpr int kBytes = kRows * kStride;
+  static constexpr int kPer = kRows * kSlots / 256;  // slots per lane of 256
+  static_assert(kRows * kSlots % 256 == 0, "whole accesses");
+
+  static __device__ __forceinline__ int swap(int r) {
+    if constexpr (kSlots == 4) return r >> 2 & 3;
+    if constexpr (kSlots == 8) return sizeof(T) == 2 ? (r >> 1 & 3) * 2 + (r >> 3 & 1) : (r >> 2 & 1) * 4 + (r >> 3 & 1) * 2 + (r >> 1 & 1);
+    return sizeof(T) == 2 ? (r & 7) * 2 + (r >> 3 & 1) : (r >> 2 & 3) * 4 + (r & 3);
+  }
+  // first channel of the group in slot x
+  static __device__ __forceinline__ int channel(int x) { return (x % kSlots ^ swap(x / kSlots)) * AttnEl<T>::kVec; }
+
+  // Where this lane's groups lie from the tile's first row on, in bytes
+  struct Source {
+    uint32_t at[kVecRows ? kPer : 1];
+  };
+  static __device__ __forceinline__ Source source(long stride, int D) {
+    Source s;
+    if constexpr (kVecRows) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = threadIdx.x + 256 * i, c = channel(x);
+        s.at[i] = c < D ? static_cast<uint32_t>((x / kSlots * stride + c) * sizeof(T)) : 0x80000000u;
+      }
+    }
+    return s;
+  }
+  // rows j0 .. of the n rows at `base` into LDS; done after loads_done() and a barrier
+  static __device__ __forceinline__ void load(unsigned char* lds, const Source& s, const T* base, long stride, int j0, int n, int D) {
+    static_assert(kVecRows, "16-byte groups");
+    const int rows = min(kRows, n - j0);
+    const uint32_t bytes = rows > 0 ? static_cast<uint32_t>(((rows - 1) * stride + D) * sizeof(T)) : 0u;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base + j0 * stride), 0, static_cast<int>(bytes), 0x00020000);
+    unsigned char* const to = lds + uniform(threadIdx.x / 64) * 1024;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(to + 4096 * i), 16, s.at[i], 0, 0, 0);
+  }
+  // the same through registers, rows from n on as zeros
   static __device__ __forceinline__ void fetch(const T* base, long stride, int j0, int n, int D, int vec, uint4 (&r)[kPer]) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int x = threadIdx.x + 256 * i, row = j0 + x / kChunks, c = x % kChunks * AttnEl<T>::kVec;
+      const int x = threadIdx.x + 256 * i, row = j0 + x / kSlots;
       r[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row < n) r[i] = attn_chunk<T>(base + row * stride, c, D, vec);
+      if (row < n) r[i] = attn_chunk<T>(base + row * stride, channel(x), D, vec);
     }
   }
   static __device__ __forceinline__ void put(unsigned char* lds, const uint4 (&r)[kPer]) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int x = threadIdx.x + 256 * i;
-      *reinterpret_cast<uint4*>(lds + x / kChunks * kStride + x % kChunks * 16) = r[i];
-    }
+    for (int i = 0; i < kPer; ++i) *reinterpret_cast<uint4*>(lds + (threadIdx.x + 256 * i) * 16) = r[i];
   }
-  // rows row0 .. row0 + 15, channels of unit u
+  // rows row0 .. row0 + 15 (row0 a multiple of 16), channels of unit u
   static __device__ __forceinline__ uint4 rows(const unsigned char* lds, int row0, int u, int lane) {
-    return *reinterpret_cast<const uint4*>(lds + (row0 + lane % 16) * kStride + u * 64 + lane / 16 * 16);
+    const int r = lane % 16, c = 4 * u + lane / 16;
+    return *reinterpret_cast<const uint4*>(lds + row0 * kStride + r * kStride + (c ^ swap(r)) * 16);
   }
   // transposed: row = channel c0 + lane % 16, along the tokens from row0 on (32 in bf16, 16 in f32)
   static __device__ __forceinline__ uint4 cols(const unsigned char* lds, int row0, int c0, int lane) {
@@ -117,15 +156,20 @@ struct AttnTile {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4* lds_ptr;
       // lane j of a group of 16 reads 8 bytes of row j / 4; it gets the four rows' values of column j
-      const unsigned char* p = lds + (row0 + 4 * g + j / 4) * kStride + c0 * 2 + j % 4 * 8;
+      const int r = 4 * g + j / 4, c = c0 / 8 + j % 4 / 2;
+      const unsigned char* p = lds + row0 * kStride + r * kStride + (c ^ swap(r)) * 16 + j % 2 * 8;
       const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
       const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + 16 * kStride));
       const uint2 a = __builtin_bit_cast(uint2, x), b = __builtin_bit_cast(uint2, y);
       return make_uint4(a.x, a.y, b.x, b.y);
     } else {
-      const unsigned char* p = lds + (row0 + 4 * g) * kStride + (c0 + j) * 4;
-      return make_uint4(*reinterpret_cast<const uint32_t*>(p), *reinterpret_cast<const uint32_t*>(p + kStride),
-                        *reinterpret_cast<const uint32_t*>(p + 2 * kStride), *reinterpret_cast<const uint32_t*>(p + 3 * kStride));
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * g + i, c = c0 / 4 + j / 4;
+        w[i] = *reinterpret_cast<const uint32_t*>(lds + row0 * kStride + r * kStride + (c ^ swap(r)) * 16 + j % 4 * 4);
+      }
+      return make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 };

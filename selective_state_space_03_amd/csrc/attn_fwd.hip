@@ -5,8 +5,8 @@ namespace ssm {
 // P enters its product in two bf16 parts for an o in bf16.
 hipError_t attn_fwd_bf16(const AttnLaunch& l, hipStream_t s) {
   // 128 queries a workgroup where that still gives every CU two workgroups
-  if (attn_tiles(l.a, 128, false) * l.a.h >= 512) return attn_fwd_d<bf16s, 2, 2>(l, s);
-  return attn_fwd_d<bf16s, 1, 2>(l, s);
+  if (l.a.vec == 2 && attn_tiles(l.a, 128, false) * l.a.h >= 512) return attn_fwd_d<bf16s, 2, 2, true>(l, s);
+  return attn_fwd_narrow<bf16s, 2>(l, s);
 }
 
 hipError_t launch_attn_fwd(const AttnLaunch& l, hipStream_t s) {

@@ -13,14 +13,13 @@
 
 namespace ssm {
 
-template <typename T, int DQ, int MT, int NP>
+template <typename T, int DQ, int MT, int NP, bool VEC>
 __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int o_bf16) {
   using E = AttnEl<T>;
   constexpr int BN = E::kTile, KT = BN / 16, KS = DQ / E::kUnit, NT = DQ / 16, BM = 64 * MT;
   constexpr int PU = sizeof(T) == 2 ? 2 : 1, UN = KT / PU;  // accumulator tiles per unit of tokens, units per tile
-  using KTile = AttnTile<T, BN, DQ, 16>;
-  using VTile = AttnTile<T, BN, DQ, 32>;
-  __shared__ __align__(16) unsigned char lds[2][KTile::kBytes + VTile::kBytes];
+  using Tile = AttnTile<T, BN, DQ, VEC>;
+  __shared__ __align__(16) unsigned char lds[2][2 * Tile::kBytes];  // keys, values
 
   const AttnWork w = attn_work(a, blockIdx.x, BM, false, a.h / a.hk);
   if (w.tile < 0) return;
@@ -63,24 +62,35 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
   const float cs = a.scale * kLog2e;
   const int p0 = off + i0, p1 = p0 + 16 * MT - 1;  // the wave's positions
 
-  uint4 kr[KTile::kPer], vr[VTile::kPer];
-  if (n > 0) {
-    const int j0 = ns > 0 ? 0 : first * BN;
-    KTile::fetch(kb, a.k_stride, j0, sq.nk, a.D, a.vec, kr);
-    VTile::fetch(vb, a.v_stride, j0, sq.nk, a.D, a.vec, vr);
-    KTile::put(lds[0], kr);
-    VTile::put(lds[0] + KTile::kBytes, vr);
-  }
-  lds_barrier();
-  for (int t = 0; t < n; ++t) {
-    const int j0 = (t < ns ? t : t - ns + first) * BN;
-    if (t + 1 < n) {
-      const int j1 = (t + 1 < ns ? t + 1 : t + 1 - ns + first) * BN;
-      KTile::fetch(kb, a.k_stride, j1, sq.nk, a.D, a.vec, kr);
-      VTile::fetch(vb, a.v_stride, j1, sq.nk, a.D, a.vec, vr);
+  uint4 kr[VEC ? 1 : Tile::kPer], vr[VEC ? 1 : Tile::kPer];
+  const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
+  const auto key = [&](int t) { return (t < ns ? t : t - ns + first) * BN; };  // first key of tile t
+  const auto load = [&](int t) {
+    if constexpr (VEC) {
+      Tile::load(lds[t & 1], ks, kb, a.k_stride, key(t), sq.nk, a.D);
+      Tile::load(lds[t & 1] + Tile::kBytes, vs, vb, a.v_stride, key(t), sq.nk, a.D);
+    } else {
+      Tile::fetch(kb, a.k_stride, key(t), sq.nk, a.D, a.vec, kr);
+      Tile::fetch(vb, a.v_stride, key(t), sq.nk, a.D, a.vec, vr);
     }
+  };
+  const auto put = [&](int t) {
+    if constexpr (!VEC) {
+      Tile::put(lds[t & 1], kr);
+      Tile::put(lds[t & 1] + Tile::kBytes, vr);
+    }
+  };
+  if (n > 0) {
+    load(0);
+    put(0);
+  }
+  for (int t = 0; t < n; ++t) {
+    if constexpr (VEC) loads_done();
+    lds_barrier();  // tile t is there, and nobody reads the tile before it any more
+    if (t + 1 < n) load(t + 1);
+    const int j0 = key(t);
     const unsigned char* const kl = lds[t & 1];
-    const unsigned char* const vl = kl + KTile::kBytes;
+    const unsigned char* const vl = kl + Tile::kBytes;
     const bool some = j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - a.window || j0 < a.sinks);
     if (some) {
       f32x4 s[MT][KT];
@@ -92,7 +102,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
       for (int u = 0; u < KS; ++u)
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-          const uint4 x = KTile::rows(kl, 16 * k, u, lane);
+          const uint4 x = Tile::rows(kl, 16 * k, u, lane);
 #pragma unroll
           for (int m = 0; m < MT; ++m) s[m][k] = attn_mma<T>(x, q[m][u], s[m][k]);
         }
@@ -153,18 +163,14 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
       for (int u = 0; u < UN; ++u)
 #pragma unroll
         for (int d = 0; d < NT; ++d) {
-          const uint4 x = VTile::cols(vl, 16 * PU * u, 16 * d, lane);
+          const uint4 x = Tile::cols(vl, 16 * PU * u, 16 * d, lane);
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = NP - 1; e >= 0; --e) o[m][d] = attn_mma<T>(x, p[m][u].p[e], o[m][d]);
         }
     }
-    if (t + 1 < n) {
-      KTile::put(lds[(t + 1) & 1], kr);
-      VTile::put(lds[(t + 1) & 1] + KTile::kBytes, vr);
-    }
-    lds_barrier();
+    if (t + 1 < n) put(t + 1);
   }
 
 #pragma unroll
@@ -183,24 +189,28 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
   }
 }
 
-template <typename T, int DQ, int MT, int NP>
+template <typename T, int DQ, int MT, int NP, bool VEC>
 hipError_t attn_fwd_go(const AttnLaunch& l, hipStream_t s) {
   const AttnArgs& a = l.a;
   const long blocks = attn_tiles(a, 64 * MT, false) * a.h;
   return timed_launch(s, [&] {
-    hipLaunchKernelGGL((attn_fwd_kernel<T, DQ, MT, NP>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a,
+    hipLaunchKernelGGL((attn_fwd_kernel<T, DQ, MT, NP, VEC>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a,
                        l.o_dtype == kBF16);
   });
 }
 
-template <typename T, int MT, int NP>
+template <typename T, int MT, int NP, bool VEC>
 hipError_t attn_fwd_d(const AttnLaunch& l, hipStream_t s) {
   switch (attn_dq(l.a.D)) {
-    case 32: return attn_fwd_go<T, 32, MT, NP>(l, s);
-    case 64: return attn_fwd_go<T, 64, MT, NP>(l, s);
-    case 96: return attn_fwd_go<T, 96, MT, NP>(l, s);
-    default: return attn_fwd_go<T, 128, MT, NP>(l, s);
+    case 32: return attn_fwd_go<T, 32, MT, NP, VEC>(l, s);
+    case 64: return attn_fwd_go<T, 64, MT, NP, VEC>(l, s);
+    case 96: return attn_fwd_go<T, 96, MT, NP, VEC>(l, s);
+    default: return attn_fwd_go<T, 128, MT, NP, VEC>(l, s);
   }
+}
+template <typename T, int NP>
+hipError_t attn_fwd_narrow(const AttnLaunch& l, hipStream_t s) {  // 64 queries a workgroup
+  return l.a.vec == 2 ? attn_fwd_d<T, 1, NP, true>(l, s) : attn_fwd_d<T, 1, NP, false>(l, s);
 }
 
 hipError_t attn_fwd_bf16(const AttnLaunch& l, hipStream_t s);
