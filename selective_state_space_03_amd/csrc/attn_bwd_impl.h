@@ -76,8 +76,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
   const auto key = [&](int t) { return (t < ns ? t : t - ns + first) * BN; };  // first key of tile t
   const auto load = [&](int t) {
     if constexpr (VEC) {
-      Tile::load(lds[t & 1], ks, kb, a.k_stride, key(t), sq.nk, a.D);
-      Tile::load(lds[t & 1] + Tile::kBytes, vs, vb, a.v_stride, key(t), sq.nk, a.D);
+      Tile::load(lds_address(lds[t & 1]), ks, kb, a.k_stride, key(t), sq.nk, a.D);
+      Tile::load(lds_address(lds[t & 1]) + Tile::kBytes, vs, vb, a.v_stride, key(t), sq.nk, a.D);
     } else {
       Tile::fetch(kb, a.k_stride, key(t), sq.nk, a.D, a.vec, kr);
       Tile::fetch(vb, a.v_stride, key(t), sq.nk, a.D, a.vec, vr);
@@ -253,8 +253,8 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
     const T* const qb = static_cast<const T*>(a.q) + sq.q0 * a.q_stride + static_cast<long>(head) * a.D;
     const T* const db = static_cast<const T*>(a.dout) + (sq.q0 * a.h + head) * a.D;
     if constexpr (VEC) {
-      Tile::load(lds[t & 1], qs, qb, a.q_stride, i0, sq.nq, a.D);
-      Tile::load(lds[t & 1] + Tile::kBytes, ds, db, dstride, i0, sq.nq, a.D);
+      Tile::load(lds_address(lds[t & 1]), qs, qb, a.q_stride, i0, sq.nq, a.D);
+      Tile::load(lds_address(lds[t & 1]) + Tile::kBytes, ds, db, dstride, i0, sq.nq, a.D);
     } else {
       Tile::fetch(qb, a.q_stride, i0, sq.nq, a.D, a.vec, qr);
       Tile::fetch(db, dstride, i0, sq.nq, a.D, a.vec, dr);

@@ -83,19 +83,39 @@ __device__ __forceinline__ uint4 attn_chunk(const T* row, int c, int D, int vec)
 // Global loads in flight of this wave, those into LDS among them, are done
 __device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// .. all but the last kLeft of them
+template <int kLeft>
+__device__ __forceinline__ void loads_left() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory"); }
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint32_t lds_address(const unsigned char* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) unsigned char*)p));
+}
+// 16 bytes a lane from its offset in the buffer to `to` and on.  As an instruction of its own: behind the
+// builtin the compiler waits for all such loads ahead of the next read of LDS, whatever that reads, so that
+// none would be in flight during the products (prompt 221 us).  It counts outstanding loads from its own
+// alone, and with others among them waits for more than it means to, not less.  The wait states are for
+// M0, and for a descriptor that has just come back from a vector register.
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(offset), "s"(rsrc)
+               : "memory", "m0");
+}
+
 // A tile of kRows rows of kD channels (a multiple of 32) in LDS, in slots of 16 bytes: group c of row r lies
 // in slot c ^ swap(r) of its row.  So neither 16 lanes that read one group of 16 rows, nor the transposed
 // reads of two groups of four rows, meet in a bank.  96 channels take the room of 128.
 // kVecRows: rows of aligned 16-byte groups go straight to LDS (a wave's load fills 64 slots in order, each
 // lane fetches the group that belongs into its slot; the buffer's range check gives zeros for rows past
 // the last and groups past D).  Other rows go through registers.
-template <typename T, int kRows, int kD, bool kVecRows>
+template <typename T, int kRows, int kD, bool kVecRows, int kThreads = 256>
 struct AttnTile {
   static constexpr int kSlots = (kD == 96 ? 128 : kD) * static_cast<int>(sizeof(T)) / 16;
   static constexpr int kStride = kSlots * 16;
   static constexpr int kBytes = kRows * kStride;
-  static constexpr int kPer = kRows * kSlots / 256;  // slots per lane of 256
-  static_assert(kRows * kSlots % 256 == 0, "whole accesses");
+  static constexpr int kAll = kRows * kSlots;
+  static constexpr int kUse = kAll < kThreads ? kAll : kThreads;  // threads that load
+  static constexpr int kPer = kAll / kUse;                        // slots of one of them
+  static_assert(kAll % kUse == 0 && kUse % 64 == 0, "whole accesses");
 
   static __device__ __forceinline__ int swap(int r) {
     if constexpr (kSlots == 4) return r >> 2 & 3;
@@ -110,39 +130,42 @@ struct AttnTile {
     uint32_t at[kVecRows ? kPer : 1];
   };
   static __device__ __forceinline__ Source source(long stride, int D) {
-    Source s;
+    Source s{};
     if constexpr (kVecRows) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int x = threadIdx.x + 256 * i, c = channel(x);
+        const int x = threadIdx.x % kThreads + kUse * i, c = channel(x);
         s.at[i] = c < D ? static_cast<uint32_t>((x / kSlots * stride + c) * sizeof(T)) : 0x80000000u;
       }
     }
     return s;
   }
-  // rows j0 .. of the n rows at `base` into LDS; done after loads_done() and a barrier
-  static __device__ __forceinline__ void load(unsigned char* lds, const Source& s, const T* base, long stride, int j0, int n, int D) {
+  // rows j0 .. of the n rows at `base` into LDS (at an address from lds_address); done after loads_done() and
+  // a barrier
+  static __device__ __forceinline__ void load(uint32_t lds, const Source& s, const T* base, long stride, int j0, int n, int D) {
     static_assert(kVecRows, "16-byte groups");
+    const int wave = uniform(threadIdx.x % kThreads / 64);
+    if (kUse < kThreads && wave >= kUse / 64) return;
     const int rows = min(kRows, n - j0);
-    const uint32_t bytes = rows > 0 ? static_cast<uint32_t>(((rows - 1) * stride + D) * sizeof(T)) : 0u;
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base + j0 * stride), 0, static_cast<int>(bytes), 0x00020000);
-    unsigned char* const to = lds + uniform(threadIdx.x / 64) * 1024;
+    const uint32_t bytes = rows > 0 ? static_cast<uint32_t>(((rows - 1) * static_cast<int>(stride) + D) * static_cast<int>(sizeof(T))) : 0u;
+    const uint64_t from = reinterpret_cast<uint64_t>(base + j0 * stride);
+    const u32x4 rsrc = {static_cast<uint32_t>(from), static_cast<uint32_t>(from >> 32) & 0xffffu, bytes, 0x00020000u};
+    const uint32_t to = lds + static_cast<uint32_t>(wave) * 1024u;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(to + 4096 * i), 16, s.at[i], 0, 0, 0);
+    for (int i = 0; i < kPer; ++i) load_to_lds(rsrc, s.at[i], to + 16u * kUse * i);
   }
   // the same through registers, rows from n on as zeros
   static __device__ __forceinline__ void fetch(const T* base, long stride, int j0, int n, int D, int vec, uint4 (&r)[kPer]) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int x = threadIdx.x + 256 * i, row = j0 + x / kSlots;
+      const int x = threadIdx.x % kThreads + kUse * i, row = j0 + x / kSlots;
       r[i] = make_uint4(0u, 0u, 0u, 0u);
       if (row < n) r[i] = attn_chunk<T>(base + row * stride, channel(x), D, vec);
     }
   }
   static __device__ __forceinline__ void put(unsigned char* lds, const uint4 (&r)[kPer]) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) *reinterpret_cast<uint4*>(lds + (threadIdx.x + 256 * i) * 16) = r[i];
+    for (int i = 0; i < kPer; ++i) *reinterpret_cast<uint4*>(lds + (threadIdx.x + kUse * i) * 16) = r[i];
   }
   // rows row0 .. row0 + 15 (row0 a multiple of 16), channels of unit u
   static __device__ __forceinline__ uint4 rows(const unsigned char* lds, int row0, int u, int lane) {
@@ -173,6 +196,91 @@ struct AttnTile {
     }
   }
 };
+
+// 32 x 32 tiles of bf16 (a unit is 16 deep; h = lane / 32): operands hold rows or columns lane % 32 and the
+// depths 8 h + i; an accumulator has column = lane % 32, row = 8 (i / 4) + 4 h + i % 4, so that its values
+// 8 s .. 8 s + 7 are an operand of unit s over the tokens 16 s + 8 (i / 4) + 4 h + i % 4.  A vector
+// instruction of another wave goes beside a 32 x 32 x 16 product without loss (32 FMA beside 8 products
+// 131 ns, the products alone 130), beside 16 x 16 x 32 only in part (106 ns for 64 and 63).
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f32x16 mma32(uint4 a, uint4 b, f32x16 acc) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+}
+template <typename Tile>  // of bf16
+struct Wide {
+  // Addresses in LDS: of this lane's part of the first unit, which the others differ from in bits of their own
+  static __device__ __forceinline__ uint32_t rows_at(const unsigned char* lds, int lane) {
+    const int r = lane % 32;
+    return lds_address(lds) + r * Tile::kStride + (lane / 32 ^ Tile::swap(r)) * 16;
+  }
+  static __device__ __forceinline__ uint32_t cols_at(const unsigned char* lds, int lane) {
+    const int j = lane % 16, r = 4 * (lane / 32) + j / 4, c = 2 * (lane / 16 % 2) + j % 4 / 2;
+    return lds_address(lds) + r * Tile::kStride + (c ^ Tile::swap(r)) * 16 + j % 2 * 8;
+  }
+  // rows row0 .. row0 + 31, channels 16 u ..
+  static __device__ __forceinline__ uint4 rows(uint32_t at, int row0, int u) {
+    typedef const __attribute__((address_space(3))) u32x4* lds_ptr;
+    const u32x4 v = *(lds_ptr)((at ^ (u << 5)) + row0 * Tile::kStride);
+    return make_uint4(v.x, v.y, v.z, v.w);
+  }
+  // transposed: row = channel 32 d + lane % 32, along the tokens of the unit from row0 (a multiple of 16) on
+  static __device__ __forceinline__ uint4 cols(uint32_t at, int row0, int d) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s16x4* lds_ptr;
+    constexpr uint32_t kEight = Tile::kSlots == 4 ? 32 : 16;  // what eight rows on change in the slot
+    const uint32_t p = at ^ (d << 6);
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p + row0 * Tile::kStride));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)((p ^ kEight) + (row0 + 8) * Tile::kStride));
+    const uint2 a = __builtin_bit_cast(uint2, x), b = __builtin_bit_cast(uint2, y);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+};
+// values 8 s .. of an accumulator over tokens as an operand of NP bf16 parts
+template <int NP>
+__device__ __forceinline__ Frag<NP> wide_operand(const f32x16& x, int s) {
+  Frag<NP> f;
+  uint32_t w[4][NP];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2<NP>(x[8 * s + 2 * i], x[8 * s + 2 * i + 1], w[i]);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) f.p[p] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+  return f;
+}
+// Scores of a tile from key j0 on, of queries from position p0 on (32 of them, the lane's at pos), of keys that
+// are not seen.  Tiles in which every query sees every key pass by; others mostly meet one border.
+template <int KT>
+__device__ __forceinline__ void wide_hide(f32x16 (&s)[KT], int j0, int p0, int pos, int h, int window, int sinks) {
+  const int d = pos - j0 - 4 * h, w = d - window, f = sinks - j0 - 4 * h;
+  if (j0 + 32 * KT - 1 > p0) {
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[k][e] = 32 * k + 8 * (e / 4) + e % 4 <= d ? s[k][e] : -INFINITY;
+  }
+  if (j0 > p0 + 31 - window || j0 + 32 * KT <= sinks) return;
+  if (j0 >= sinks) {
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[k][e] = 32 * k + 8 * (e / 4) + e % 4 > w ? s[k][e] : -INFINITY;
+  } else {
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int j = 32 * k + 8 * (e / 4) + e % 4;
+        s[k][e] = j > w || j < f ? s[k][e] : -INFINITY;
+      }
+  }
+}
+__device__ __forceinline__ float half_max(float x) {  // over the two halves of the wave
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
 
 // Accumulator tiles over tokens as an operand of NP bf16 parts (f32: as they are).  x: the tiles of one
 // unit, two of 16 tokens in bf16, one in f32.
@@ -207,27 +315,37 @@ __device__ __forceinline__ float group_sum(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// One column (row of the output) of accumulator tiles over channels: D values at element `at` of a dense
-// tensor in f32 or bf16; lane group g holds the channels 16 t + 4 g ..
+// Four channels from d on of a row of D at element `at` of a dense tensor in f32 or bf16
+__device__ __forceinline__ void attn_store4(void* out, size_t at, float x0, float x1, float x2, float x3, int d, int D, int bf16, int vec) {
+  if (D % 4 == 0 && vec > 0) {
+    if (d < D) {
+      if (bf16) *reinterpret_cast<uint2*>(static_cast<bf16s*>(out) + at + d) = make_uint2(pack_rne(x0, x1), pack_rne(x2, x3));
+      else *reinterpret_cast<float4*>(static_cast<float*>(out) + at + d) = make_float4(x0, x1, x2, x3);
+    }
+  } else {
+    const float x[4] = {x0, x1, x2, x3};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (d + i < D) {
+        if (bf16) st<bf16s>(out, at + d + i, x[i]);
+        else st<float>(out, at + d + i, x[i]);
+      }
+  }
+}
+// One column (row of the output) of accumulator tiles over channels: lane group g holds 16 t + 4 g ..
 template <int NT>
 __device__ __forceinline__ void attn_store_row(void* out, size_t at, const f32x4 (&x)[NT], int D, int g, int bf16, int vec) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int d = 16 * t + 4 * g;
-    if (D % 4 == 0 && vec > 0) {
-      if (d < D) {
-        if (bf16) *reinterpret_cast<uint2*>(static_cast<bf16s*>(out) + at + d) = make_uint2(pack_rne(x[t][0], x[t][1]), pack_rne(x[t][2], x[t][3]));
-        else *reinterpret_cast<float4*>(static_cast<float*>(out) + at + d) = make_float4(x[t][0], x[t][1], x[t][2], x[t][3]);
-      }
-    } else {
+  for (int t = 0; t < NT; ++t) attn_store4(out, at, x[t][0], x[t][1], x[t][2], x[t][3], 16 * t + 4 * g, D, bf16, vec);
+}
+// .. of 32 x 32 tiles: half h of the wave holds 32 t + 8 i + 4 h ..
+template <int NT>
+__device__ __forceinline__ void wide_store_row(void* out, size_t at, const f32x16 (&x)[NT], int D, int h, int bf16, int vec) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (d + i < D) {
-          if (bf16) st<bf16s>(out, at + d + i, x[t][i]);
-          else st<float>(out, at + d + i, x[t][i]);
-        }
-    }
-  }
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      attn_store4(out, at, x[t][4 * i], x[t][4 * i + 1], x[t][4 * i + 2], x[t][4 * i + 3], 32 * t + 8 * i + 4 * h, D, bf16, vec);
 }
 
 struct AttnSeq {
