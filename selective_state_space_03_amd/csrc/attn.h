@@ -47,6 +47,7 @@ inline long attn_tiles(const AttnArgs& a, int rows, bool keys) {
 inline long attn_pieces(const AttnArgs& a) {
   return a.cu_q ? a.lq / a.span + a.nseq : static_cast<long>(a.nseq) * ((a.lq + a.span - 1) / a.span);
 }
+constexpr int kSinkRows = 64;  // keys of a tile of the backward pass
 hipError_t launch_attn_fwd(const AttnLaunch& l, hipStream_t s);
 hipError_t launch_attn_bwd(const AttnLaunch& l, hipStream_t s);
 hipError_t launch_attn_sinks(const AttnArgs& a, hipStream_t s);

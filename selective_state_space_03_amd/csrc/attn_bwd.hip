@@ -32,22 +32,29 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(const AttnArgs a, long 
   }
 }
 
-// Adds the pieces' partial sums of the keys of the sinks' tiles, in order: a workgroup per (sequence, key
-// head, tile)
+// Adds the pieces' partial sums of the keys of the sinks' tiles, in order: a workgroup for four keys of a
+// (sequence, key head, tile)
 __global__ __launch_bounds__(256) void attn_sink_kernel(const AttnArgs a) {
-  const int tile = blockIdx.x % a.sink_tiles, r = blockIdx.x / a.sink_tiles, kh = r % a.hk, s = r / a.hk;
+  const int parts = kSinkRows / 4, part = blockIdx.x % parts;
+  unsigned r = blockIdx.x / parts;
+  const int tile = r % a.sink_tiles;
+  r /= a.sink_tiles;
+  const int kh = r % a.hk, s = r / a.hk;
   const AttnSeq q = attn_seq(a, s);
   const long slot = a.cu_q ? q.q0 / a.span + s : static_cast<long>(s) * ((a.lq + a.span - 1) / a.span);
-  const int pieces = (q.nq + a.span - 1) / a.span;
-  const int rows = min(64, q.nk - tile * 64);
+  const int pieces = (q.nq + a.span - 1) / a.span, j0 = tile * kSinkRows;
+  const int rows = min(4, q.nk - j0 - 4 * part);
+  const size_t step = static_cast<size_t>(a.hk) * a.sink_tiles * kSinkRows * a.D;  // from a piece to the next
   for (int e = threadIdx.x; e < rows * a.D; e += 256) {
+    const int row = 4 * part + e / a.D, d = e % a.D;
+    const size_t at = (((static_cast<size_t>(slot) * a.hk + kh) * a.sink_tiles + tile) * kSinkRows + row) * a.D + d;
     float k = 0.0f, v = 0.0f;
+#pragma unroll 4
     for (int p = 0; p < pieces; ++p) {
-      const size_t at = ((static_cast<size_t>(slot + p) * a.hk + kh) * a.sink_tiles + tile) * 64 * a.D + e;
-      k += a.dk_part[at];
-      v += a.dv_part[at];
+      k += a.dk_part[at + p * step];
+      v += a.dv_part[at + p * step];
     }
-    const size_t to = (static_cast<size_t>(q.k0 + tile * 64 + e / a.D) * a.hk + kh) * a.D + e % a.D;
+    const size_t to = (static_cast<size_t>(q.k0 + j0 + row) * a.hk + kh) * a.D + d;
     if (a.grad_bf16) {
       if (a.dk) st<bf16s>(a.dk, to, k);
       if (a.dv) st<bf16s>(a.dv, to, v);
@@ -68,11 +75,13 @@ hipError_t delta_go(const AttnArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_attn_sinks(const AttnArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(attn_sink_kernel, dim3(static_cast<unsigned>(a.nseq) * a.hk * a.sink_tiles), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(attn_sink_kernel, dim3(static_cast<unsigned>(a.nseq) * a.hk * a.sink_tiles * (kSinkRows / 4)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-hipError_t attn_bwd_bf16(const AttnLaunch& l, hipStream_t s) { return attn_bwd_d<bf16s, 1, 2>(l, s); }
+hipError_t attn_bwd_bf16(const AttnArgs& a, hipStream_t s) {
+  return a.vec == 2 ? attn_bwd_wide<2>(a, s) : attn_bwd_d<bf16s, 2>(a, s);
+}
 
 hipError_t launch_attn_bwd(const AttnLaunch& l, hipStream_t s) {
   if (l.a.nseq == 0) return hipSuccess;
@@ -82,8 +91,8 @@ hipError_t launch_attn_bwd(const AttnLaunch& l, hipStream_t s) {
     else e = l.o_dtype == kBF16 ? delta_go<float, bf16s>(l.a, s) : delta_go<float, float>(l.a, s);
     if (e != hipSuccess) return e;
   }
-  if (l.in_dtype != kBF16) return attn_bwd_f32(l, s);
-  return l.grad_dtype == kBF16 ? attn_bwd_bf16(l, s) : attn_bwd_bf16_f32(l, s);
+  if (l.in_dtype != kBF16) return attn_bwd_f32(l.a, s);
+  return l.grad_dtype == kBF16 ? attn_bwd_bf16(l.a, s) : attn_bwd_bf16_f32(l.a, s);
 }
 
 }  // namespace ssm

@@ -373,42 +373,400 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
   }
 }
 
-template <typename T, int DQ, int MT, int NP, bool VEC>
-hipError_t attn_bwd_go(const AttnLaunch& l, hipStream_t s) {
-  const AttnArgs& a = l.a;
+// The queries' gradients of bf16 rows of aligned 16-byte groups in 32 x 32 tiles: 128 queries a workgroup, 32 a
+// wave, tiles of 32 keys.  Operands are read from LDS a step of products ahead, in an order that is held.
+template <int DQ, int NP>
+__global__ __launch_bounds__(256, 2) void attn_dq_wide_kernel(const AttnArgs a) {
+  constexpr int BN = 32, KS = DQ / 16, NT = DQ / 32, BM = 128;
+  using Tile = AttnTile<bf16s, BN, DQ, true>;
+  using W = Wide<Tile>;
+  __shared__ __align__(16) unsigned char lds[4][Tile::kBytes];  // keys, keys, values, values
+
+  const AttnWork w = attn_work(a, blockIdx.x, BM, false, a.h / a.hk);
+  if (w.tile < 0) return;
+  const AttnSeq sq = w.seq;
+  const int wave = uniform(threadIdx.x / 64), lane = threadIdx.x % 64, h = lane / 32, c = lane % 32;
+  const int kh = w.head / (a.h / a.hk);
+  const int off = sq.nk - sq.nq;
+  const int i0 = w.tile * BM + wave * 32;
+  const bf16s* const kb = static_cast<const bf16s*>(a.k) + sq.k0 * a.k_stride + static_cast<long>(kh) * a.D;
+  const bf16s* const vb = static_cast<const bf16s*>(a.v) + sq.k0 * a.v_stride + static_cast<long>(kh) * a.D;
+
+  uint4 q[KS], dO[KS];
+  float lse = INFINITY, delta = 0.0f;
+  {
+    const int i = i0 + c;
+    const long at = (sq.q0 + i) * a.h + w.head;
+    const bf16s* const qrow = static_cast<const bf16s*>(a.q) + (sq.q0 + i) * a.q_stride + static_cast<long>(w.head) * a.D;
+    const bf16s* const drow = static_cast<const bf16s*>(a.dout) + at * a.D;
+#pragma unroll
+    for (int u = 0; u < KS; ++u) {
+      const bool in = i < sq.nq && 16 * u + 8 * h < a.D;
+      q[u] = load16_if(qrow + 16 * u + 8 * h, in);
+      dO[u] = load16_if(drow + 16 * u + 8 * h, in);
+    }
+    if (i < sq.nq) {
+      lse = attn_lse2(a.lse[at]);
+      delta = a.delta[at];
+    }
+  }
+
+  const int last = off + min(w.tile * BM + BM, sq.nq) - 1;
+  const int lo = max(0, off + w.tile * BM - a.window + 1);
+  const int first = lo / BN;
+  const int ns = min((a.sinks + BN - 1) / BN, first);
+  const int n = last < 0 ? 0 : ns + max(0, last / BN + 1 - first);
+
+  f32x16 dq[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) dq[t] = f32x16{};
+  const float cs = a.scale * kLog2e;
+  const int p0 = off + i0, p1 = p0 + 31;
+  const bool lone_all = a.window == 1 && a.sinks == 0;
+
+  const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
+  const uint32_t lds0 = lds_address(lds[0]), k0 = W::rows_at(lds[0], lane), v0 = W::rows_at(lds[2], lane), c0 = W::cols_at(lds[0], lane);
+  const auto key = [&](int t) { return (t < ns ? t : t - ns + first) * BN; };
+  const auto load = [&](int t) {
+    Tile::load(lds0 + (t & 1) * Tile::kBytes, ks, kb, a.k_stride, key(t), sq.nk, a.D);
+    Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, vs, vb, a.v_stride, key(t), sq.nk, a.D);
+  };
+  if (n > 0) load(0);
+  for (int t = 0; t < n; ++t) {
+    loads_done();
+    lds_barrier();
+    if (t + 1 < n) load(t + 1);
+    const int j0 = key(t);
+    if (!(j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - a.window || j0 < a.sinks))) continue;
+    const uint32_t kl = k0 + (t & 1) * Tile::kBytes, vl = v0 + (t & 1) * Tile::kBytes, cl = c0 + (t & 1) * Tile::kBytes;
+    f32x16 s = {}, dp = {};
+    uint4 kf[2][2], vf[2][2], cf[2][NT];
+    const auto read = [&](int st) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        kf[st & 1][x] = W::rows(kl, 0, 2 * st + x);
+        vf[st & 1][x] = W::rows(vl, 0, 2 * st + x);
+      }
+    };
+    const auto read_c = [&](int u) {
+#pragma unroll
+      for (int d = 0; d < NT; ++d) cf[u][d] = W::cols(cl, 16 * u, d);
+    };
+    read(0);
+#pragma unroll
+    for (int st = 0; st < KS / 2; ++st) {
+      if (st + 1 < KS / 2) read(st + 1);
+      else read_c(0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        s = mma32(kf[st & 1][x], q[2 * st + x], s);
+        dp = mma32(vf[st & 1][x], dO[2 * st + x], dp);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = exp2_fast(fmaf(s[e], cs, -lse)) * (dp[e] - delta);
+    if (!(j0 + BN - 1 <= p0 && (j0 > p1 - a.window || j0 + BN <= a.sinks))) {
+      const int pos = p0 + c, d = pos - j0 - 4 * h, v = d - a.window, f = a.sinks - j0 - 4 * h;
+      const bool lone = pos == 0 || lone_all;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int j = 8 * (e / 4) + e % 4;
+        s[e] = j <= d && (j > v || j < f) && !lone ? s[e] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const Frag<NP> p = wide_operand<NP>(s, u);
+      if (u == 0) read_c(1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int e = NP - 1; e >= 0; --e)
+#pragma unroll
+        for (int d = 0; d < NT; ++d) dq[d] = mma32(cf[u][d], p.p[e], dq[d]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  const int i = i0 + c;
+  if (i >= sq.nq) return;
+#pragma unroll
+  for (int d = 0; d < NT; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) dq[d][e] *= a.scale;
+  wide_store_row<NT>(a.dq, (static_cast<size_t>(sq.q0 + i) * a.h + w.head) * a.D, dq, a.D, h, a.grad_bf16, a.vec);
+}
+
+// The keys' and values' gradients: 64 keys a workgroup, 32 a wave as columns, four pairs of waves that take every
+// fourth tile of 32 queries.  The keys are held in registers; the values, for which there is no room beside both
+// sums, in LDS.  The pairs' sums are added in LDS at the end.
+template <int DQ, int NP>
+__global__ __launch_bounds__(512, 2) void attn_dkv_wide_kernel(const AttnArgs a, unsigned sink_blocks) {
+  constexpr int BN = 32, KS = DQ / 16, NT = DQ / 32, BM = 64, G = 4;
+  constexpr int CT = NT == 4 ? 2 : NT, CS = NT / CT;  // channels' tiles of a step of products
+  using Tile = AttnTile<bf16s, BN, DQ, true, 128>;    // loaded by a pair of waves
+  using VTile = AttnTile<bf16s, BM, DQ, true, 512>;
+  using W = Wide<Tile>;
+  __shared__ __align__(16) unsigned char vlds[VTile::kBytes];
+  __shared__ __align__(16) unsigned char lds[G][4][Tile::kBytes];  // queries, queries, dout, dout; at the end sums
+  __shared__ __align__(16) float stats[G][2][2 * BN];              // lse, delta
+  static_assert(sizeof(lds) >= G * BM * DQ * 4, "room for the sums");
+
+  const int heads = a.h / a.hk;
+  const bool sink = blockIdx.x < sink_blocks;
+  AttnWork w;
+  long slot = 0;
+  int piece = 0;
+  if (sink) {
+    const unsigned per = static_cast<unsigned>(a.hk) * a.sink_tiles;
+    slot = blockIdx.x / per;
+    const unsigned r = blockIdx.x % per;
+    w.head = r / a.sink_tiles;
+    w.tile = r % a.sink_tiles;
+    if (a.cu_q) {
+      piece = attn_slot(a.cu_q, a.nseq, a.rows_q, a.span, slot, &w.seq, a, false);
+    } else {
+      const int pieces = (a.lq + a.span - 1) / a.span;
+      w.seq = attn_seq(a, static_cast<int>(slot / pieces));
+      piece = static_cast<int>(slot % pieces);
+    }
+    if (piece < 0) return;
+  } else {
+    w = attn_work(a, blockIdx.x - sink_blocks, BM, true, 1);
+    if (w.tile < a.sink_tiles) return;  // (also an unused slot)
+  }
+  const AttnSeq sq = w.seq;
+  const int wave = uniform(threadIdx.x / 64), g = wave / 2, lane = threadIdx.x % 64, h = lane / 32, c = lane % 32;
+  const int kh = w.head;
+  const int off = sq.nk - sq.nq;
+  const int jt = w.tile * BM, j0 = jt + wave % 2 * 32, j1 = j0 + 31;
+
+  VTile::load(lds_address(vlds), VTile::source(a.v_stride, a.D), static_cast<const bf16s*>(a.v) + sq.k0 * a.v_stride + static_cast<long>(kh) * a.D,
+              a.v_stride, jt, sq.nk, a.D);
+  uint4 k[KS];
+  {
+    const int j = j0 + c;
+    const bf16s* const row = static_cast<const bf16s*>(a.k) + (sq.k0 + j) * a.k_stride + static_cast<long>(kh) * a.D;
+#pragma unroll
+    for (int u = 0; u < KS; ++u) k[u] = load16_if(row + 16 * u + 8 * h, j < sq.nk && 16 * u + 8 * h < a.D);
+  }
+
+  // queries that see some key of the workgroup
+  long lo = max(0, jt - off), hi = sq.nq - 1L;
+  if (a.window != kAttnAll && jt >= a.sinks) hi = min(hi, static_cast<long>(min(jt + BM, sq.nk)) + a.window - 2 - off);
+  if (sink) {
+    lo = max(lo, static_cast<long>(piece) * a.span);
+    hi = min(hi, static_cast<long>(piece) * a.span + a.span - 1);
+  }
+  if (jt >= sq.nk) hi = -1;
+  const int first = static_cast<int>(lo / BN);
+  const int per = hi < lo ? 0 : static_cast<int>(hi / BN) + 1 - first;  // tiles of a head
+  const int n = per * heads, steps = (n + G - 1) / G;
+
+  f32x16 dk[NT], dv[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) dk[t] = dv[t] = f32x16{};
+  const float cs = a.scale * kLog2e;
+  const bool lone_all = a.window == 1 && a.sinks == 0;
+
+  const long dstride = static_cast<long>(a.h) * a.D;
+  const typename Tile::Source qs = Tile::source(a.q_stride, a.D), ds = Tile::source(dstride, a.D);
+  unsigned char(&mine)[4][Tile::kBytes] = lds[g];
+  const uint32_t lds0 = lds_address(mine[0]), q0 = W::rows_at(mine[0], lane), qc0 = W::cols_at(mine[0], lane);
+  const uint32_t vl = Wide<VTile>::rows_at(vlds + wave % 2 * 32 * VTile::kStride, lane);
+  const bool stater = threadIdx.x % 128 < 2 * BN;
+  float st = 0.0f;
+  int head = kh * heads, tile = first;  // of the tile asked for next
+  const auto skip = [&](int by) {
+    for (tile += by; tile >= first + per && per > 0; tile -= per) ++head;
+  };
+  const auto load = [&](int t) {
+    const int i0 = tile * BN;
+    Tile::load(lds0 + (t & 1) * Tile::kBytes, qs, static_cast<const bf16s*>(a.q) + sq.q0 * a.q_stride + static_cast<long>(head) * a.D, a.q_stride,
+               i0, sq.nq, a.D);
+    Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, ds, static_cast<const bf16s*>(a.dout) + (sq.q0 * a.h + head) * a.D, dstride, i0, sq.nq, a.D);
+    if (stater) {  // lse, then delta
+      const int x = threadIdx.x % (2 * BN), i = i0 + x % BN;
+      const long row = (sq.q0 + i) * a.h + head;
+      st = x < BN ? INFINITY : 0.0f;
+      if (i < sq.nq) st = x < BN ? attn_lse2(a.lse[row]) : a.delta[row];
+    }
+  };
+  skip(g);
+  int now = tile;  // the tile at hand
+  if (g < n) {
+    load(0);
+    if (stater) stats[g][0][threadIdx.x % (2 * BN)] = st;
+  }
+  for (int t = 0; t < steps; ++t) {
+    loads_done();
+    lds_barrier();
+    const bool more = G * (t + 1) + g < n;
+    const int i0 = now * BN, p0 = off + i0, p1 = p0 + BN - 1;
+    if (more) {
+      skip(G);
+      now = tile;
+      load(t + 1);
+    }
+    if (G * t + g < n && j0 <= p1 && j0 < sq.nk && (j1 > p0 - a.window || j0 < a.sinks)) {
+      const uint32_t ql = q0 + (t & 1) * Tile::kBytes, dl = ql + 2 * Tile::kBytes;
+      const uint32_t qc = qc0 + (t & 1) * Tile::kBytes, dc = qc + 2 * Tile::kBytes;
+      f32x16 s = {}, dp = {};
+      uint4 qf[2], df[2], vf[2], cf[2][CT];
+      const auto read = [&](int u) {
+        qf[u & 1] = W::rows(ql, 0, u);
+        df[u & 1] = W::rows(dl, 0, u);
+        vf[u & 1] = Wide<VTile>::rows(vl, 0, u);
+      };
+      const auto read_c = [&](int z) {  // dout's two units of 16 queries, then the queries', CT tiles of channels each
+        const int x = z / CS;
+#pragma unroll
+        for (int d = 0; d < CT; ++d) cf[z & 1][d] = W::cols(x < 2 ? dc : qc, 16 * (x & 1), z % CS * CT + d);
+      };
+      read(0);
+#pragma unroll
+      for (int u = 0; u < KS; ++u) {
+        if (u + 1 < KS) read(u + 1);
+        else read_c(0);
+        __builtin_amdgcn_sched_barrier(0);
+        s = mma32(qf[u & 1], k[u], s);
+        dp = mma32(df[u & 1], vf[u & 1], dp);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const f32x4 lse = *reinterpret_cast<const f32x4*>(&stats[g][t & 1][8 * x + 4 * h]);
+        const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[g][t & 1][BN + 8 * x + 4 * h]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[4 * x + i] = exp2_fast(fmaf(s[4 * x + i], cs, -lse[i]));
+          dp[4 * x + i] = s[4 * x + i] * (dp[4 * x + i] - delta[i]);
+        }
+      }
+      if (!(j1 <= p0 && (j0 > p1 - a.window || j1 < a.sinks) && i0 + BN <= sq.nq)) {
+        const int j = j0 + c, d = j - p0 - 4 * h, end = sq.nq - i0 - 4 * h;  // rows from d on, before d + window (or a sink), before end
+        const long far = j < a.sinks ? static_cast<long>(kAttnAll) * 2 : static_cast<long>(d) + a.window;
+        const int upto = static_cast<int>(min(static_cast<long>(end), far)), zero = -p0 - 4 * h;  // the row at position 0
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int r = 8 * (e / 4) + e % 4;
+          const bool see = r >= d && r < upto;
+          s[e] = see ? s[e] : 0.0f;
+          dp[e] = see && r != zero && !lone_all ? dp[e] : 0.0f;
+        }
+      }
+      Frag<NP> p;
+#pragma unroll
+      for (int z = 0; z < 4 * CS; ++z) {
+        const int x = z / CS, y = z % CS * CT;
+        if (z % CS == 0) p = wide_operand<NP>(x < 2 ? s : dp, x & 1);
+        if (z + 1 < 4 * CS) read_c(z + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int e = NP - 1; e >= 0; --e)
+#pragma unroll
+          for (int d = 0; d < CT; ++d) {
+            if (x < 2) dv[y + d] = mma32(cf[z & 1][d], p.p[e], dv[y + d]);
+            else dk[y + d] = mma32(cf[z & 1][d], p.p[e], dk[y + d]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (more && stater) stats[g][(t + 1) & 1][threadIdx.x % (2 * BN)] = st;
+  }
+  loads_done();  // (the values, where no query sees a key)
+
+  // each pair adds every fourth tile of channels, in the pairs' order
+  const int j = j0 + c;
+  float* const sums = reinterpret_cast<float*>(lds);
+  const auto join = [&](f32x16(&x)[NT], float f, void* out, float* part) {
+    lds_barrier();
+#pragma unroll
+    for (int d = 0; d < NT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x4*>(sums + (((wave * NT + d) * 4 + i) * 64 + lane) * 4) = f32x4{x[d][4 * i], x[d][4 * i + 1], x[d][4 * i + 2], x[d][4 * i + 3]};
+    lds_barrier();
+    if (j >= sq.nk) return;
+    for (int d = g; d < NT; d += G) {
+      f32x16 r[1] = {};
+#pragma unroll
+      for (int y = 0; y < G; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 add = *reinterpret_cast<const f32x4*>(sums + ((((2 * y + wave % 2) * NT + d) * 4 + i) * 64 + lane) * 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[0][4 * i + e] += add[e];
+        }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) r[0][e] *= f;
+      if (sink) {
+        const size_t at = (((static_cast<size_t>(slot) * a.hk + kh) * a.sink_tiles + w.tile) * BM + (j - jt)) * a.D;
+        wide_store_row<1>(part, at + 32 * d, r, a.D - 32 * d, h, 0, a.vec);
+      } else if (out) {
+        wide_store_row<1>(out, (static_cast<size_t>(sq.k0 + j) * a.hk + kh) * a.D + 32 * d, r, a.D - 32 * d, h, a.grad_bf16, a.vec);
+      }
+    }
+  };
+  join(dk, a.scale, a.dk, a.dk_part);
+  join(dv, 1.0f, a.dv, a.dv_part);
+}
+
+// The launches: dq in tiles of `rows` queries, then dk and dv in tiles of 64 keys with their sinks
+template <typename DQ, typename DKV>
+hipError_t attn_bwd_launch(const AttnArgs& a, int rows, hipStream_t s, DQ&& dq, DKV&& dkv) {
   if (a.dq && a.rows_q > 0) {
-    const long blocks = attn_tiles(a, 64 * MT, false) * a.h;
-    hipLaunchKernelGGL((attn_dq_kernel<T, DQ, MT, NP, VEC>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a);
+    dq(static_cast<unsigned>(attn_tiles(a, rows, false) * a.h));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (!(a.dk || a.dv) || a.rows_k == 0) return hipSuccess;
   const long sinks = a.sink_tiles > 0 ? attn_pieces(a) * a.hk * a.sink_tiles : 0;
-  const long blocks = sinks + attn_tiles(a, 64, true) * a.hk;
-  hipError_t e = timed_launch(s, [&] {
-    hipLaunchKernelGGL((attn_dkv_kernel<T, DQ, 1, NP, VEC>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, a,
-                       static_cast<unsigned>(sinks));
-  });
+  const long blocks = sinks + attn_tiles(a, kSinkRows, true) * a.hk;
+  hipError_t e = timed_launch(s, [&] { dkv(static_cast<unsigned>(blocks), static_cast<unsigned>(sinks)); });
   if (e == hipSuccess && a.sink_tiles > 0) e = launch_attn_sinks(a, s);
   return e;
 }
 
-template <typename T, int MT, int NP, bool VEC>
-hipError_t attn_bwd_vec(const AttnLaunch& l, hipStream_t s) {
-  switch (attn_dq(l.a.D)) {
-    case 32: return attn_bwd_go<T, 32, MT, NP, VEC>(l, s);
-    case 64: return attn_bwd_go<T, 64, MT, NP, VEC>(l, s);
-    case 96: return attn_bwd_go<T, 96, MT, NP, VEC>(l, s);
-    default: return attn_bwd_go<T, 128, MT, NP, VEC>(l, s);
+template <typename T, int DQ, int NP, bool VEC>
+hipError_t attn_bwd_go(const AttnArgs& a, hipStream_t s) {
+  return attn_bwd_launch(
+      a, 64, s,
+      [&](unsigned blocks) { hipLaunchKernelGGL((attn_dq_kernel<T, DQ, 1, NP, VEC>), dim3(blocks), dim3(256), 0, s, a); },
+      [&](unsigned blocks, unsigned sinks) { hipLaunchKernelGGL((attn_dkv_kernel<T, DQ, 1, NP, VEC>), dim3(blocks), dim3(256), 0, s, a, sinks); });
+}
+template <typename T, int NP, bool VEC>
+hipError_t attn_bwd_vec(const AttnArgs& a, hipStream_t s) {
+  switch (attn_dq(a.D)) {
+    case 32: return attn_bwd_go<T, 32, NP, VEC>(a, s);
+    case 64: return attn_bwd_go<T, 64, NP, VEC>(a, s);
+    case 96: return attn_bwd_go<T, 96, NP, VEC>(a, s);
+    default: return attn_bwd_go<T, 128, NP, VEC>(a, s);
   }
 }
-template <typename T, int MT, int NP>
-hipError_t attn_bwd_d(const AttnLaunch& l, hipStream_t s) {
-  return l.a.vec == 2 ? attn_bwd_vec<T, MT, NP, true>(l, s) : attn_bwd_vec<T, MT, NP, false>(l, s);
+template <typename T, int NP>
+hipError_t attn_bwd_d(const AttnArgs& a, hipStream_t s) {
+  return a.vec == 2 ? attn_bwd_vec<T, NP, true>(a, s) : attn_bwd_vec<T, NP, false>(a, s);
 }
 
-hipError_t attn_bwd_bf16(const AttnLaunch& l, hipStream_t s);
-hipError_t attn_bwd_bf16_f32(const AttnLaunch& l, hipStream_t s);
-hipError_t attn_bwd_f32(const AttnLaunch& l, hipStream_t s);
+template <int DQ, int NP>
+hipError_t attn_bwd_wide_go(const AttnArgs& a, hipStream_t s) {
+  return attn_bwd_launch(
+      a, 128, s, [&](unsigned blocks) { hipLaunchKernelGGL((attn_dq_wide_kernel<DQ, NP>), dim3(blocks), dim3(256), 0, s, a); },
+      [&](unsigned blocks, unsigned sinks) { hipLaunchKernelGGL((attn_dkv_wide_kernel<DQ, NP>), dim3(blocks), dim3(512), 0, s, a, sinks); });
+}
+template <int NP>
+hipError_t attn_bwd_wide(const AttnArgs& a, hipStream_t s) {
+  switch (attn_dq(a.D)) {
+    case 32: return attn_bwd_wide_go<32, NP>(a, s);
+    case 64: return attn_bwd_wide_go<64, NP>(a, s);
+    case 96: return attn_bwd_wide_go<96, NP>(a, s);
+    default: return attn_bwd_wide_go<128, NP>(a, s);
+  }
+}
+
+hipError_t attn_bwd_bf16(const AttnArgs& a, hipStream_t s);
+hipError_t attn_bwd_bf16_f32(const AttnArgs& a, hipStream_t s);
+hipError_t attn_bwd_f32(const AttnArgs& a, hipStream_t s);
 
 }  // namespace ssm

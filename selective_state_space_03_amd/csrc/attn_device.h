@@ -396,7 +396,7 @@ struct AttnWork {
 
 // Workgroup b's tile and head.  The heads of a key head and their tiles share its keys: they are neighbours,
 // and go to one XCD (workgroups are dealt round the 8 of them) where the (sequence, key head) pairs come out
-// even on those.  Later tiles, which see more keys without a window, come first.
+// even on those.  The longest come first: later queries, earlier keys (tile by tile over the pairs).
 // heads: workgroups per key head and tile (h / hk, or 1).
 __device__ __forceinline__ AttnWork attn_work(const AttnArgs& a, unsigned b, int rows, bool keys, int heads) {
   AttnWork w;
@@ -405,7 +405,13 @@ __device__ __forceinline__ AttnWork attn_work(const AttnArgs& a, unsigned b, int
   const unsigned pairs = a.cu_q ? a.hk : static_cast<unsigned>(a.nseq) * a.hk;
   const unsigned per = static_cast<unsigned>(slots) * heads;
   unsigned pair, r;
-  if (pairs % 8 == 0) {
+  if (keys && pairs % 8 == 0) {
+    pair = (b & 7u) + 8 * ((b >> 3) % (pairs / 8));
+    r = (b >> 3) / (pairs / 8);
+  } else if (keys) {
+    pair = b % pairs;
+    r = b / pairs;
+  } else if (pairs % 8 == 0) {
     pair = (b & 7u) + 8 * ((b >> 3) / per);
     r = (b >> 3) % per;
   } else {
@@ -413,7 +419,7 @@ __device__ __forceinline__ AttnWork attn_work(const AttnArgs& a, unsigned b, int
     r = b % per;
   }
   const unsigned kh = pair % a.hk;
-  const long x = slots - 1 - r / heads;
+  const long x = keys ? r : slots - 1 - r / heads;
   w.head = static_cast<int>(kh * heads + r % heads);
   if (a.cu_q) {
     w.tile = attn_slot(keys ? a.cu_k : a.cu_q, a.nseq, keys ? a.rows_k : a.rows_q, rows, x, &w.seq, a, keys);

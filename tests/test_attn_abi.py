@@ -105,7 +105,8 @@ BAD = (
        (_step, dict(nheads=3), 1), (_step, dict(scale=-1.0), 1), (_step, dict(window=-2), 1), (_step, dict(sinks=-1), 1),
        (_step, dict(q=None), 1), (_step, dict(o=None), 1), (_step, dict(q_stride=255), 1), (_step, dict(o_dtype=2), 1),
        (_step, dict(o=_addr(6)), 1), (_step, dict(o=_addr(10) + 2), 1), (_step, dict(q=_addr(1) + 1), 1), (_step, dict(batch=1 << 23), 2),
-       (_step, dict(workspace=None), 3), (_step, dict(workspace=_addr(20) + 4), 1), (_step, dict(workspace_bytes=64), 3)])
+       (_step, dict(table_rows=300, workspace=None), 3), (_step, dict(table_rows=300, workspace=_addr(20) + 4), 1),
+       (_step, dict(table_rows=300, workspace_bytes=64), 3)])
 
 
 @pytest.mark.parametrize("make,kw,status", BAD, ids=[f"{m.__name__}-{i}" for i, (m, _, _) in enumerate(BAD)])
