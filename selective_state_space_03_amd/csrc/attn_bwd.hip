@@ -35,8 +35,8 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(const AttnArgs a, long 
 // Adds the pieces' partial sums of the keys of the sinks' tiles, in order: a workgroup for four keys of a
 // (sequence, key head, tile)
 __global__ __launch_bounds__(256) void attn_sink_kernel(const AttnArgs a) {
-  const int parts = kSinkRows / 4, part = blockIdx.x % parts;
-  unsigned r = blockIdx.x / parts;
+  const int part = blockIdx.y;
+  unsigned r = blockIdx.x;
   const int tile = r % a.sink_tiles;
   r /= a.sink_tiles;
   const int kh = r % a.hk, s = r / a.hk;
@@ -75,7 +75,7 @@ hipError_t delta_go(const AttnArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_attn_sinks(const AttnArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(attn_sink_kernel, dim3(static_cast<unsigned>(a.nseq) * a.hk * a.sink_tiles * (kSinkRows / 4)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(attn_sink_kernel, dim3(static_cast<unsigned>(a.nseq) * a.hk * a.sink_tiles, kSinkRows / 4), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -373,22 +373,32 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
   }
 }
 
-// The queries' gradients of bf16 rows of aligned 16-byte groups in 32 x 32 tiles: 128 queries a workgroup, 32 a
-// wave, tiles of 32 keys.  Operands are read from LDS a step of products ahead, in an order that is held.
-template <int DQ, int NP>
-__global__ __launch_bounds__(256, 2) void attn_dq_wide_kernel(const AttnArgs a) {
-  constexpr int BN = 32, KS = DQ / 16, NT = DQ / 32, BM = 128;
-  using Tile = AttnTile<bf16s, BN, DQ, true>;
-  using W = Wide<Tile>;
-  __shared__ __align__(16) unsigned char lds[4][Tile::kBytes];  // keys, keys, values, values
+constexpr int wide_bwd_lds(int dq) {  // bytes: keys' workgroups need the more
+  const int row = (dq == 96 ? 128 : dq) * 2;
+  return 4 * 4 * 32 * row + 64 * row + 4 * 2 * 64 * 4;
+}
 
-  const AttnWork w = attn_work(a, blockIdx.x, BM, false, a.h / a.hk);
+// The gradients of bf16 rows of aligned 16-byte groups in 32 x 32 tiles by eight waves.  Operands are read from
+// LDS a step of products ahead, in an order that is held.
+// The queries': 32 a wave, tiles of 32 keys; the two halves of the workgroup take 128 queries of two heads that
+// share their keys, or 256 of one head.
+template <int DQ, int NP>
+__device__ __forceinline__ void attn_dq_wide(const AttnArgs& a, unsigned char* mem, unsigned block) {
+  constexpr int BN = 32, KS = DQ / 16, NT = DQ / 32;
+  using Tile = AttnTile<bf16s, BN, DQ, true, 512>;
+  using W = Wide<Tile>;
+  unsigned char(&lds)[4][Tile::kBytes] = *reinterpret_cast<unsigned char(*)[4][Tile::kBytes]>(mem);  // keys, keys, values, values
+
+  const int heads = a.h / a.hk;
+  const bool two = heads % 2 == 0;  // heads, else tiles
+  const int BM = two ? 128 : 256;
+  const AttnWork w = attn_work(a, block, BM, false, two ? heads / 2 : heads);
   if (w.tile < 0) return;
   const AttnSeq sq = w.seq;
   const int wave = uniform(threadIdx.x / 64), lane = threadIdx.x % 64, h = lane / 32, c = lane % 32;
-  const int kh = w.head / (a.h / a.hk);
+  const int head = two ? 2 * w.head + wave / 4 : w.head, kh = head / heads;
   const int off = sq.nk - sq.nq;
-  const int i0 = w.tile * BM + wave * 32;
+  const int i0 = w.tile * BM + (two ? wave % 4 : wave) * 32;
   const bf16s* const kb = static_cast<const bf16s*>(a.k) + sq.k0 * a.k_stride + static_cast<long>(kh) * a.D;
   const bf16s* const vb = static_cast<const bf16s*>(a.v) + sq.k0 * a.v_stride + static_cast<long>(kh) * a.D;
 
@@ -396,8 +406,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_wide_kernel(const AttnArgs a) 
   float lse = INFINITY, delta = 0.0f;
   {
     const int i = i0 + c;
-    const long at = (sq.q0 + i) * a.h + w.head;
-    const bf16s* const qrow = static_cast<const bf16s*>(a.q) + (sq.q0 + i) * a.q_stride + static_cast<long>(w.head) * a.D;
+    const long at = (sq.q0 + i) * a.h + head;
+    const bf16s* const qrow = static_cast<const bf16s*>(a.q) + (sq.q0 + i) * a.q_stride + static_cast<long>(head) * a.D;
     const bf16s* const drow = static_cast<const bf16s*>(a.dout) + at * a.D;
 #pragma unroll
     for (int u = 0; u < KS; ++u) {
@@ -494,33 +504,38 @@ __global__ __launch_bounds__(256, 2) void attn_dq_wide_kernel(const AttnArgs a) 
   for (int d = 0; d < NT; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) dq[d][e] *= a.scale;
-  wide_store_row<NT>(a.dq, (static_cast<size_t>(sq.q0 + i) * a.h + w.head) * a.D, dq, a.D, h, a.grad_bf16, a.vec);
+  wide_store_row<NT>(a.dq, (static_cast<size_t>(sq.q0 + i) * a.h + head) * a.D, dq, a.D, h, a.grad_bf16, a.vec);
 }
 
 // The keys' and values' gradients: 64 keys a workgroup, 32 a wave as columns, four pairs of waves that take every
 // fourth tile of 32 queries.  The keys are held in registers; the values, for which there is no room beside both
 // sums, in LDS.  The pairs' sums are added in LDS at the end.
 template <int DQ, int NP>
-__global__ __launch_bounds__(512, 2) void attn_dkv_wide_kernel(const AttnArgs a, unsigned sink_blocks) {
+__device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* mem, unsigned block, unsigned sink_blocks) {
   constexpr int BN = 32, KS = DQ / 16, NT = DQ / 32, BM = 64, G = 4;
   constexpr int CT = NT == 4 ? 2 : NT, CS = NT / CT;  // channels' tiles of a step of products
   using Tile = AttnTile<bf16s, BN, DQ, true, 128>;    // loaded by a pair of waves
   using VTile = AttnTile<bf16s, BM, DQ, true, 512>;
   using W = Wide<Tile>;
-  __shared__ __align__(16) unsigned char vlds[VTile::kBytes];
-  __shared__ __align__(16) unsigned char lds[G][4][Tile::kBytes];  // queries, queries, dout, dout; at the end sums
-  __shared__ __align__(16) float stats[G][2][2 * BN];              // lse, delta
-  static_assert(sizeof(lds) >= G * BM * DQ * 4, "room for the sums");
+  struct Lds {
+    unsigned char tiles[G][4][Tile::kBytes];  // queries, queries, dout, dout; at the end sums
+    unsigned char values[VTile::kBytes];
+    float stats[G][2][2 * BN];  // lse, delta
+  };
+  static_assert(sizeof(Lds) <= wide_bwd_lds(DQ) && sizeof(Lds::tiles) >= G * BM * DQ * 4, "room for the sums");
+  auto& lds = reinterpret_cast<Lds*>(mem)->tiles;
+  auto& vlds = reinterpret_cast<Lds*>(mem)->values;
+  auto& stats = reinterpret_cast<Lds*>(mem)->stats;
 
   const int heads = a.h / a.hk;
-  const bool sink = blockIdx.x < sink_blocks;
+  const bool sink = block < sink_blocks;
   AttnWork w;
   long slot = 0;
   int piece = 0;
   if (sink) {
     const unsigned per = static_cast<unsigned>(a.hk) * a.sink_tiles;
-    slot = blockIdx.x / per;
-    const unsigned r = blockIdx.x % per;
+    slot = block / per;
+    const unsigned r = block % per;
     w.head = r / a.sink_tiles;
     w.tile = r % a.sink_tiles;
     if (a.cu_q) {
@@ -532,7 +547,7 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_wide_kernel(const AttnArgs a,
     }
     if (piece < 0) return;
   } else {
-    w = attn_work(a, blockIdx.x - sink_blocks, BM, true, 1);
+    w = attn_work(a, block - sink_blocks, BM, true, 1);
     if (w.tile < a.sink_tiles) return;  // (also an unused slot)
   }
   const AttnSeq sq = w.seq;
@@ -712,28 +727,34 @@ __global__ __launch_bounds__(512, 2) void attn_dkv_wide_kernel(const AttnArgs a,
   join(dv, 1.0f, a.dv, a.dv_part);
 }
 
-// The launches: dq in tiles of `rows` queries, then dk and dv in tiles of 64 keys with their sinks
-template <typename DQ, typename DKV>
-hipError_t attn_bwd_launch(const AttnArgs& a, int rows, hipStream_t s, DQ&& dq, DKV&& dkv) {
-  if (a.dq && a.rows_q > 0) {
-    dq(static_cast<unsigned>(attn_tiles(a, rows, false) * a.h));
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (!(a.dk || a.dv) || a.rows_k == 0) return hipSuccess;
+// One launch of both, so that queries' workgroups fill the compute units that the keys' leave
+template <int DQ, int NP>
+__global__ __launch_bounds__(512, 2) void attn_bwd_wide_kernel(const AttnArgs a, unsigned sink_blocks, unsigned key_blocks) {
+  __shared__ __align__(16) unsigned char lds[wide_bwd_lds(DQ)];
+  if (blockIdx.x < key_blocks) attn_dkv_wide<DQ, NP>(a, lds, blockIdx.x, sink_blocks);
+  else attn_dq_wide<DQ, NP>(a, lds, blockIdx.x - key_blocks);
+}
+
+struct KeyBlocks {
+  unsigned sinks, all;  // workgroups: of the sinks' pieces, with those of 64 keys
+};
+inline KeyBlocks key_blocks(const AttnArgs& a) {
+  if (!(a.dk || a.dv) || a.rows_k == 0) return {0, 0};
   const long sinks = a.sink_tiles > 0 ? attn_pieces(a) * a.hk * a.sink_tiles : 0;
-  const long blocks = sinks + attn_tiles(a, kSinkRows, true) * a.hk;
-  hipError_t e = timed_launch(s, [&] { dkv(static_cast<unsigned>(blocks), static_cast<unsigned>(sinks)); });
-  if (e == hipSuccess && a.sink_tiles > 0) e = launch_attn_sinks(a, s);
-  return e;
+  return {static_cast<unsigned>(sinks), static_cast<unsigned>(sinks + attn_tiles(a, kSinkRows, true) * a.hk)};
 }
 
 template <typename T, int DQ, int NP, bool VEC>
 hipError_t attn_bwd_go(const AttnArgs& a, hipStream_t s) {
-  return attn_bwd_launch(
-      a, 64, s,
-      [&](unsigned blocks) { hipLaunchKernelGGL((attn_dq_kernel<T, DQ, 1, NP, VEC>), dim3(blocks), dim3(256), 0, s, a); },
-      [&](unsigned blocks, unsigned sinks) { hipLaunchKernelGGL((attn_dkv_kernel<T, DQ, 1, NP, VEC>), dim3(blocks), dim3(256), 0, s, a, sinks); });
+  if (a.dq && a.rows_q > 0) {
+    hipLaunchKernelGGL((attn_dq_kernel<T, DQ, 1, NP, VEC>), dim3(static_cast<unsigned>(attn_tiles(a, 64, false) * a.h)), dim3(256), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const KeyBlocks b = key_blocks(a);
+  if (b.all == 0) return hipSuccess;
+  const hipError_t e = timed_launch(s, [&] { hipLaunchKernelGGL((attn_dkv_kernel<T, DQ, 1, NP, VEC>), dim3(b.all), dim3(256), 0, s, a, b.sinks); });
+  return e == hipSuccess && b.sinks > 0 ? launch_attn_sinks(a, s) : e;
 }
 template <typename T, int NP, bool VEC>
 hipError_t attn_bwd_vec(const AttnArgs& a, hipStream_t s) {
@@ -751,9 +772,14 @@ hipError_t attn_bwd_d(const AttnArgs& a, hipStream_t s) {
 
 template <int DQ, int NP>
 hipError_t attn_bwd_wide_go(const AttnArgs& a, hipStream_t s) {
-  return attn_bwd_launch(
-      a, 128, s, [&](unsigned blocks) { hipLaunchKernelGGL((attn_dq_wide_kernel<DQ, NP>), dim3(blocks), dim3(256), 0, s, a); },
-      [&](unsigned blocks, unsigned sinks) { hipLaunchKernelGGL((attn_dkv_wide_kernel<DQ, NP>), dim3(blocks), dim3(512), 0, s, a, sinks); });
+  const KeyBlocks b = key_blocks(a);
+  long blocks = 0;
+  if (a.dq && a.rows_q > 0) blocks = attn_query_blocks(a);
+  blocks += b.all;
+  if (blocks == 0) return hipSuccess;
+  const hipError_t e =
+      timed_launch(s, [&] { hipLaunchKernelGGL((attn_bwd_wide_kernel<DQ, NP>), dim3(static_cast<unsigned>(blocks)), dim3(512), 0, s, a, b.sinks, b.all); });
+  return e == hipSuccess && b.sinks > 0 ? launch_attn_sinks(a, s) : e;
 }
 template <int NP>
 hipError_t attn_bwd_wide(const AttnArgs& a, hipStream_t s) {
