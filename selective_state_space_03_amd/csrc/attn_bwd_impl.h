@@ -380,6 +380,15 @@ constexpr int wide_bwd_lds(int dq) {  // bytes: keys' workgroups need the more
 
 // The gradients of bf16 rows of aligned 16-byte groups in 32 x 32 tiles by eight waves.  Operands are read from
 // LDS a step of products ahead, in an order that is held.
+// A wave's vector work goes between its own products
+template <int n>
+__device__ __forceinline__ void beside_products() {
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    __builtin_amdgcn_sched_group_barrier(8, 1, 0);  // a product
+    __builtin_amdgcn_sched_group_barrier(2, 4, 0);  // vector instructions
+  }
+}
 // The queries': 32 a wave, tiles of 32 keys; the two halves of the workgroup take 128 queries of two heads that
 // share their keys, or 256 of one head.
 template <int DQ, int NP>
@@ -450,13 +459,10 @@ __device__ __forceinline__ void attn_dq_wide(const AttnArgs& a, unsigned char* m
     if (!(j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - a.window || j0 < a.sinks))) continue;
     const uint32_t kl = k0 + (t & 1) * Tile::kBytes, vl = v0 + (t & 1) * Tile::kBytes, cl = c0 + (t & 1) * Tile::kBytes;
     f32x16 s = {}, dp = {};
-    uint4 kf[2][2], vf[2][2], cf[2][NT];
-    const auto read = [&](int st) {
+    uint4 kf[2][2], cf[2][NT];
+    const auto read = [&](int st) {  // keys, then values
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        kf[st & 1][x] = W::rows(kl, 0, 2 * st + x);
-        vf[st & 1][x] = W::rows(vl, 0, 2 * st + x);
-      }
+      for (int x = 0; x < 2; ++x) kf[st & 1][x] = st < KS / 2 ? W::rows(kl, 0, 2 * st + x) : W::rows(vl, 0, 2 * (st - KS / 2) + x);
     };
     const auto read_c = [&](int u) {
 #pragma unroll
@@ -464,37 +470,54 @@ __device__ __forceinline__ void attn_dq_wide(const AttnArgs& a, unsigned char* m
     };
     read(0);
 #pragma unroll
-    for (int st = 0; st < KS / 2; ++st) {
-      if (st + 1 < KS / 2) read(st + 1);
+    for (int st = 0; st < KS; ++st) {
+      if (st + 1 < KS) read(st + 1);
       else read_c(0);
       __builtin_amdgcn_sched_barrier(0);
+      if (st < KS / 2) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        s = mma32(kf[st & 1][x], q[2 * st + x], s);
-        dp = mma32(vf[st & 1][x], dO[2 * st + x], dp);
+        for (int x = 0; x < 2; ++x) s = mma32(kf[st & 1][x], q[2 * st + x], s);
+      } else {
+        const int u = st - KS / 2;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) dp = mma32(kf[st & 1][x], dO[2 * u + x], dp);
+#pragma unroll
+        for (int e = 16 * u / (KS / 2); e < 16 * (u + 1) / (KS / 2); ++e) {
+          s[e] = exp2_fast(fmaf(s[e], cs, -lse));
+          asm volatile("" : "+v"(s[e]));  // (here, not where it is used)
+        }
+        beside_products<2>();
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) s[e] = exp2_fast(fmaf(s[e], cs, -lse)) * (dp[e] - delta);
     if (!(j0 + BN - 1 <= p0 && (j0 > p1 - a.window || j0 + BN <= a.sinks))) {
       const int pos = p0 + c, d = pos - j0 - 4 * h, v = d - a.window, f = a.sinks - j0 - 4 * h;
       const bool lone = pos == 0 || lone_all;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int j = 8 * (e / 4) + e % 4;
-        s[e] = j <= d && (j > v || j < f) && !lone ? s[e] : 0.0f;
+        const bool see = j <= d && (j > v || j < f) && !lone;
+        s[e] = see ? s[e] : 0.0f;
+        dp[e] = see ? dp[e] : 0.0f;
       }
     }
+    Frag<NP> p[2];
+    const auto form = [&](int u) {
+#pragma unroll
+      for (int e = 8 * u; e < 8 * u + 8; ++e) s[e] *= dp[e] - delta;
+      p[u] = wide_operand<NP>(s, u);
+    };
+    form(0);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const Frag<NP> p = wide_operand<NP>(s, u);
       if (u == 0) read_c(1);
       __builtin_amdgcn_sched_barrier(0);
+      if (u == 0) form(1);
 #pragma unroll
       for (int e = NP - 1; e >= 0; --e)
 #pragma unroll
-        for (int d = 0; d < NT; ++d) dq[d] = mma32(cf[u][d], p.p[e], dq[d]);
+        for (int d = 0; d < NT; ++d) dq[d] = mma32(cf[u][d], p[u].p[e], dq[d]);
+      beside_products<NP * NT>();
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -520,7 +543,7 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
   struct Lds {
     unsigned char tiles[G][4][Tile::kBytes];  // queries, queries, dout, dout; at the end sums
     unsigned char values[VTile::kBytes];
-    float stats[G][2][2 * BN];  // lse, delta
+    float stats[G][2][2 * BN];  // lse, -delta
   };
   static_assert(sizeof(Lds) <= wide_bwd_lds(DQ) && sizeof(Lds::tiles) >= G * BM * DQ * 4, "room for the sums");
   auto& lds = reinterpret_cast<Lds*>(mem)->tiles;
@@ -600,11 +623,11 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
     Tile::load(lds0 + (t & 1) * Tile::kBytes, qs, static_cast<const bf16s*>(a.q) + sq.q0 * a.q_stride + static_cast<long>(head) * a.D, a.q_stride,
                i0, sq.nq, a.D);
     Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, ds, static_cast<const bf16s*>(a.dout) + (sq.q0 * a.h + head) * a.D, dstride, i0, sq.nq, a.D);
-    if (stater) {  // lse, then delta
+    if (stater) {  // lse, then -delta
       const int x = threadIdx.x % (2 * BN), i = i0 + x % BN;
       const long row = (sq.q0 + i) * a.h + head;
       st = x < BN ? INFINITY : 0.0f;
-      if (i < sq.nq) st = x < BN ? attn_lse2(a.lse[row]) : a.delta[row];
+      if (i < sq.nq) st = x < BN ? attn_lse2(a.lse[row]) : -a.delta[row];
     }
   };
   skip(g);
@@ -626,10 +649,11 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
     if (G * t + g < n && j0 <= p1 && j0 < sq.nk && (j1 > p0 - a.window || j0 < a.sinks)) {
       const uint32_t ql = q0 + (t & 1) * Tile::kBytes, dl = ql + 2 * Tile::kBytes;
       const uint32_t qc = qc0 + (t & 1) * Tile::kBytes, dc = qc + 2 * Tile::kBytes;
-      f32x16 s = {}, dp = {};
+      f32x16 s = {}, dp;
       uint4 qf[2], df[2], vf[2], cf[2][CT];
-      const auto read = [&](int u) {
-        qf[u & 1] = W::rows(ql, 0, u);
+      f32x4 lse[4];
+      const auto read_q = [&](int u) { qf[u & 1] = W::rows(ql, 0, u); };
+      const auto read_d = [&](int u) {
         df[u & 1] = W::rows(dl, 0, u);
         vf[u & 1] = Wide<VTile>::rows(vl, 0, u);
       };
@@ -638,25 +662,37 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
 #pragma unroll
         for (int d = 0; d < CT; ++d) cf[z & 1][d] = W::cols(x < 2 ? dc : qc, 16 * (x & 1), z % CS * CT + d);
       };
-      read(0);
+      read_q(0);
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
-        if (u + 1 < KS) read(u + 1);
-        else read_c(0);
+        if (u + 1 < KS) {
+          read_q(u + 1);
+        } else {
+          read_d(0);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            lse[x] = *reinterpret_cast<const f32x4*>(&stats[g][t & 1][8 * x + 4 * h]);
+            const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[g][t & 1][BN + 8 * x + 4 * h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dp[4 * x + i] = delta[i];
+          }
+        }
         __builtin_amdgcn_sched_barrier(0);
         s = mma32(qf[u & 1], k[u], s);
-        dp = mma32(df[u & 1], vf[u & 1], dp);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const f32x4 lse = *reinterpret_cast<const f32x4*>(&stats[g][t & 1][8 * x + 4 * h]);
-        const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[g][t & 1][BN + 8 * x + 4 * h]);
+      for (int u = 0; u < KS; ++u) {
+        if (u + 1 < KS) read_d(u + 1);
+        else read_c(0);
+        __builtin_amdgcn_sched_barrier(0);
+        dp = mma32(df[u & 1], vf[u & 1], dp);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[4 * x + i] = exp2_fast(fmaf(s[4 * x + i], cs, -lse[i]));
-          dp[4 * x + i] = s[4 * x + i] * (dp[4 * x + i] - delta[i]);
+        for (int e = 16 * u / KS; e < 16 * (u + 1) / KS; ++e) {
+          s[e] = exp2_fast(fmaf(s[e], cs, -lse[e / 4][e % 4]));
+          asm volatile("" : "+v"(s[e]));  // (here, not where it is used)
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (!(j1 <= p0 && (j0 > p1 - a.window || j1 < a.sinks) && i0 + BN <= sq.nq)) {
         const int j = j0 + c, d = j - p0 - 4 * h, end = sq.nq - i0 - 4 * h;  // rows from d on, before d + window (or a sink), before end
@@ -670,20 +706,35 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
           dp[e] = see && r != zero && !lone_all ? dp[e] : 0.0f;
         }
       }
-      Frag<NP> p;
+      uint32_t pw[2][NP][4];
+      const auto form = [&](int x, int from, int to) {  // pairs of P's units, then dS's
+#pragma unroll
+        for (int i = from; i < to; ++i) {
+          const int e = 8 * (x & 1) + 2 * i;
+          uint32_t w2[NP];
+          if (x < 2) split2<NP>(s[e], s[e + 1], w2);
+          else split2<NP>(s[e] * dp[e], s[e + 1] * dp[e + 1], w2);
+#pragma unroll
+          for (int y = 0; y < NP; ++y) pw[x & 1][y][i] = w2[y];
+        }
+      };
+      form(0, 0, 4);
 #pragma unroll
       for (int z = 0; z < 4 * CS; ++z) {
         const int x = z / CS, y = z % CS * CT;
-        if (z % CS == 0) p = wide_operand<NP>(x < 2 ? s : dp, x & 1);
         if (z + 1 < 4 * CS) read_c(z + 1);
         __builtin_amdgcn_sched_barrier(0);
+        if (x < 3) form(x + 1, 4 * (z % CS) / CS, 4 * (z % CS + 1) / CS);
 #pragma unroll
-        for (int e = NP - 1; e >= 0; --e)
+        for (int e = NP - 1; e >= 0; --e) {
+          const uint4 p = make_uint4(pw[x & 1][e][0], pw[x & 1][e][1], pw[x & 1][e][2], pw[x & 1][e][3]);
 #pragma unroll
           for (int d = 0; d < CT; ++d) {
-            if (x < 2) dv[y + d] = mma32(cf[z & 1][d], p.p[e], dv[y + d]);
-            else dk[y + d] = mma32(cf[z & 1][d], p.p[e], dk[y + d]);
+            if (x < 2) dv[y + d] = mma32(cf[z & 1][d], p, dv[y + d]);
+            else dk[y + d] = mma32(cf[z & 1][d], p, dk[y + d]);
           }
+        }
+        beside_products<NP * CT>();
         __builtin_amdgcn_sched_barrier(0);
       }
     }
