@@ -459,28 +459,29 @@ __device__ __forceinline__ void attn_dq_wide(const AttnArgs& a, unsigned char* m
     if (!(j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - a.window || j0 < a.sinks))) continue;
     const uint32_t kl = k0 + (t & 1) * Tile::kBytes, vl = v0 + (t & 1) * Tile::kBytes, cl = c0 + (t & 1) * Tile::kBytes;
     f32x16 s = {}, dp = {};
-    uint4 kf[2][2], cf[2][NT];
+    uint4 kf[3][2], cf[2][NT];
     const auto read = [&](int st) {  // keys, then values
 #pragma unroll
-      for (int x = 0; x < 2; ++x) kf[st & 1][x] = st < KS / 2 ? W::rows(kl, 0, 2 * st + x) : W::rows(vl, 0, 2 * (st - KS / 2) + x);
+      for (int x = 0; x < 2; ++x) kf[st % 3][x] = st < KS / 2 ? W::rows(kl, 0, 2 * st + x) : W::rows(vl, 0, 2 * (st - KS / 2) + x);
     };
     const auto read_c = [&](int u) {
 #pragma unroll
       for (int d = 0; d < NT; ++d) cf[u][d] = W::cols(cl, 16 * u, d);
     };
     read(0);
+    read(1);
 #pragma unroll
     for (int st = 0; st < KS; ++st) {
-      if (st + 1 < KS) read(st + 1);
-      else read_c(0);
+      if (st + 2 < KS) read(st + 2);
+      if (st == KS - 1) read_c(0);
       __builtin_amdgcn_sched_barrier(0);
       if (st < KS / 2) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) s = mma32(kf[st & 1][x], q[2 * st + x], s);
+        for (int x = 0; x < 2; ++x) s = mma32(kf[st % 3][x], q[2 * st + x], s);
       } else {
         const int u = st - KS / 2;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) dp = mma32(kf[st & 1][x], dO[2 * u + x], dp);
+        for (int x = 0; x < 2; ++x) dp = mma32(kf[st % 3][x], dO[2 * u + x], dp);
 #pragma unroll
         for (int e = 16 * u / (KS / 2); e < 16 * (u + 1) / (KS / 2); ++e) {
           s[e] = exp2_fast(fmaf(s[e], cs, -lse));
@@ -543,7 +544,7 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
   struct Lds {
     unsigned char tiles[G][4][Tile::kBytes];  // queries, queries, dout, dout; at the end sums
     unsigned char values[VTile::kBytes];
-    float stats[G][2][2 * BN];  // lse, -delta
+    float stats[G][2][2 * BN];  // -lse / scale, -delta: what the products start from
   };
   static_assert(sizeof(Lds) <= wide_bwd_lds(DQ) && sizeof(Lds::tiles) >= G * BM * DQ * 4, "room for the sums");
   auto& lds = reinterpret_cast<Lds*>(mem)->tiles;
@@ -604,7 +605,7 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
   f32x16 dk[NT], dv[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) dk[t] = dv[t] = f32x16{};
-  const float cs = a.scale * kLog2e;
+  const float cs = fmaxf(a.scale * kLog2e, 1e-30f), inv = 1.0f / cs;  // (scale may be zero)
   const bool lone_all = a.window == 1 && a.sinks == 0;
 
   const long dstride = static_cast<long>(a.h) * a.D;
@@ -623,11 +624,11 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
     Tile::load(lds0 + (t & 1) * Tile::kBytes, qs, static_cast<const bf16s*>(a.q) + sq.q0 * a.q_stride + static_cast<long>(head) * a.D, a.q_stride,
                i0, sq.nq, a.D);
     Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, ds, static_cast<const bf16s*>(a.dout) + (sq.q0 * a.h + head) * a.D, dstride, i0, sq.nq, a.D);
-    if (stater) {  // lse, then -delta
+    if (stater) {
       const int x = threadIdx.x % (2 * BN), i = i0 + x % BN;
       const long row = (sq.q0 + i) * a.h + head;
-      st = x < BN ? INFINITY : 0.0f;
-      if (i < sq.nq) st = x < BN ? attn_lse2(a.lse[row]) : -a.delta[row];
+      st = x < BN ? -INFINITY : 0.0f;
+      if (i < sq.nq) st = x < BN ? attn_lse2(a.lse[row]) * -inv : -a.delta[row];
     }
   };
   skip(g);
@@ -649,10 +650,9 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
     if (G * t + g < n && j0 <= p1 && j0 < sq.nk && (j1 > p0 - a.window || j0 < a.sinks)) {
       const uint32_t ql = q0 + (t & 1) * Tile::kBytes, dl = ql + 2 * Tile::kBytes;
       const uint32_t qc = qc0 + (t & 1) * Tile::kBytes, dc = qc + 2 * Tile::kBytes;
-      f32x16 s = {}, dp;
-      uint4 qf[2], df[2], vf[2], cf[2][CT];
-      f32x4 lse[4];
-      const auto read_q = [&](int u) { qf[u & 1] = W::rows(ql, 0, u); };
+      f32x16 s, dp;
+      uint4 qf[3], df[2], vf[2], cf[2][CT];
+      const auto read_q = [&](int u) { qf[u % 3] = W::rows(ql, 0, u); };
       const auto read_d = [&](int u) {
         df[u & 1] = W::rows(dl, 0, u);
         vf[u & 1] = Wide<VTile>::rows(vl, 0, u);
@@ -662,34 +662,37 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
 #pragma unroll
         for (int d = 0; d < CT; ++d) cf[z & 1][d] = W::cols(x < 2 ? dc : qc, 16 * (x & 1), z % CS * CT + d);
       };
-      read_q(0);
+      const auto read_stats = [&](int of, f32x16& to) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const f32x4 r = *reinterpret_cast<const f32x4*>(&stats[g][t & 1][of * BN + 8 * x + 4 * h]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) to[4 * x + i] = r[i];
+        }
+      };
+      read_stats(0, s);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) read_q(u);
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
-        if (u + 1 < KS) {
-          read_q(u + 1);
-        } else {
+        if (u + 2 < KS) read_q(u + 2);
+        if (u == KS - 1) {
           read_d(0);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            lse[x] = *reinterpret_cast<const f32x4*>(&stats[g][t & 1][8 * x + 4 * h]);
-            const f32x4 delta = *reinterpret_cast<const f32x4*>(&stats[g][t & 1][BN + 8 * x + 4 * h]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dp[4 * x + i] = delta[i];
-          }
+          read_stats(1, dp);
         }
         __builtin_amdgcn_sched_barrier(0);
-        s = mma32(qf[u & 1], k[u], s);
+        s = mma32(qf[u % 3], k[u], s);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
         if (u + 1 < KS) read_d(u + 1);
-        else read_c(0);
+        if (u == KS - 1) read_c(0);
         __builtin_amdgcn_sched_barrier(0);
         dp = mma32(df[u & 1], vf[u & 1], dp);
 #pragma unroll
         for (int e = 16 * u / KS; e < 16 * (u + 1) / KS; ++e) {
-          s[e] = exp2_fast(fmaf(s[e], cs, -lse[e / 4][e % 4]));
+          s[e] = exp2_fast(s[e] * cs);
           asm volatile("" : "+v"(s[e]));  // (here, not where it is used)
         }
         __builtin_amdgcn_sched_barrier(0);
