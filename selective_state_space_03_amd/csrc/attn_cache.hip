@@ -3,8 +3,9 @@
 // A wave takes the keys (or values) of one head of one page that the call meets: the tokens that the page
 // holds already, and the new ones.  8 bits: the page's scale is the least power of two s = 2^e with
 // max |x| <= 448 s over the new ones, or the page's own where that is larger; products with 1 / s are exact.
-// One pass over the new rows for the maximum, one (from L2) that writes their codes; a page whose scale
-// grows has its codes read and written again.
+// A page of whole 16-byte groups is read at once into registers, up to 16 of them a lane, from which the maximum
+// and the codes are formed; others pass twice over the new rows, for the maximum and (from L2) for the codes.  A
+// page whose scale grows has its codes read and written again.  Bound by the reads and writes.
 #include "attn.h"
 #include "delta_device.h"
 
@@ -130,27 +131,16 @@ __global__ __launch_bounds__(256) void attn_cache_kernel(const AttnCacheArgs a, 
   CT* const dst = static_cast<CT*>(values ? a.v_cache : a.k_cache) + ph * a.page * a.D;
   const int groups = (a.D + 7) / 8, count = (rows - keep) * groups;
 
-  if constexpr (sizeof(CT) == 1) {
+  // the page's scale, of new rows with this largest value; codes held are put to it where it grows
+  const auto scaled = [&](float top) {
     float* const scale = (values ? a.v_scale : a.k_scale) + ph;
-    float top = 0.0f;
-    for (int e = lane; e < count; e += 64) {
-      float x[8];
-      const int row = keep + e / groups, c = e % groups * 8;
-      load_in8<IN>(src + (first + row) * stride, c, a.D, a.vec, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fabsf(x[i]);
-        top = fmaxf(top, m < INFINITY ? m : 0.0f);
-      }
-    }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
     float to = ldexpf(1.0f, scale_exp(top));
     if (keep > 0) {
       const float had = *scale;
-      if (had >= to) {
-        to = had;
-      } else {  // the codes held are put to the larger scale
+      if (had >= to) return had;
+      if constexpr (sizeof(CT) == 1) {
         const float f = had / to;
         for (int e = lane; e < keep * groups; e += 64) {
           const int row = e / groups, c = e % groups * 8, left = a.D - c;
@@ -163,23 +153,73 @@ __global__ __launch_bounds__(256) void attn_cache_kernel(const AttnCacheArgs a, 
         }
       }
     }
-    const float inv = 1.0f / to;
-    for (int e = lane; e < count; e += 64) {
-      float x[8];
-      const int row = keep + e / groups, c = e % groups * 8;
-      load_in8<IN>(src + (first + row) * stride, c, a.D, a.vec, x);
+    if (lane == 0) *scale = to;
+    return to;
+  };
+  const auto largest = [&](const float (&x)[8], float top) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float m = fabsf(x[i]);
+      top = fmaxf(top, m < INFINITY ? m : 0.0f);
+    }
+    return top;
+  };
+  const auto put = [&](int row, int c, float (&x)[8], float inv) {
+    CT* const p = dst + static_cast<long>(row) * a.D + c;
+    if constexpr (sizeof(CT) == 1) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] *= inv;
-      put_codes(dst + static_cast<long>(row) * a.D + c, codes_of(x), a.D - c, a.vec);
+      put_codes(p, codes_of(x), a.D - c, a.vec);
+    } else {
+      put_row(p, x, a.D - c, a.vec);
     }
-    if (lane == 0) *scale = to;
-  } else {
+  };
+
+  constexpr int kHold = sizeof(IN) == 2 ? 16 : 8;
+  const int per = 64 / groups;  // rows of the wave
+  if (a.vec && per * groups == 64 && rows - keep <= kHold * per) {
+    const int r0 = keep + lane / groups, c = lane % groups * 8;
+    Row8<IN> held_rows[kHold];
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (keep + i * per < rows) held_rows[i].load(src + (first + min(r0 + i * per, rows - 1)) * stride, c, a.D, true);
+    float inv = 1.0f;
+    if constexpr (sizeof(CT) == 1) {
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) {
+        if (keep + i * per >= rows) continue;
+        float x[8];
+        held_rows[i].get(8, x);
+        top = largest(x, top);
+      }
+      inv = 1.0f / scaled(top);
+    }
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      if (r0 + i * per >= rows) continue;
+      float x[8];
+      held_rows[i].get(8, x);
+      put(r0 + i * per, c, x, inv);
+    }
+    return;
+  }
+
+  float inv = 1.0f;
+  if constexpr (sizeof(CT) == 1) {
+    float top = 0.0f;
     for (int e = lane; e < count; e += 64) {
       float x[8];
-      const int row = keep + e / groups, c = e % groups * 8;
-      load_in8<IN>(src + (first + row) * stride, c, a.D, a.vec, x);
-      put_row(dst + static_cast<long>(row) * a.D + c, x, a.D - c, a.vec);
+      load_in8<IN>(src + (first + keep + e / groups) * stride, e % groups * 8, a.D, a.vec, x);
+      top = largest(x, top);
     }
+    inv = 1.0f / scaled(top);
+  }
+  for (int e = lane; e < count; e += 64) {
+    float x[8];
+    const int row = keep + e / groups, c = e % groups * 8;
+    load_in8<IN>(src + (first + row) * stride, c, a.D, a.vec, x);
+    put(row, c, x, inv);
   }
 }
 
