@@ -48,9 +48,9 @@ inline long attn_pieces(const AttnArgs& a) {
   return a.cu_q ? a.lq / a.span + a.nseq : static_cast<long>(a.nseq) * ((a.lq + a.span - 1) / a.span);
 }
 constexpr int kSinkRows = 64;  // keys of a tile of the backward pass
-// Workgroups of its queries, each two heads of 128 queries or one of 256
-inline long attn_query_blocks(const AttnArgs& a) {
-  return a.h / a.hk % 2 == 0 ? attn_tiles(a, 128, false) * a.h / 2 : attn_tiles(a, 256, false) * a.h;
+// Workgroups of its queries, each two heads of `rows` queries or one of twice as many
+inline long attn_query_blocks(const AttnArgs& a, int rows) {
+  return a.h / a.hk % 2 == 0 ? attn_tiles(a, rows, false) * a.h / 2 : attn_tiles(a, 2 * rows, false) * a.h;
 }
 hipError_t launch_attn_fwd(const AttnLaunch& l, hipStream_t s);
 hipError_t launch_attn_bwd(const AttnLaunch& l, hipStream_t s);

@@ -228,14 +228,14 @@ BwdWs bwd_ws(const P* p) {
   w.total = at;
   return w;
 }
-// Workgroups of keys, pieces and queries may stand in one launch, of 512 threads.
+// Workgroups of keys, pieces and queries stand in one launch, of 512 threads each.
 bool bwd_fields(const ssm_attn_bwd_params_t* p) {
   if (!attn_fields(p)) return false;
   ssm::AttnLaunch l{};
   attn_plan(p, l);
   sink_plan(p, l.a);
   const long most = (1L << 23) - 1, sinks = l.a.sink_tiles > 0 ? std::max<long>(ssm::attn_pieces(l.a), l.a.nseq) * l.a.sink_tiles : 0;
-  return sinks + ssm::attn_tiles(l.a, ssm::kSinkRows, true) <= (most - ssm::attn_query_blocks(l.a)) / p->nkheads;
+  return sinks + ssm::attn_tiles(l.a, ssm::kSinkRows, true) <= (most - ssm::attn_query_blocks(l.a, 64)) / p->nkheads;
 }
 
 ssm_status_t attn_bwd_check(const ssm_attn_bwd_params_t* p) {

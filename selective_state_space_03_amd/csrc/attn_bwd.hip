@@ -80,7 +80,7 @@ hipError_t launch_attn_sinks(const AttnArgs& a, hipStream_t s) {
 }
 
 hipError_t attn_bwd_bf16(const AttnArgs& a, hipStream_t s) {
-  return a.vec == 2 ? attn_bwd_wide<2>(a, s) : attn_bwd_d<bf16s, 2>(a, s);
+  return a.vec == 2 ? attn_bwd_wide<2>(a, s) : attn_bwd_vec<bf16s, 2, false>(a, s);
 }
 
 hipError_t launch_attn_bwd(const AttnLaunch& l, hipStream_t s) {

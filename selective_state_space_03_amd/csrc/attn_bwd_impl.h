@@ -14,21 +14,30 @@ namespace ssm {
 
 __device__ __forceinline__ float attn_lse2(float lse) { return lse == -INFINITY ? INFINITY : lse * kLog2e; }
 
-template <typename T, int DQ, int MT, int NP, bool VEC>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
-  using E = AttnEl<T>;
-  constexpr int BN = E::kTile, KS = DQ / E::kUnit, NT = DQ / 16, BM = 64 * MT;
-  constexpr int PU = sizeof(T) == 2 ? 2 : 1, UN = BN / 16 / PU;
-  using Tile = AttnTile<T, BN, DQ, VEC>;
-  __shared__ __align__(16) unsigned char lds[2][2 * Tile::kBytes];  // keys, values
+// Bytes of LDS: two tiles of queries and dout, with their statistics, for each half of a workgroup of keys
+template <typename T, int DQ>
+constexpr int kNarrowBwdLds = 4 * (2 * AttnTile<T, AttnEl<T>::kTile, DQ, true>::kBytes + 8 * AttnEl<T>::kTile);
 
-  const AttnWork w = attn_work(a, blockIdx.x, BM, false, a.h / a.hk);
+// The queries' gradients: a wave takes 16 queries as columns; the two halves of the workgroup 64 queries of two
+// heads that share their keys, or 128 of one head.
+template <typename T, int DQ, int NP, bool VEC>
+__device__ __forceinline__ void attn_dq(const AttnArgs& a, unsigned char* mem, unsigned block) {
+  using E = AttnEl<T>;
+  constexpr int MT = 1, BN = E::kTile, KS = DQ / E::kUnit, NT = DQ / 16;
+  constexpr int PU = sizeof(T) == 2 ? 2 : 1, UN = BN / 16 / PU;
+  using Tile = AttnTile<T, BN, DQ, VEC, 512>;
+  unsigned char(&lds)[2][2 * Tile::kBytes] = *reinterpret_cast<unsigned char(*)[2][2 * Tile::kBytes]>(mem);  // keys, values
+
+  const int heads = a.h / a.hk;
+  const bool two = heads % 2 == 0;  // heads, else tiles
+  const int BM = two ? 64 : 128;
+  const AttnWork w = attn_work(a, block, BM, false, two ? heads / 2 : heads);
   if (w.tile < 0) return;
   const AttnSeq sq = w.seq;
-  const int lane = threadIdx.x % 64, g = lane / 16, c = lane % 16;
-  const int kh = w.head / (a.h / a.hk);
+  const int wave = uniform(threadIdx.x / 64), lane = threadIdx.x % 64, g = lane / 16, c = lane % 16;
+  const int head = two ? 2 * w.head + wave / 4 : w.head, kh = head / heads;
   const int off = sq.nk - sq.nq;
-  const int i0 = w.tile * BM + threadIdx.x / 64 * (16 * MT);
+  const int i0 = w.tile * BM + (two ? wave % 4 : wave) * 16;
   const T* const kb = static_cast<const T*>(a.k) + sq.k0 * a.k_stride + static_cast<long>(kh) * a.D;
   const T* const vb = static_cast<const T*>(a.v) + sq.k0 * a.v_stride + static_cast<long>(kh) * a.D;
 
@@ -37,8 +46,8 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int i = i0 + 16 * m + c;
-    const long row = (sq.q0 + i) * a.h + w.head;
-    const T* qrow = static_cast<const T*>(a.q) + (sq.q0 + i) * a.q_stride + static_cast<long>(w.head) * a.D;
+    const long row = (sq.q0 + i) * a.h + head;
+    const T* qrow = static_cast<const T*>(a.q) + (sq.q0 + i) * a.q_stride + static_cast<long>(head) * a.D;
     const T* drow = static_cast<const T*>(a.dout) + row * a.D;
     lse[m] = INFINITY;
     delta[m] = 0.0f;
@@ -162,32 +171,36 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(const AttnArgs a) {
     for (int d = 0; d < NT; ++d)
 #pragma unroll
       for (int r = 0; r < 4; ++r) dq[m][d][r] *= a.scale;
-    attn_store_row<NT>(a.dq, (static_cast<size_t>(sq.q0 + i) * a.h + w.head) * a.D, dq[m], a.D, g, a.grad_bf16, a.vec);
+    attn_store_row<NT>(a.dq, (static_cast<size_t>(sq.q0 + i) * a.h + head) * a.D, dq[m], a.D, g, a.grad_bf16, a.vec);
   }
 }
 
-// A workgroup takes 64 MT keys of one key head, a wave 16 MT of them as columns, and walks the tiles of
-// queries that see them, head by head of the key head's (their sum stays in registers).
+// The keys' and values' gradients: a workgroup takes 64 keys of one key head, a wave 16 of them as columns, and
+// walks the tiles of queries that see them, head by head of the key head's (their sum stays in registers); each
+// half of the workgroup takes every second tile, and their sums are added in LDS at the end.
 // The tiles that hold sinks are seen by every later query.  Where they are few (a.sink_tiles), the queries
 // are cut into pieces of a.span for them, the first workgroups of the launch, whose partial sums
 // attn_sink_kernel adds up.
-template <typename T, int DQ, int MT, int NP, bool VEC>
-__global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsigned sink_blocks) {
+template <typename T, int DQ, int NP, bool VEC>
+__device__ __forceinline__ void attn_dkv(const AttnArgs& a, unsigned char* mem, unsigned block, unsigned sink_blocks) {
   using E = AttnEl<T>;
-  constexpr int BN = E::kTile, KS = DQ / E::kUnit, NT = DQ / 16, BM = 64 * MT;
+  constexpr int MT = 1, BN = E::kTile, KS = DQ / E::kUnit, NT = DQ / 16, BM = kSinkRows;
   constexpr int PU = sizeof(T) == 2 ? 2 : 1, UN = BN / 16 / PU;
-  using Tile = AttnTile<T, BN, DQ, VEC>;
-  __shared__ __align__(16) unsigned char lds[2][2 * Tile::kBytes + 8 * BN];
+  using Tile = AttnTile<T, BN, DQ, VEC, 256>;  // loaded by a half
+  constexpr int kBuf = 2 * Tile::kBytes + 8 * BN;  // queries, dout, lse, delta
+  static_assert(4 * kBuf <= kNarrowBwdLds<T, DQ> && 8 * BM * DQ <= kNarrowBwdLds<T, DQ>, "room for the tiles, for the sums");
+  const int wave = uniform(threadIdx.x / 64), half = wave / 4, x256 = threadIdx.x % 256;
+  unsigned char(&lds)[2][kBuf] = reinterpret_cast<unsigned char(*)[2][kBuf]>(mem)[half];
 
   const int heads = a.h / a.hk;
-  const bool sink = blockIdx.x < sink_blocks;
+  const bool sink = block < sink_blocks;
   AttnWork w;
   long slot = 0;
   int piece = 0;
   if (sink) {
     const unsigned per = static_cast<unsigned>(a.hk) * a.sink_tiles;
-    slot = blockIdx.x / per;
-    const unsigned r = blockIdx.x % per;
+    slot = block / per;
+    const unsigned r = block % per;
     w.head = r / a.sink_tiles;
     w.tile = r % a.sink_tiles;
     if (a.cu_q) {
@@ -199,14 +212,14 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
     }
     if (piece < 0) return;
   } else {
-    w = attn_work(a, blockIdx.x - sink_blocks, BM, true, 1);
+    w = attn_work(a, block - sink_blocks, BM, true, 1);
     if (w.tile < a.sink_tiles) return;  // (also an unused slot)
   }
   const AttnSeq sq = w.seq;
   const int lane = threadIdx.x % 64, g = lane / 16, c = lane % 16;
   const int kh = w.head;
   const int off = sq.nk - sq.nq;
-  const int jt = w.tile * BM, j0 = jt + threadIdx.x / 64 * (16 * MT), j1 = j0 + 16 * MT - 1;
+  const int jt = w.tile * BM, j0 = jt + wave % 4 * 16, j1 = j0 + 16 * MT - 1;
 
   uint4 k[MT][KS], v[MT][KS];
 #pragma unroll
@@ -234,7 +247,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
   if (jt >= sq.nk) hi = -1;
   const int first = static_cast<int>(lo / BN);
   const int per = hi < lo ? 0 : static_cast<int>(hi / BN) + 1 - first;  // tiles of a head
-  const int n = per * heads;
+  const int n = per * heads, steps = (n + 1) / 2;  // of both halves, of one
 
   f32x4 dk[MT][NT], dv[MT][NT];
 #pragma unroll
@@ -249,7 +262,7 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
   const long dstride = static_cast<long>(a.h) * a.D;
   const typename Tile::Source qs = Tile::source(a.q_stride, a.D), ds = Tile::source(dstride, a.D);
   const auto load = [&](int t) {
-    const int head = kh * heads + t / per, i0 = (first + t % per) * BN;
+    const int x = 2 * t + half, head = kh * heads + x / per, i0 = (first + x % per) * BN;
     const T* const qb = static_cast<const T*>(a.q) + sq.q0 * a.q_stride + static_cast<long>(head) * a.D;
     const T* const db = static_cast<const T*>(a.dout) + (sq.q0 * a.h + head) * a.D;
     if constexpr (VEC) {
@@ -259,11 +272,11 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
       Tile::fetch(qb, a.q_stride, i0, sq.nq, a.D, a.vec, qr);
       Tile::fetch(db, dstride, i0, sq.nq, a.D, a.vec, dr);
     }
-    if (threadIdx.x < 2 * BN) {  // lse, then delta
-      const int i = i0 + threadIdx.x % BN;
+    if (x256 < 2 * BN) {  // lse, then delta
+      const int i = i0 + x256 % BN;
       const long row = (sq.q0 + i) * a.h + head;
-      st = threadIdx.x < BN ? INFINITY : 0.0f;
-      if (i < sq.nq) st = threadIdx.x < BN ? attn_lse2(a.lse[row]) : a.delta[row];
+      st = x256 < BN ? INFINITY : 0.0f;
+      if (i < sq.nq) st = x256 < BN ? attn_lse2(a.lse[row]) : a.delta[row];
     }
   };
   const auto put = [&](int t) {
@@ -272,21 +285,22 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
       Tile::put(to, qr);
       Tile::put(to + Tile::kBytes, dr);
     }
-    if (threadIdx.x < 2 * BN) reinterpret_cast<float*>(to + 2 * Tile::kBytes)[threadIdx.x] = st;
+    if (x256 < 2 * BN) reinterpret_cast<float*>(to + 2 * Tile::kBytes)[x256] = st;
   };
-  if (n > 0) {
+  if (half < n) {
     load(0);
     put(0);
   }
-  for (int t = 0; t < n; ++t) {
+  for (int t = 0; t < steps; ++t) {
     if constexpr (VEC) loads_done();
     lds_barrier();
-    if (t + 1 < n) load(t + 1);
+    const bool more = 2 * (t + 1) + half < n;
+    if (more) load(t + 1);
     const unsigned char* const ql = lds[t & 1];
     const unsigned char* const dl = ql + Tile::kBytes;
     const float* const sl = reinterpret_cast<const float*>(ql + 2 * Tile::kBytes);
-    const int i0 = (first + t % per) * BN, p0 = off + i0, p1 = p0 + BN - 1;
-    const bool some = j0 <= p1 && j0 < sq.nk && (j1 > p0 - a.window || j0 < a.sinks);
+    const int i0 = (first + (2 * t + half) % per) * BN, p0 = off + i0, p1 = p0 + BN - 1;
+    const bool some = 2 * t + half < n && j0 <= p1 && j0 < sq.nk && (j1 > p0 - a.window || j0 < a.sinks);
     if (some) {
       const bool whole = j1 <= p0 && (j0 > p1 - a.window || j1 < a.sinks) && i0 + BN <= sq.nq;
 #pragma unroll
@@ -351,26 +365,45 @@ __global__ __launch_bounds__(256, 2) void attn_dkv_kernel(const AttnArgs a, unsi
         }
       }
     }
-    if (t + 1 < n) put(t + 1);
+    if (more) put(t + 1);
   }
+
+  // the second half's sums in LDS: [wave][dk, dv][tile of channels][lane]
+  f32x4* const sums = reinterpret_cast<f32x4*>(mem) + wave % 4 * (2 * NT * 64) + lane;
+  lds_barrier();
+  if (half == 1) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int j = j0 + 16 * m + c;
-    if (j >= sq.nk) continue;
-#pragma unroll
-    for (int d = 0; d < NT; ++d)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dk[m][d][r] *= a.scale;
-    if (sink) {
-      const size_t at = (((static_cast<size_t>(slot) * a.hk + kh) * a.sink_tiles + w.tile) * BM + (j - jt)) * a.D;
-      attn_store_row<NT>(a.dk_part, at, dk[m], a.D, g, 0, a.vec);
-      attn_store_row<NT>(a.dv_part, at, dv[m], a.D, g, 0, a.vec);
-    } else {
-      const size_t at = (static_cast<size_t>(sq.k0 + j) * a.hk + kh) * a.D;
-      if (a.dk) attn_store_row<NT>(a.dk, at, dk[m], a.D, g, a.grad_bf16, a.vec);
-      if (a.dv) attn_store_row<NT>(a.dv, at, dv[m], a.D, g, a.grad_bf16, a.vec);
+    for (int d = 0; d < NT; ++d) {
+      sums[d * 64] = dk[0][d];
+      sums[(NT + d) * 64] = dv[0][d];
     }
   }
+  lds_barrier();
+  if (half == 1) return;
+#pragma unroll
+  for (int d = 0; d < NT; ++d) {
+    dk[0][d] = (dk[0][d] + sums[d * 64]) * a.scale;
+    dv[0][d] += sums[(NT + d) * 64];
+  }
+  const int j = j0 + c;
+  if (j >= sq.nk) return;
+  if (sink) {
+    const size_t at = (((static_cast<size_t>(slot) * a.hk + kh) * a.sink_tiles + w.tile) * BM + (j - jt)) * a.D;
+    attn_store_row<NT>(a.dk_part, at, dk[0], a.D, g, 0, a.vec);
+    attn_store_row<NT>(a.dv_part, at, dv[0], a.D, g, 0, a.vec);
+  } else {
+    const size_t at = (static_cast<size_t>(sq.k0 + j) * a.hk + kh) * a.D;
+    if (a.dk) attn_store_row<NT>(a.dk, at, dk[0], a.D, g, a.grad_bf16, a.vec);
+    if (a.dv) attn_store_row<NT>(a.dv, at, dv[0], a.D, g, a.grad_bf16, a.vec);
+  }
+}
+
+// One launch of both, so that queries' workgroups fill the compute units that the keys' leave
+template <typename T, int DQ, int NP, bool VEC>
+__global__ __launch_bounds__(512, 2) void attn_bwd_kernel(const AttnArgs a, unsigned sink_blocks, unsigned key_blocks) {
+  __shared__ __align__(16) unsigned char lds[kNarrowBwdLds<T, DQ>];
+  if (blockIdx.x < key_blocks) attn_dkv<T, DQ, NP, VEC>(a, lds, blockIdx.x, sink_blocks);
+  else attn_dq<T, DQ, NP, VEC>(a, lds, blockIdx.x - key_blocks);
 }
 
 constexpr int wide_bwd_lds(int dq) {  // bytes: keys' workgroups need the more
@@ -798,25 +831,24 @@ inline KeyBlocks key_blocks(const AttnArgs& a) {
   return {static_cast<unsigned>(sinks), static_cast<unsigned>(sinks + attn_tiles(a, kSinkRows, true) * a.hk)};
 }
 
-template <typename T, int DQ, int NP, bool VEC>
-hipError_t attn_bwd_go(const AttnArgs& a, hipStream_t s) {
-  if (a.dq && a.rows_q > 0) {
-    hipLaunchKernelGGL((attn_dq_kernel<T, DQ, 1, NP, VEC>), dim3(static_cast<unsigned>(attn_tiles(a, 64, false) * a.h)), dim3(256), 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
+// One launch of a kernel whose query workgroups take `rows` queries, and of the sinks' pieces
+template <typename K>
+hipError_t attn_bwd_launch(const AttnArgs& a, int rows, K* kernel, hipStream_t s) {
   const KeyBlocks b = key_blocks(a);
-  if (b.all == 0) return hipSuccess;
-  const hipError_t e = timed_launch(s, [&] { hipLaunchKernelGGL((attn_dkv_kernel<T, DQ, 1, NP, VEC>), dim3(b.all), dim3(256), 0, s, a, b.sinks); });
+  const long blocks = b.all + (a.dq && a.rows_q > 0 ? attn_query_blocks(a, rows) : 0);
+  if (blocks == 0) return hipSuccess;
+  const hipError_t e =
+      timed_launch(s, [&] { hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(512), 0, s, a, b.sinks, b.all); });
   return e == hipSuccess && b.sinks > 0 ? launch_attn_sinks(a, s) : e;
 }
+
 template <typename T, int NP, bool VEC>
 hipError_t attn_bwd_vec(const AttnArgs& a, hipStream_t s) {
   switch (attn_dq(a.D)) {
-    case 32: return attn_bwd_go<T, 32, NP, VEC>(a, s);
-    case 64: return attn_bwd_go<T, 64, NP, VEC>(a, s);
-    case 96: return attn_bwd_go<T, 96, NP, VEC>(a, s);
-    default: return attn_bwd_go<T, 128, NP, VEC>(a, s);
+    case 32: return attn_bwd_launch(a, 64, attn_bwd_kernel<T, 32, NP, VEC>, s);
+    case 64: return attn_bwd_launch(a, 64, attn_bwd_kernel<T, 64, NP, VEC>, s);
+    case 96: return attn_bwd_launch(a, 64, attn_bwd_kernel<T, 96, NP, VEC>, s);
+    default: return attn_bwd_launch(a, 64, attn_bwd_kernel<T, 128, NP, VEC>, s);
   }
 }
 template <typename T, int NP>
@@ -824,24 +856,13 @@ hipError_t attn_bwd_d(const AttnArgs& a, hipStream_t s) {
   return a.vec == 2 ? attn_bwd_vec<T, NP, true>(a, s) : attn_bwd_vec<T, NP, false>(a, s);
 }
 
-template <int DQ, int NP>
-hipError_t attn_bwd_wide_go(const AttnArgs& a, hipStream_t s) {
-  const KeyBlocks b = key_blocks(a);
-  long blocks = 0;
-  if (a.dq && a.rows_q > 0) blocks = attn_query_blocks(a);
-  blocks += b.all;
-  if (blocks == 0) return hipSuccess;
-  const hipError_t e =
-      timed_launch(s, [&] { hipLaunchKernelGGL((attn_bwd_wide_kernel<DQ, NP>), dim3(static_cast<unsigned>(blocks)), dim3(512), 0, s, a, b.sinks, b.all); });
-  return e == hipSuccess && b.sinks > 0 ? launch_attn_sinks(a, s) : e;
-}
 template <int NP>
 hipError_t attn_bwd_wide(const AttnArgs& a, hipStream_t s) {
   switch (attn_dq(a.D)) {
-    case 32: return attn_bwd_wide_go<32, NP>(a, s);
-    case 64: return attn_bwd_wide_go<64, NP>(a, s);
-    case 96: return attn_bwd_wide_go<96, NP>(a, s);
-    default: return attn_bwd_wide_go<128, NP>(a, s);
+    case 32: return attn_bwd_launch(a, 128, attn_bwd_wide_kernel<32, NP>, s);
+    case 64: return attn_bwd_launch(a, 128, attn_bwd_wide_kernel<64, NP>, s);
+    case 96: return attn_bwd_launch(a, 128, attn_bwd_wide_kernel<96, NP>, s);
+    default: return attn_bwd_launch(a, 128, attn_bwd_wide_kernel<128, NP>, s);
   }
 }
 

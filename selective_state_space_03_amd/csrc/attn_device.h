@@ -156,6 +156,7 @@ struct AttnTile {
   }
   // the same through registers, rows from n on as zeros
   static __device__ __forceinline__ void fetch(const T* base, long stride, int j0, int n, int D, int vec, uint4 (&r)[kPer]) {
+    if (kUse < kThreads && threadIdx.x % kThreads >= kUse) return;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int x = threadIdx.x % kThreads + kUse * i, row = j0 + x / kSlots;
@@ -164,8 +165,9 @@ struct AttnTile {
     }
   }
   static __device__ __forceinline__ void put(unsigned char* lds, const uint4 (&r)[kPer]) {
+    if (kUse < kThreads && threadIdx.x % kThreads >= kUse) return;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) *reinterpret_cast<uint4*>(lds + (threadIdx.x + kUse * i) * 16) = r[i];
+    for (int i = 0; i < kPer; ++i) *reinterpret_cast<uint4*>(lds + (threadIdx.x % kThreads + kUse * i) * 16) = r[i];
   }
   // rows row0 .. row0 + 15 (row0 a multiple of 16), channels of unit u
   static __device__ __forceinline__ uint4 rows(const unsigned char* lds, int row0, int u, int lane) {

@@ -152,4 +152,4 @@ def test_workspace_sizes(L):
     assert size(_bwd(d_head=200)) == 0 and size(_bwd(struct_size=4)) == 0
     assert L.ssm_attn_decode_workspace_size(ctypes.byref(_step(d_head=200))) == 0
     # sizes past 32 bits
-    assert size(_bwd(batch=1, num_seqs=1, seqlen=1 << 26, seqlen_k=1 << 26, nkheads=1, nheads=15)) >= 1 << 32
+    assert size(_bwd(batch=1, num_seqs=1, seqlen=1 << 26, seqlen_k=1 << 20, nkheads=1, nheads=15, window=1000)) >= 1 << 32
