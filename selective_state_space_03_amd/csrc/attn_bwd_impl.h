@@ -422,6 +422,13 @@ __device__ __forceinline__ void beside_products() {
     __builtin_amdgcn_sched_group_barrier(2, 4, 0);  // vector instructions
   }
 }
+// Ahead of a branch between products and the first use of their results: there the compiler counts the wait
+// states (11 behind a product of 32 x 32 x 16) along one path only.
+__device__ __forceinline__ void products_done() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 10");
+  __builtin_amdgcn_sched_barrier(0);
+}
 // The queries': 32 a wave, tiles of 32 keys; the two halves of the workgroup take 128 queries of two heads that
 // share their keys, or 256 of one head.
 template <int DQ, int NP>
@@ -524,6 +531,7 @@ __device__ __forceinline__ void attn_dq_wide(const AttnArgs& a, unsigned char* m
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    products_done();
     if (!(j0 + BN - 1 <= p0 && (j0 > p1 - a.window || j0 + BN <= a.sinks))) {
       const int pos = p0 + c, d = pos - j0 - 4 * h, v = d - a.window, f = a.sinks - j0 - 4 * h;
       const bool lone = pos == 0 || lone_all;
@@ -730,6 +738,7 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      products_done();
       if (!(j1 <= p0 && (j0 > p1 - a.window || j1 < a.sinks) && i0 + BN <= sq.nq)) {
         const int j = j0 + c, d = j - p0 - 4 * h, end = sq.nq - i0 - 4 * h;  // rows from d on, before d + window (or a sink), before end
         const long far = j < a.sinks ? static_cast<long>(kAttnAll) * 2 : static_cast<long>(d) + a.window;
