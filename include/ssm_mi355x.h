@@ -695,7 +695,7 @@ ssm_status_t ssm_block_norm_bwd_check(const ssm_block_norm_bwd_params_t *p);
  *             (query i is at i + Lk - L); with fewer, the first see nothing
  *   window    keys that a query sees at most besides the sinks, itself among them; 0: all
  *   sinks     first keys of the sequence that stay visible behind the window
- *   scale     finite, not negative
+ *   scale     finite, not negative (less than 1e-30: the scores count as those of 1e-30)
  *   cu_seqlens (num_seqs + 1) int32 in DEVICE memory or NULL: packed sequences, Bt = 1,
  *             sequence i holds the queries [cu[i], cu[i+1]); offsets rise from 0 to L (empty
  *             sequences allowed).  They are not read on the host; offsets out of range are
@@ -864,8 +864,10 @@ size_t ssm_params_sizeof(int32_t which);
  * full-segment scan kernel of ssm_scan_fwd; the walk over the chunks of
  * ssm_delta_chunk_fwd, without the kernel that forms its operands; the gradients'
  * kernel of ssm_delta_chunk_bwd, without operands, walks and the sums of shared
- * heads; the row kernel of ssm_block_norm_bwd, without the column sums; all of
- * ssm_layer_fwd; the main or only kernel of the others.  The events are only
+ * heads; the row kernel of ssm_block_norm_bwd, without the column sums; the
+ * gradients' kernel of ssm_attn_bwd, without dout.o and the sums of the sinks'
+ * pieces; the kernel over the cache of ssm_attn_decode_step, without the join of
+ * its parts; all of ssm_layer_fwd; the main or only kernel of the others.  The events are only
  * recorded, never created, synchronised or destroyed by the library. */
 void ssm_set_timing_events(void *start, void *stop);
 

@@ -646,7 +646,7 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
   f32x16 dk[NT], dv[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) dk[t] = dv[t] = f32x16{};
-  const float cs = fmaxf(a.scale * kLog2e, 1e-30f), inv = 1.0f / cs;  // (scale may be zero)
+  const float cs = attn_log2_scale(a.scale), inv = 1.0f / cs;
   const bool lone_all = a.window == 1 && a.sinks == 0;
 
   const long dstride = static_cast<long>(a.h) * a.D;

@@ -350,6 +350,9 @@ __device__ __forceinline__ void wide_store_row(void* out, size_t at, const f32x1
       attn_store4(out, at, x[t][4 * i], x[t][4 * i + 1], x[t][4 * i + 2], x[t][4 * i + 3], 32 * t + 8 * i + 4 * h, D, bf16, vec);
 }
 
+// Factor of the scores in powers of two.  Not zero: a score of -infinity (a key that is not seen) has to stay that.
+__device__ __forceinline__ float attn_log2_scale(float scale) { return fmaxf(scale * kLog2e, 1e-30f); }
+
 struct AttnSeq {
   long q0, k0;  // first query and key
   int nq, nk;

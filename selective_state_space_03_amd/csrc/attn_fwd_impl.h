@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
 #pragma unroll
     for (int t = 0; t < NT; ++t) o[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  const float cs = a.scale * kLog2e;
+  const float cs = attn_log2_scale(a.scale);
   const int p0 = off + i0, p1 = p0 + 16 * MT - 1;  // the wave's positions
 
   uint4 kr[VEC ? 1 : Tile::kPer], vr[VEC ? 1 : Tile::kPer];
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(256, 3) void attn_fwd_wide_kernel(const AttnArgs a,
 #pragma unroll
   for (int t = 0; t < NT; ++t) o[t] = f32x16{};
   float mx = -INFINITY, l = 0.0f;
-  const float cs = a.scale * kLog2e;
+  const float cs = attn_log2_scale(a.scale);
   const int p0 = off + i0, p1 = p0 + 31;  // the wave's positions
 
   const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
@@ -391,7 +391,7 @@ __global__ __launch_bounds__(512, 2) void attn_fwd_long_kernel(const AttnArgs a,
 #pragma unroll
   for (int t = 0; t < NT; ++t) o[t] = f32x16{};
   float mx = -INFINITY, l = 0.0f;
-  const float cs = a.scale * kLog2e;
+  const float cs = attn_log2_scale(a.scale);
   const int p0 = off + i0, p1 = p0 + 31;  // the wave's positions
 
   const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);

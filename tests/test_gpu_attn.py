@@ -268,3 +268,36 @@ def test_another_stream_and_a_graph():
         ge = ssm.attn_bwd(*x[:3], e, le, x[3], **kw)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip([o3, lse3, *g3.values()], [e, le, *ge.values()])), i
+
+
+@pytest.mark.parametrize("D", [24, 64, 96, 128])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (70, 3), (1, 2)])
+def test_forward_of_many_workgroups(D, window, sinks):
+    """Whole sequences and packed ones, empty ones among them, that fill the GPU (512 workgroups of 128 queries)."""
+    _run(_case(D, 8, 200, 200, 4, 32, D, BF), grads=False, window=window, sinks=sinks)
+    cu = [0, 300, 300, 429, 430, 900, 1156, 1190]
+    _run(_case(D, 1, 1200, 1200, 4, 40, D, BF), grads=False, window=window, sinks=sinks, cu=cu)
+
+
+@pytest.mark.parametrize("D", [24, 64, 96, 128])
+@pytest.mark.parametrize("window,sinks", [(None, 0), (1100, 3)])
+def test_few_queries_of_many_keys(D, window, sinks):
+    for L, Lk in ((1, 1024), (60, 1500), (130, 2049), (1500, 1400)):
+        _run(_case(L, 1, L, Lk, 1, 2, D, BF), grads=False, window=window, sinks=sinks)
+    _run(_case(D, 1, 200, 4000, 1, 3, D, BF), grads=False, window=window, sinks=sinks, cu=[0, 1, 1, 130, 190], cu_k=[0, 1500, 1502, 1520, 3900])
+
+
+@pytest.mark.parametrize("D", [24, 64, 96, 128])
+@pytest.mark.parametrize("n,Hk,H", [(4, 2, 4), (1, 1, 3), (1, 3, 3)])
+def test_gradients_over_many_tiles(D, n, Hk, H):
+    """Shared heads in pairs and odd ones, key heads that fall evenly on the XCDs and not, more queries than a workgroup."""
+    for window, sinks in ((None, 0), (150, 70)):
+        _run(_case(D + H, n, 400, 400, Hk, H, D, BF), window=window, sinks=sinks)
+    _run(_case(D, 1, 700, 800, Hk, H, D, BF), window=100, sinks=5, cu=[0, 300, 301, 690], cu_k=[0, 400, 401, 790])
+
+
+@DTYPES
+@pytest.mark.parametrize("scale", [0.0, 1e-20, 1e-4])
+def test_small_scales(dtype, scale):
+    """Scores that vanish: P averages the visible values."""
+    _run(_case(3, 1, 150, 150, 1, 2, 64, dtype), window=40, sinks=2, scale=scale)
