@@ -703,6 +703,8 @@ ssm_status_t ssm_block_norm_bwd_check(const ssm_block_norm_bwd_params_t *p);
  *   cu_seqlens_k  the same for the keys; NULL with cu_seqlens: the same offsets (L = Lk)
  *   lse       (Bt, L, H) f32 or NULL; -infinity where a query sees nothing (o is zero there)
  *   o         (Bt, L, H, D) o_dtype, dense
+ *   o_rest    (Bt, L, H, D) bf16, dense, or NULL: what rounding took from an o in bf16
+ *             (o + o_rest has 16 bits), for ssm_attn_bwd
  * Sums and the softmax's statistics are f32.  Scores are products of the inputs as they
  * are; their exponentials enter the product with v in f32 for f32 inputs, in three bf16
  * parts (24 bits) for bf16 inputs and an f32 o, in two (16 bits) for a bf16 o.
@@ -724,6 +726,7 @@ typedef struct ssm_attn_params {
   float *lse;
   void *o;
   int32_t o_dtype;
+  void *o_rest;
   void *workspace;
   size_t workspace_bytes;
 } ssm_attn_params_t;
@@ -740,9 +743,12 @@ ssm_status_t ssm_attn_check(const ssm_attn_params_t *p);
  *   dq_p = scale sum_j dS_pj k_j,  dk_j = scale sum_p dS_pj q_p,  dv_j = sum_p P_pj dout_p
  * Key heads shared by several heads receive the sum over them.  Sums are taken in a
  * fixed order, without atomics: results repeat bit for bit.  dout_p.o_p comes from o as
- * it is given: an o in bf16 moves dS_pj by P_pj |dout_p||o_p| 2^-9 at most, one in f32
- * does not.  P and dS enter their products as they do in the forward (grad_dtype in the
- * place of o_dtype).  Queries and keys outside every sequence are not written.
+ * it is given: an o in bf16 moves dS_pj by P_pj |dout_p||o_p| 2^-9 at most, which is as
+ * much as the gradients' rounding to bf16 or, where dS is small, several times that; with
+ * its o_rest, or in f32, it does not.  P and dS enter their products as they do in the
+ * forward (grad_dtype in the place of o_dtype).  A NaN or infinity in a row of dout may
+ * reach the keys of its tiles that the row does not see, as one in v does in the forward.
+ * Queries and keys outside every sequence are not written.
  * Workspace: ssm_attn_bwd_workspace_size() bytes, 256-byte aligned.
  * ---------------------------------------------------------------------- */
 typedef struct ssm_attn_bwd_params {
@@ -757,6 +763,7 @@ typedef struct ssm_attn_bwd_params {
   const float *lse;
   const void *o;
   int32_t o_dtype;
+  const void *o_rest;
   const void *dout;
   void *dq, *dk, *dv;
   int32_t grad_dtype;

@@ -76,15 +76,22 @@ def _inputs(p, q, k, v, window, sinks, scale, cu_seqlens, cu_seqlens_k):
         p.cu_seqlens_k = _offsets(cu_seqlens_k, "cu_seqlens_k", dev)
 
 
+def _rest(p, o, o_rest, dev):
+    if o_rest is not None and o.dtype != torch.bfloat16:
+        raise TypeError("o_rest goes with an o in bfloat16")
+    p.o_rest = _arg(o_rest, "o_rest", o.shape, torch.bfloat16, dev)
+
+
 def attn_fwd(q, k, v, *, window=None, sinks=0, scale=None, cu_seqlens=None, cu_seqlens_k=None, lse=None, o=None,
-             o_dtype=None, workspace=None, stream=None, prepare=False):
+             o_dtype=None, o_rest=None, workspace=None, stream=None, prepare=False):
     """Causal attention with a sliding window and sinks over whole sequences (ssm_attn_fwd): q (batch, L, H, D),
     k and v (batch, Lk, Hk, D); head h reads key head h // (H // Hk).  The query at position p sees the keys
     j <= p with j > p - window (all without a window) or j < sinks; with more keys than queries the queries
     are the last positions.  cu_seqlens: int32 offsets on the GPU of sequences packed into one batch row
     (queries of no sequence are not written), cu_seqlens_k those of the keys where they differ.  scale
     defaults to 1 / sqrt(D).  q, k and v may be slices of a wider tensor along the token's row.  lse: a
-    (batch, L, H) fp32 tensor that receives the log of the softmax's sum (attn_bwd needs it).
+    (batch, L, H) fp32 tensor that receives the log of the softmax's sum (attn_bwd needs it).  o_rest: a bfloat16
+    tensor like o that receives what rounding took from an o in bfloat16, for attn_bwd.
     Returns o (batch, L, H, D), or with prepare=True a Call that enqueues this same call again."""
     L_ = lib()
     dev = _gpu(q, "q")
@@ -95,17 +102,19 @@ def attn_fwd(q, k, v, *, window=None, sinks=0, scale=None, cu_seqlens=None, cu_s
     p.lse = _arg(lse, "lse", q.shape[:3], _F32, dev)
     p.o = _arg(o, "o", q.shape, o.dtype, dev)
     p.o_dtype = _code(o, "o")
+    _rest(p, o, o_rest, dev)
     workspace = _workspace(p, L_.ssm_attn_workspace_size(_byref(p)), workspace, dev, stream)
-    call = Call(L_.ssm_attn_fwd, p, _on(dev, stream), o, (q, k, v, cu_seqlens, cu_seqlens_k, lse, workspace))
+    call = Call(L_.ssm_attn_fwd, p, _on(dev, stream), o, (q, k, v, cu_seqlens, cu_seqlens_k, lse, o_rest, workspace))
     return call if prepare else call.run()
 
 
 def attn_bwd(q, k, v, o, lse, dout, *, window=None, sinks=0, scale=None, cu_seqlens=None, cu_seqlens_k=None,
-             grad_dtype=None, workspace=None, stream=None, prepare=False):
+             grad_dtype=None, o_rest=None, workspace=None, stream=None, prepare=False):
     """Backward of attn_fwd (ssm_attn_bwd): the forward's inputs, its results o and lse, and dout (batch, L, H, D) in
     q's dtype.  Returns a dict of the gradients q, k and v in grad_dtype (fp32 unless given; zeros for rows of
     no sequence), or with prepare=True a Call whose run() enqueues it again (its .out is that dict).
-    Gradients as exact as fp32 need an o in fp32 (attn_fwd's o_dtype)."""
+    The rounding of an o in bfloat16 enters the gradients of q and k (as much as theirs to bfloat16, or several
+    times that); with its o_rest from attn_fwd, or an o in fp32, it does not."""
     L_ = lib()
     dev = _gpu(q, "q")
     p = AttnBwdParams()
@@ -114,6 +123,7 @@ def attn_bwd(q, k, v, o, lse, dout, *, window=None, sinks=0, scale=None, cu_seql
         raise TypeError("o and lse must be the forward's results")
     p.o = _arg(o, "o", q.shape, o.dtype, dev)
     p.o_dtype = _code(o, "o")
+    _rest(p, o, o_rest, dev)
     p.lse = _arg(lse, "lse", q.shape[:3], _F32, dev)
     p.dout = _arg(dout, "dout", q.shape, q.dtype, dev)
     gd = grad_dtype or _F32
@@ -125,7 +135,7 @@ def attn_bwd(q, k, v, o, lse, dout, *, window=None, sinks=0, scale=None, cu_seql
             setattr(p, field, out[name].data_ptr())
     workspace = _workspace(p, L_.ssm_attn_bwd_workspace_size(_byref(p)), workspace, dev, stream)
     kind = Call if cu_seqlens is None else _PackedGrads
-    call = kind(L_.ssm_attn_bwd, p, _on(dev, stream), out, (q, k, v, o, lse, dout, cu_seqlens, cu_seqlens_k, workspace))
+    call = kind(L_.ssm_attn_bwd, p, _on(dev, stream), out, (q, k, v, o, o_rest, lse, dout, cu_seqlens, cu_seqlens_k, workspace))
     return call if prepare else call.run()
 
 

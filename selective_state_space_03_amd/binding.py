@@ -163,7 +163,7 @@ _ATTN_HEAD = [
     ("struct_size", ctypes.c_uint32), ("batch", _i32), ("seqlen", _i32), ("seqlen_k", _i32), ("num_seqs", _i32),
     ("nkheads", _i32), ("nheads", _i32), ("d_head", _i32), ("q", _vp), ("k", _vp), ("v", _vp), ("x_dtype", _i32),
     ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("scale", _f32), ("window", _i32), ("sinks", _i32),
-    ("cu_seqlens", _vp), ("cu_seqlens_k", _vp), ("lse", _vp), ("o", _vp), ("o_dtype", _i32),
+    ("cu_seqlens", _vp), ("cu_seqlens_k", _vp), ("lse", _vp), ("o", _vp), ("o_dtype", _i32), ("o_rest", _vp),
 ]
 
 

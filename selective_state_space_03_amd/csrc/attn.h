@@ -22,6 +22,7 @@ struct AttnArgs {
   float scale;
   int vec;                            // rows of 16-byte groups (2), of 8-byte groups (1), of any elements (0)
   void* o;                            // (rows_q, h, D)
+  void* o_rest;                       // bf16: what rounding took from an o in bf16, or null
   float* lse;                         // (rows_q, h) or null
   // backward
   const void* dout;

@@ -159,6 +159,8 @@ ssm_status_t attn_common(const P* p) {
   if (!valid_dtype(p->o_dtype)) return fail(SSM_ERR_INVALID_ARG, "o_dtype: unknown dtype");
   if (rows_q(p) > 0 && !p->o) return fail(SSM_ERR_INVALID_ARG, "o is NULL");
   if (!aligned({p->o}, esize(p->o_dtype))) return fail(SSM_ERR_INVALID_ARG, "o is not aligned to its element size");
+  if (p->o_rest && p->o_dtype != SSM_BF16) return fail(SSM_ERR_INVALID_ARG, "o_rest goes with an o in bf16");
+  if (!aligned({p->o_rest}, 2)) return fail(SSM_ERR_INVALID_ARG, "o_rest is not aligned to its element size");
   if (!attn_fields(p)) return fail(SSM_ERR_UNSUPPORTED, "too many tiles and heads for one launch");
   return SSM_OK;
 }
@@ -183,7 +185,7 @@ ssm_status_t attn_check(const ssm_attn_params_t* p) {
   if (p->struct_size != sizeof(*p)) return fail(SSM_ERR_INVALID_ARG, "struct_size does not match this library");
   const ssm_status_t s = attn_common(p);
   if (s != SSM_OK) return s;
-  return check_overlap({{p->o, q_elems(p) * esize(p->o_dtype)}, {p->lse, static_cast<size_t>(rows_q(p)) * p->nheads * 4}},
+  return check_overlap({{p->o, q_elems(p) * esize(p->o_dtype)}, {p->lse, static_cast<size_t>(rows_q(p)) * p->nheads * 4}, {p->o_rest, q_elems(p) * 2}},
                        {q_range(p), k_range(p, p->k, p->k_stride), k_range(p, p->v, p->v_stride), {p->cu_seqlens, cu_bytes(p)},
                         {p->cu_seqlens_k, cu_bytes(p)}});
 }
@@ -254,7 +256,7 @@ ssm_status_t attn_bwd_check(const ssm_attn_bwd_params_t* p) {
   const size_t eg = esize(p->grad_dtype);
   return check_overlap({{p->dq, q_elems(p) * eg}, {p->dk, k_elems(p) * eg}, {p->dv, k_elems(p) * eg}, {p->workspace, need}},
                        {q_range(p), k_range(p, p->k, p->k_stride), k_range(p, p->v, p->v_stride), {p->cu_seqlens, cu_bytes(p)},
-                        {p->cu_seqlens_k, cu_bytes(p)}, {p->o, q_elems(p) * esize(p->o_dtype)},
+                        {p->cu_seqlens_k, cu_bytes(p)}, {p->o, q_elems(p) * esize(p->o_dtype)}, {p->o_rest, q_elems(p) * 2},
                         {p->lse, static_cast<size_t>(rows_q(p)) * p->nheads * 4}, {p->dout, q_elems(p) * esize(p->x_dtype)}});
 }
 
@@ -443,8 +445,9 @@ ssm_status_t ssm_attn_fwd(const ssm_attn_params_t* p, void* stream) {
   attn_plan(p, l);
   l.a.o = p->o;
   l.a.lse = p->lse;
+  l.a.o_rest = p->o_rest;
   l.o_dtype = p->o_dtype;
-  l.a.vec = vec_of(p->d_head, p->x_dtype, {l.a.q_stride, l.a.k_stride, l.a.v_stride}, {p->q, p->k, p->v, p->o});
+  l.a.vec = vec_of(p->d_head, p->x_dtype, {l.a.q_stride, l.a.k_stride, l.a.v_stride}, {p->q, p->k, p->v, p->o, p->o_rest});
   return hip_status(ssm::launch_attn_fwd(l, static_cast<hipStream_t>(stream)));
 }
 
@@ -463,6 +466,7 @@ ssm_status_t ssm_attn_bwd(const ssm_attn_bwd_params_t* p, void* stream) {
   sink_plan(p, l.a);
   l.a.o = const_cast<void*>(p->o);
   l.a.lse = const_cast<float*>(p->lse);
+  l.a.o_rest = const_cast<void*>(p->o_rest);
   l.a.dout = p->dout;
   l.a.dq = p->dq;
   l.a.dk = p->dk;
@@ -476,7 +480,7 @@ ssm_status_t ssm_attn_bwd(const ssm_attn_bwd_params_t* p, void* stream) {
   l.a.dk_part = reinterpret_cast<float*>(ws + w.dk_part);
   l.a.dv_part = reinterpret_cast<float*>(ws + w.dv_part);
   l.a.vec = vec_of(p->d_head, p->x_dtype, {l.a.q_stride, l.a.k_stride, l.a.v_stride},
-                   {p->q, p->k, p->v, p->o, p->dout, p->dq, p->dk, p->dv});
+                   {p->q, p->k, p->v, p->o, p->o_rest, p->dout, p->dq, p->dk, p->dv});
   return hip_status(ssm::launch_attn_bwd(l, static_cast<hipStream_t>(stream)));
 }
 

@@ -3,7 +3,7 @@
 namespace ssm {
 namespace {
 
-// delta = sum_d do o: 16 lanes per (query, head), 8 channels each, four rows in turn (a launch's 2^32
+// delta = sum_d do (o + o_rest): 16 lanes per (query, head), 8 channels each, four rows in turn (a launch's 2^32
 // threads hold 2^30 rows that way)
 template <typename T, typename OT>
 __global__ __launch_bounds__(256) void attn_delta_kernel(const AttnArgs a, long rows) {
@@ -25,6 +25,13 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(const AttnArgs a, long 
       v.get(a.D - d, h);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x = fmaf(f[e], h[e], x);
+      if (a.o_rest) {
+        Row8<bf16s> w;
+        w.load(static_cast<const bf16s*>(a.o_rest) + row * a.D, d, a.D, vec);
+        w.get(a.D - d, h);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x = fmaf(f[e], h[e], x);
+      }
     }
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) x += __shfl_xor(x, o);

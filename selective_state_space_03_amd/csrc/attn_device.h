@@ -340,6 +340,9 @@ __device__ __forceinline__ void attn_store_row(void* out, size_t at, const f32x4
 #pragma unroll
   for (int t = 0; t < NT; ++t) attn_store4(out, at, x[t][0], x[t][1], x[t][2], x[t][3], 16 * t + 4 * g, D, bf16, vec);
 }
+// What rounding to bf16 takes from x
+__device__ __forceinline__ float rest_of(float x) { return x - __uint_as_float(pack_rne(x, 0.0f) << 16); }
+
 // .. of 32 x 32 tiles: half h of the wave holds 32 t + 8 i + 4 h ..
 template <int NT>
 __device__ __forceinline__ void wide_store_row(void* out, size_t at, const f32x16 (&x)[NT], int D, int h, int bf16, int vec) {
@@ -348,6 +351,17 @@ __device__ __forceinline__ void wide_store_row(void* out, size_t at, const f32x1
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       attn_store4(out, at, x[t][4 * i], x[t][4 * i + 1], x[t][4 * i + 2], x[t][4 * i + 3], 32 * t + 8 * i + 4 * h, D, bf16, vec);
+}
+
+template <int NT>
+__device__ __forceinline__ void wide_store_o(const AttnArgs& a, size_t at, f32x16 (&o)[NT], int h, int bf16) {
+  wide_store_row<NT>(a.o, at, o, a.D, h, bf16, a.vec);
+  if (!a.o_rest) return;
+#pragma unroll
+  for (int d = 0; d < NT; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[d][e] = rest_of(o[d][e]);
+  wide_store_row<NT>(a.o_rest, at, o, a.D, h, 1, a.vec);
 }
 
 // Factor of the scores in powers of two.  Not zero: a score of -infinity (a key that is not seen) has to stay that.

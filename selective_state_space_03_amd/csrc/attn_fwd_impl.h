@@ -188,6 +188,13 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
 #pragma unroll
       for (int r = 0; r < 4; ++r) o[m][d][r] *= f;
     attn_store_row<NT>(a.o, row * a.D, o[m], a.D, g, o_bf16, a.vec);
+    if (a.o_rest) {
+#pragma unroll
+      for (int d = 0; d < NT; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[m][d][r] = rest_of(o[m][d][r]);
+      attn_store_row<NT>(a.o_rest, row * a.D, o[m], a.D, g, 1, a.vec);
+    }
   }
 }
 
@@ -339,7 +346,7 @@ __global__ __launch_bounds__(256, 3) void attn_fwd_wide_kernel(const AttnArgs a,
   for (int d = 0; d < NT; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] *= f;
-  wide_store_row<NT>(a.o, row * a.D, o, a.D, h, o_bf16, a.vec);
+  wide_store_o<NT>(a, row * a.D, o, h, o_bf16);
 }
 
 // The same for few queries that see many keys: one workgroup of 128 queries on a CU has eight waves, two on
@@ -560,7 +567,7 @@ __global__ __launch_bounds__(512, 2) void attn_fwd_long_kernel(const AttnArgs a,
   for (int d = 0; d < NT; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = (o[d][e] * f0 + red[(d * 16 + e) * 64] * f1) * inv;
-  wide_store_row<NT>(a.o, row * a.D, o, a.D, h, o_bf16, a.vec);
+  wide_store_o<NT>(a, row * a.D, o, h, o_bf16);
 }
 
 template <int DQ, int NP>

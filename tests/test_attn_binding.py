@@ -38,6 +38,11 @@ def test_host_tensors_are_refused(name, monkeypatch):
         CALLS[name]()
 
 
+def test_a_rest_needs_an_o_in_bf16():
+    with pytest.raises(TypeError, match="o_rest"):
+        attn._rest(ssm.binding.AttnParams(), Q, Q.bfloat16(), None)
+
+
 @pytest.mark.parametrize("window,sinks", [(0, 0), (-3, 0), (5, -1), (2 ** 31, 0)])
 def test_masks_out_of_range_are_refused(window, sinks):
     with pytest.raises(ValueError, match="window|sinks"):

@@ -36,12 +36,14 @@ def _inside(t, cu):
     return np.array([[any(a <= x < b for a, b in zip(cu[:-1], cu[1:])) for x in at]])
 
 
-def _run(c, out=None, cu=None, cu_k=None, grads=True, o_dtype=None, grad_dtype=None, **kw):
-    """Forward (and backward), both against the oracle; o and lse start as NaN."""
+def _run(c, out=None, cu=None, cu_k=None, grads=True, o_dtype=None, grad_dtype=None, rest=False, **kw):
+    """Forward (and backward), both against the oracle; o and lse start as NaN.  rest: with what rounding took from o,
+    so that the gradients are those of an exact o."""
     q, k, v, do = c
     o = torch.full(q.shape, float("nan"), dtype=o_dtype or q.dtype, device=DEV)
     lse = torch.full(q.shape[:3], float("nan"), device=DEV)
-    ssm.attn_fwd(q, k, v, lse=lse, o=o, cu_seqlens=_cu(cu), cu_seqlens_k=_cu(cu_k), **kw)
+    orest = torch.full_like(o, float("nan")) if rest else None
+    ssm.attn_fwd(q, k, v, lse=lse, o=o, o_rest=orest, cu_seqlens=_cu(cu), cu_seqlens_k=_cu(cu_k), **kw)
     torch.cuda.synchronize()
     ok = dict(kw, cu=cu, cu_k=cu_k)
     ok["window"] = kw.get("window") or 0
@@ -51,15 +53,18 @@ def _run(c, out=None, cu=None, cu_k=None, grads=True, o_dtype=None, grad_dtype=N
     assert np.isnan(got[~inq]).all() and np.isnan(gl[~inq]).all()  # rows of no sequence are left as they were
     bf = o.dtype == BF
     check(got[inq], ro[inq], TOL_BF16 if bf else TOL_F32, "o", out_bf16=bf)
+    if rest:
+        assert np.isnan(np64(orest)[~inq]).all()
+        check((got + np64(orest))[inq], ro[inq], TOL_BF16, "o + rest")
     none = np.isneginf(rl[inq])
     assert np.array_equal(np.isneginf(gl[inq]), none) and not got[inq][none].any()
     check(gl[inq][~none], rl[inq][~none], TOL_F32, "lse")
     if not grads:
         return
     gd = grad_dtype or q.dtype
-    g = ssm.attn_bwd(q, k, v, o, lse, do, grad_dtype=gd, cu_seqlens=_cu(cu), cu_seqlens_k=_cu(cu_k), **kw)
+    g = ssm.attn_bwd(q, k, v, o, lse, do, o_rest=orest, grad_dtype=gd, cu_seqlens=_cu(cu), cu_seqlens_k=_cu(cu_k), **kw)
     torch.cuda.synchronize()
-    rg = A.attention_backward(*(np64(x) for x in (q, k, v, do)), o=np64(o), **ok)
+    rg = A.attention_backward(*(np64(x) for x in (q, k, v, do)), o=None if rest else np64(o), **ok)
     for x in g:
         assert g[x].dtype == gd
         check(np64(g[x]), rg[x], TOL_BF16 if gd == BF else TOL_F32, "d" + x, out_bf16=gd == BF)
@@ -301,3 +306,12 @@ def test_gradients_over_many_tiles(D, n, Hk, H):
 def test_small_scales(dtype, scale):
     """Scores that vanish: P averages the visible values."""
     _run(_case(3, 1, 150, 150, 1, 2, 64, dtype), window=40, sinks=2, scale=scale)
+
+
+@pytest.mark.parametrize("D", [40, 64, 66, 96, 127, 128])
+def test_gradients_of_an_exact_o(D):
+    """With what rounding took from o, narrow, wide and long kernels: gradients as of an o in 64 bits."""
+    _run(_case(D, 2, 90, 90, 2, 4, D, BF), rest=True, window=30, sinks=2)
+    _run(_case(D, 1, 200, 200, 1, 3, D, BF), rest=True, cu=[0, 1, 14, 14, 150, 190])
+    _run(_case(D, 8, 200, 200, 4, 32, D, BF), rest=True, grads=False)
+    _run(_case(D, 1, 60, 1500, 1, 2, D, BF), rest=True)

@@ -151,7 +151,7 @@ def _step(seed, lens, h, hk, page, D, dtype, kind, window=None, sinks=0, o_dtype
     ssm.attn_decode_step(q, kc, vc, _dev(table), _dev(lens), k_scale=ks, v_scale=vs, window=window, sinks=sinks, o=o, **kw)
     torch.cuda.synchronize()
     want = A.decode_step(np64(q), _values(kc), _values(vc), table, lens, k_scale=None if ks is None else np64(ks),
-                         v_scale=None if vs is None else np64(vs), window=window or 0, sinks=sinks)
+                         v_scale=None if vs is None else np64(vs), window=window or 0, sinks=sinks, scale=kw.get("scale"))
     check(np64(o), want, TOL, "o", out_bf16=o.dtype == BF)
 
 
@@ -168,6 +168,13 @@ def test_step(dtype, kind, page, D):
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (100, 3), (31, 64), (299, 1), (300, 0), (10 ** 9, 2)])
 def test_step_masks(dtype, kind, window, sinks):
     _step(window % 997, [300, 1, 64, 130], 4, 2, 16, 64, dtype, kind, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("dtype,kind", STEPS)
+@pytest.mark.parametrize("scale", [0.0, 1e-20])
+def test_step_small_scales(dtype, kind, scale):
+    """The mean of the visible values."""
+    _step(3, [300, 1, 64, 0], 4, 2, 16, 64, dtype, kind, window=50, sinks=3, scale=scale)
 
 
 @pytest.mark.parametrize("dtype,kind", STEPS)
