@@ -746,9 +746,10 @@ ssm_status_t ssm_attn_check(const ssm_attn_params_t *p);
  * it is given: an o in bf16 moves dS_pj by P_pj |dout_p||o_p| 2^-9 at most, which is as
  * much as the gradients' rounding to bf16 or, where dS is small, several times that; with
  * its o_rest, or in f32, it does not.  P and dS enter their products as they do in the
- * forward (grad_dtype in the place of o_dtype).  A NaN or infinity in a row of dout may
- * reach the keys of its tiles that the row does not see, as one in v does in the forward.
- * Queries and keys outside every sequence are not written.
+ * forward (grad_dtype in the place of o_dtype).  A NaN or infinity in a row of q, k
+ * or dout may reach the gradients of rows of its tiles that do not see it, or that it does
+ * not see, as one in v does in the forward; rows of other sequences never do.  Queries and
+ * keys outside every sequence are not written.
  * Workspace: ssm_attn_bwd_workspace_size() bytes, 256-byte aligned.
  * ---------------------------------------------------------------------- */
 typedef struct ssm_attn_bwd_params {

@@ -315,3 +315,36 @@ def test_gradients_of_an_exact_o(D):
     _run(_case(D, 1, 200, 200, 1, 3, D, BF), rest=True, cu=[0, 1, 14, 14, 150, 190])
     _run(_case(D, 8, 200, 200, 4, 32, D, BF), rest=True, grads=False)
     _run(_case(D, 1, 60, 1500, 1, 2, D, BF), rest=True)
+
+
+@DTYPES
+def test_no_queries(dtype):
+    """Keys that no query sees have gradients of zero."""
+    q, k, v, do = _case(1, 2, 0, 70, 2, 4, 64, dtype)
+    lse = torch.empty(q.shape[:3], device=DEV)
+    o = ssm.attn_fwd(q, k, v, lse=lse, window=20, sinks=2)
+    g = ssm.attn_bwd(q, k, v, o, lse, do, window=20, sinks=2, grad_dtype=dtype)
+    assert o.shape == q.shape and g["q"].shape == q.shape and g["k"].shape == k.shape
+    assert not g["k"].any() and not g["v"].any()
+
+
+def test_two_calls_at_once():
+    """Forward and backward of two inputs on two streams side by side, several times: the results of each alone."""
+    cases = [_case(s, 2, 900, 900, 2, 4, 64, BF) for s in (20, 21)]
+    kw = dict(window=200, sinks=4)
+
+    def one(c, stream=None):
+        lse, rest = torch.empty(c[0].shape[:3], device=DEV), torch.empty_like(c[0])
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        o = ssm.attn_fwd(*c[:3], lse=lse, o_rest=rest, stream=stream, **kw)
+        return [o, lse, rest, *ssm.attn_bwd(*c[:3], o, lse, c[3], o_rest=rest, stream=stream, **kw).values()]
+
+    want = [one(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(4):
+        got = [one(c, s) for c, s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, w))
