@@ -24,6 +24,8 @@ struct AttnArgs {
   void* o;                            // (rows_q, h, D)
   void* o_rest;                       // bf16: what rounding took from an o in bf16, or null
   float* lse;                         // (rows_q, h) or null
+  int nsplit;                         // parts of the visible keys (forward of few queries), 1: whole
+  float* part;                        // (rows_q, h, nsplit, attn_dq(D)) sums, then (rows_q, h, nsplit) of (maximum, sum)
   // backward
   const void* dout;
   void *dq, *dk, *dv;                 // dense, or null
@@ -47,6 +49,15 @@ inline long attn_tiles(const AttnArgs& a, int rows, bool keys) {
 // Pieces of queries over all sequences
 inline long attn_pieces(const AttnArgs& a) {
   return a.cu_q ? a.lq / a.span + a.nseq : static_cast<long>(a.nseq) * ((a.lq + a.span - 1) / a.span);
+}
+// Parts of the keys of a forward in bf16 whose workgroups of 128 queries leave half of the CUs idle: as many as fill
+// them, of 512 keys or more (8 heads of 128 and 8192 keys: one query 123 -> 25 us, 128 queries 29)
+inline int attn_fwd_splits(const AttnArgs& a) {
+  const long blocks = attn_tiles(a, 128, false) * a.h;
+  const long seen = a.window == kAttnAll ? a.lk : (a.lk < a.window + 128L + a.sinks ? a.lk : a.window + 128L + a.sinks);
+  if (a.cu_q || blocks == 0 || blocks > 128 || seen < 2048 || a.window < 1024) return 1;
+  const long fill = 256 / blocks, most = seen / 512;
+  return static_cast<int>(fill < most ? fill : most);
 }
 constexpr int kSinkRows = 64;  // keys of a tile of the backward pass
 // Workgroups of its queries, each two heads of `rows` queries or one of twice as many

@@ -180,12 +180,28 @@ size_t k_elems(const P* p) { return static_cast<size_t>(rows_k(p)) * p->nkheads 
 template <typename P>
 size_t cu_bytes(const P* p) { return (static_cast<size_t>(p->num_seqs) + 1) * 4; }
 
+// The workspace holds the parts of a call whose keys are split, which goes by sizes and types, not by alignment.
+int fwd_splits(const ssm_attn_params_t* p) {
+  if (p->x_dtype != SSM_BF16 || p->o_dtype != SSM_BF16) return 1;
+  ssm::AttnLaunch l{};
+  attn_plan(p, l);
+  return ssm::attn_fwd_splits(l.a);
+}
+size_t fwd_ws(const ssm_attn_params_t* p) {
+  const int n = fwd_splits(p);
+  return n > 1 ? static_cast<size_t>(rows_q(p)) * p->nheads * n * (ssm::attn_dq(p->d_head) + 2) * 4 : 0;
+}
+
 ssm_status_t attn_check(const ssm_attn_params_t* p) {
   if (!p) return fail(SSM_ERR_INVALID_ARG, "params is NULL");
   if (p->struct_size != sizeof(*p)) return fail(SSM_ERR_INVALID_ARG, "struct_size does not match this library");
   const ssm_status_t s = attn_common(p);
   if (s != SSM_OK) return s;
-  return check_overlap({{p->o, q_elems(p) * esize(p->o_dtype)}, {p->lse, static_cast<size_t>(rows_q(p)) * p->nheads * 4}, {p->o_rest, q_elems(p) * 2}},
+  const size_t need = fwd_ws(p);
+  if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return fail(SSM_ERR_WORKSPACE, "workspace is missing or too small");
+  if (need > 0 && !aligned({p->workspace}, 256)) return fail(SSM_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return check_overlap({{p->o, q_elems(p) * esize(p->o_dtype)}, {p->lse, static_cast<size_t>(rows_q(p)) * p->nheads * 4}, {p->o_rest, q_elems(p) * 2},
+                        {p->workspace, need}},
                        {q_range(p), k_range(p, p->k, p->k_stride), k_range(p, p->v, p->v_stride), {p->cu_seqlens, cu_bytes(p)},
                         {p->cu_seqlens_k, cu_bytes(p)}});
 }
@@ -434,8 +450,8 @@ extern "C" {
 ssm_status_t ssm_attn_check(const ssm_attn_params_t* p) { return done(attn_check(p)); }
 
 size_t ssm_attn_workspace_size(const ssm_attn_params_t* p) {
-  (void)p;
-  return 0;
+  if (!p || p->struct_size != sizeof(*p) || !attn_fields(p)) return 0;
+  return fwd_ws(p);
 }
 
 ssm_status_t ssm_attn_fwd(const ssm_attn_params_t* p, void* stream) {
@@ -446,6 +462,8 @@ ssm_status_t ssm_attn_fwd(const ssm_attn_params_t* p, void* stream) {
   l.a.o = p->o;
   l.a.lse = p->lse;
   l.a.o_rest = p->o_rest;
+  l.a.nsplit = fwd_splits(p);
+  l.a.part = static_cast<float*>(p->workspace);
   l.o_dtype = p->o_dtype;
   l.a.vec = vec_of(p->d_head, p->x_dtype, {l.a.q_stride, l.a.k_stride, l.a.v_stride}, {p->q, p->k, p->v, p->o, p->o_rest});
   return hip_status(ssm::launch_attn_fwd(l, static_cast<hipStream_t>(stream)));

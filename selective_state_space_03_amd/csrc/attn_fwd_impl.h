@@ -391,7 +391,9 @@ __global__ __launch_bounds__(512, 2) void attn_fwd_long_kernel(const AttnArgs a,
   const int lo = max(0, off + w.tile * BM - a.window + 1);
   const int first = lo / BN;
   const int ns = min((a.sinks + BN - 1) / BN, first);
-  const int n = last < 0 ? 0 : ns + max(0, last / BN + 1 - first);
+  const int all = last < 0 ? 0 : ns + max(0, last / BN + 1 - first);
+  const int from = static_cast<int>(static_cast<long>(all) * blockIdx.y / a.nsplit);  // the part's tiles
+  const int n = static_cast<int>(static_cast<long>(all) * (blockIdx.y + 1) / a.nsplit) - from;
 
   f32x16 o[NT], s[KT];
   Frag<NP> p[KT][2];
@@ -403,7 +405,7 @@ __global__ __launch_bounds__(512, 2) void attn_fwd_long_kernel(const AttnArgs a,
 
   const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
   unsigned char(&mine)[4][Tile::kBytes] = lds[half];
-  const auto key = [&](int t) { return (t < ns ? t : t - ns + first) * BN; };  // first key of tile t
+  const auto key = [&](int t) { return (t + from < ns ? t + from : t + from - ns + first) * BN; };  // first key of tile t
   // the half's tile i (none: zeros, so that the number of loads in flight stays)
   const auto load_k = [&](int i) {
     const int t = 2 * i + half;
@@ -560,13 +562,21 @@ __global__ __launch_bounds__(512, 2) void attn_fwd_long_kernel(const AttnArgs a,
   const float mo = red[NT * 16 * 64], to = fmaxf(mx, mo), sub = to == -INFINITY ? 0.0f : to;
   const float f0 = exp2_fast(mx - sub), f1 = exp2_fast(mo - sub);
   const float sum = l * f0 + red[(NT * 16 + 1) * 64] * f1;
-  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;  // (nothing visible: zeros)
+  const float inv = a.nsplit > 1 ? 1.0f : sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;  // (nothing visible: zeros)
   const size_t row = static_cast<size_t>(sq.q0 + i) * a.h + w.head;
-  if (a.lse && h == 0) a.lse[row] = sum > 0.0f || sum != sum ? (to + log2_fast(sum)) * kLn2 : -INFINITY;
 #pragma unroll
   for (int d = 0; d < NT; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = (o[d][e] * f0 + red[(d * 16 + e) * 64] * f1) * inv;
+  if (a.nsplit > 1) {
+    const size_t at = row * a.nsplit + blockIdx.y;
+    wide_store_row<NT>(a.part, at * DQ, o, a.D, h, 0, a.vec);
+    float* const stats = a.part + static_cast<size_t>(a.rows_q) * a.h * a.nsplit * DQ + 2 * at;
+    if (h == 0) stats[0] = to;
+    else stats[1] = sum;
+    return;
+  }
+  if (a.lse && h == 0) a.lse[row] = sum > 0.0f || sum != sum ? (to + log2_fast(sum)) * kLn2 : -INFINITY;
   wide_store_o<NT>(a, row * a.D, o, h, o_bf16);
 }
 
@@ -574,7 +584,7 @@ template <int DQ, int NP>
 hipError_t attn_fwd_wide_go(const AttnLaunch& l, bool few, hipStream_t s) {
   const unsigned blocks = static_cast<unsigned>(attn_tiles(l.a, 128, false) * l.a.h);
   return timed_launch(s, [&] {
-    if (few) hipLaunchKernelGGL((attn_fwd_long_kernel<DQ, NP>), dim3(blocks), dim3(512), 0, s, l.a, l.o_dtype == kBF16);
+    if (few) hipLaunchKernelGGL((attn_fwd_long_kernel<DQ, NP>), dim3(blocks, l.a.nsplit), dim3(512), 0, s, l.a, l.o_dtype == kBF16);
     else hipLaunchKernelGGL((attn_fwd_wide_kernel<DQ, NP>), dim3(blocks), dim3(256), 0, s, l.a, l.o_dtype == kBF16);
   });
 }

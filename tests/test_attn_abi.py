@@ -94,7 +94,9 @@ BAD = (
        for c in _POOL_BAD]
     + [(_fwd, dict(o=_addr(2) + 64), 1), (_fwd, dict(lse=_addr(5) + 4), 1), (_fwd, dict(o=_addr(1)), 1),
        (_fwd, dict(o_rest=_addr(17) + 1), 1), (_fwd, dict(o_rest=_addr(17), o_dtype=0), 1), (_fwd, dict(o_rest=_addr(5) + 64), 1),
-       (_fwd, dict(o_rest=_addr(2)), 1), (_bwd, dict(o_rest=_addr(17) + 1), 1), (_bwd, dict(o_rest=_addr(17), o_dtype=0), 1),
+       (_fwd, dict(o_rest=_addr(2)), 1), (_fwd, dict(seqlen_k=4096, window=0, workspace=None), 3),
+       (_fwd, dict(seqlen_k=4096, window=0, workspace_bytes=1000), 3), (_fwd, dict(seqlen_k=4096, window=0, workspace=_addr(20) + 64), 1),
+       (_fwd, dict(seqlen_k=4096, window=0, workspace=_addr(2)), 1), (_bwd, dict(o_rest=_addr(17) + 1), 1), (_bwd, dict(o_rest=_addr(17), o_dtype=0), 1),
        (_bwd, dict(o_rest=_addr(17), dq=_addr(17)), 1),
        (_bwd, dict(dout=None), 1), (_bwd, dict(lse=None), 1), (_bwd, dict(grad_dtype=2), 1), (_bwd, dict(dq=_addr(12)), 1),
        (_bwd, dict(dk=_addr(15)), 1), (_bwd, dict(dv=_addr(15) + 2), 1), (_bwd, dict(dout=_addr(12) + 1), 1),

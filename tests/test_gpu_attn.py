@@ -348,3 +348,11 @@ def test_two_calls_at_once():
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+@pytest.mark.parametrize("D", [24, 64, 66, 96, 128])
+def test_keys_split_over_workgroups(D):
+    """Few queries of many keys, whose parts a second kernel joins; some parts hold no visible key, some rows see none."""
+    for n, L, Lk, Hk, H, kw in ((1, 1, 8192, 1, 2, {}), (2, 5, 3000, 2, 4, {}), (1, 200, 2500, 1, 3, dict(window=2300, sinks=5)),
+                                (1, 130, 5000, 2, 2, dict(window=1950, sinks=1)), (1, 2300, 2100, 1, 1, {})):
+        _run(_case(L + D, n, L, Lk, Hk, H, D, BF), grads=False, rest=True, **kw)
