@@ -323,9 +323,8 @@ def _own_train(s):
 
     mask = dict(window=s["window"] or None, sinks=s["sinks"], cu_seqlens=s["cu"])
     lse = torch.empty(s["q"].shape[:3], dtype=torch.float32, device=s["q"].device)
-    rest = torch.empty_like(s["q"]) if s["q"].dtype == torch.bfloat16 else None
-    o = ssm.attn_fwd(s["q"], s["k"], s["v"], lse=lse, o_rest=rest, **mask)
-    got = ssm.attn_bwd(s["q"], s["k"], s["v"], o, lse, s["do"], o_rest=rest, grad_dtype=s["q"].dtype, **mask)
+    o = ssm.attn_fwd(s["q"], s["k"], s["v"], lse=lse, **mask)
+    got = ssm.attn_bwd(s["q"], s["k"], s["v"], o, lse, s["do"], grad_dtype=s["q"].dtype, **mask)
     return {"o": o, "dq": got["q"], "dk": got["k"], "dv": got["v"]}
 
 
