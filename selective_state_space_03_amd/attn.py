@@ -17,6 +17,7 @@ from .binding import (
     Call,
     _code,
     _empty,
+    _torch_stream,
     lib,
 )
 from .delta import _arg, _dtype, _fits, _gpu, _on, _rows, _workspace
@@ -32,7 +33,7 @@ class _PackedGrads(Call):
     run clears the gradients first, on the call's stream (the offsets may have changed since the last)."""
 
     def run(self):
-        with torch.cuda.stream(torch.cuda.ExternalStream(self._stream.value or 0, device=self.out["q"].device)):
+        with torch.cuda.stream(_torch_stream(self._stream.value, self.out["q"].device)):
             for t in self.out.values():
                 t.zero_()
         return super().run()

@@ -377,6 +377,12 @@ def _stream(device, stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _torch_stream(handle, device):
+    """torch's stream of a raw handle.  The null handle is the default stream's: ExternalStream would take it for
+    none given, and answer with a stream of torch's pool that nothing on the default stream is ordered with."""
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
 def _empty(shape, dtype, device, stream):
     """torch.empty for a buffer the library writes on `stream`.  torch's caching
     allocator ties a block to the stream current at allocation; when the call

@@ -19,6 +19,7 @@ from .binding import (
     _empty,
     _ptr,
     _stream,
+    _torch_stream,
     lib,
 )
 
@@ -106,7 +107,7 @@ class _PackedGrads(Call):
 
     def run(self):
         clear = [self.out[name] for name in ("q", "k", "v", "g", "beta")]
-        with torch.cuda.stream(torch.cuda.ExternalStream(self._stream.value or 0, device=clear[0].device)):
+        with torch.cuda.stream(_torch_stream(self._stream.value, clear[0].device)):
             for t in clear:
                 t.zero_()
         return super().run()
