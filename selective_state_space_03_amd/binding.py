@@ -385,12 +385,17 @@ def _torch_stream(handle, device):
 
 def _empty(shape, dtype, device, stream):
     """torch.empty for a buffer the library writes on `stream`.  torch's caching
-    allocator ties a block to the stream current at allocation; when the call
-    runs on another stream the block is also recorded on that one, so it is not
-    handed out again before the work queued there has finished with it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and stream != torch.cuda.current_stream(device):
-        t.record_stream(stream)
+    allocator ties a block to the stream current at allocation, and hands it out
+    again while that stream's earlier work may still use it: a call on another
+    stream takes its block from that one's.  It is also recorded on the current
+    stream, whose work reads the result, so that it is not handed out again before
+    that has finished with it."""
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
     return t
 
 
