@@ -185,6 +185,7 @@ __global__ __launch_bounds__(256, VEC && QP == 1 && sizeof(CT) < 4 ? 3 : 2) void
     return p;
   };
   float ks_next = 0.0f, vs_next = 0.0f;
+  bool there_next = false;
   // a tile's row addresses; its scales are loaded, and put there by the time they are used.  Whether every
   // key of it is there.
   const auto put_info = [&](Info& to, Page p) {
@@ -194,6 +195,7 @@ __global__ __launch_bounds__(256, VEC && QP == 1 && sizeof(CT) < 4 ? 3 : 2) void
       to.base[lane] = (ph * a.page + (in ? p.row : 0)) * a.D;
       to.add[lane] = in ? 0.0f : -INFINITY;
       if constexpr (sizeof(CT) == 1) {
+        there_next = in;
         ks_next = a.k_scale[ph];
         vs_next = a.v_scale[ph];
       }
@@ -266,7 +268,7 @@ __global__ __launch_bounds__(256, VEC && QP == 1 && sizeof(CT) < 4 ? 3 : 2) void
     if constexpr (sizeof(CT) == 1)
       if (lane < TK) {
         in.ks[lane] = ks_next * cs;
-        in.vs[lane] = vs_next;
+        in.vs[lane] = there_next ? vs_next : 0.0f;  // (P is zero there, but not its product with what is no number)
       }
     const bool whole_next = put_info(infos[wave][at ^ 1], next);
     next = page_of(x0 + 8 * TK);
