@@ -709,7 +709,9 @@ ssm_status_t ssm_block_norm_bwd_check(const ssm_block_norm_bwd_params_t *p);
  * are; their exponentials enter the product with v in f32 for f32 inputs, in three bf16
  * parts (24 bits) for bf16 inputs and an f32 o, in two (16 bits) for a bf16 o.
  * A NaN or infinity in a row of v that a query does not see may reach it where another
- * query of its tile of 128 sees that row; rows of other sequences never do.
+ * query of its tile of 128 (from the sequence's first query on) sees that row; rows that
+ * none of these sees, and rows of other sequences, never do.  One in a row of k reaches
+ * only the queries that see it.
  * Workspace: ssm_attn_workspace_size() bytes, 256-byte aligned.
  * Supported: D <= 128, x_dtype and o_dtype f32 or bf16, L and Lk up to 2^30; a launch's
  * 2^32 threads bound the tiles of 64 queries times H to below 2^24.

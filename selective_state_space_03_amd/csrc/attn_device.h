@@ -393,6 +393,27 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int s) {
   return q;
 }
 
+// The keys that some query at the positions p .. last sees, as tiles of BN: the sinks, then those from the window's
+// begin on.  A tile ends where its range does and the rows behind are zeros: a row that none of these queries sees is
+// not in any product, where a NaN would not vanish beside P = 0.
+template <int BN>
+struct AttnKeys {
+  int sinks, first, end;  // sinks ahead of the window, its first key, past the last one
+  int ns, n;              // tiles of sinks, of all
+  __device__ __forceinline__ AttnKeys(const AttnArgs& a, int p, int last) {
+    const int lo = max(0, p - a.window + 1);
+    const bool apart = lo > a.sinks;
+    sinks = apart ? a.sinks : 0;
+    first = apart ? lo : 0;
+    end = last + 1;
+    ns = (sinks + BN - 1) / BN;
+    n = last < 0 ? 0 : ns + (end - first + BN - 1) / BN;
+  }
+  __device__ __forceinline__ int key(int t) const { return t < ns ? t * BN : (t - ns) * BN + first; }  // first of tile t
+  __device__ __forceinline__ int upto(int t) const { return t < ns ? sinks : end; }                    // its rows end
+  __device__ __forceinline__ int window(int t, int w) const { return t < ns ? 0 : w; }                 // of its mask
+};
+
 // The tile of `rows` queries (keys) in slot x of a packed call: its sequence, and its number in it (-1: an
 // unused slot).
 __device__ __forceinline__ int attn_slot(const int32_t* cu, int nseq, long total, int rows, long x, AttnSeq* q, const AttnArgs& a,

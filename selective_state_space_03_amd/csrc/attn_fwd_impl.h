@@ -1,8 +1,8 @@
 // Forward of the window attention for gfx950.
 //
 // A workgroup of four waves takes 64 MT queries of one head, a wave 16 MT of them as columns; the keys and
-// values of the tiles that some query sees (the tiles with sinks, then those from the window's begin to the
-// last query) go through LDS, double buffered, the next tile's loads in flight during the products.  Per tile
+// values that some query sees (the sinks, then those from the window's begin to the last query, in tiles) go
+// through LDS, double buffered, the next tile's loads in flight during the products.  Per tile
 //   S^T = K Q^T   (accumulator columns are queries, so a query's maximum and sum stay in four lanes)
 //   P = 2^(scale log2(e) S - m),  m a running maximum, l the running sum
 //   O^T += V^T P^T   (the tiles of P are operands as they stand; V is read transposed from LDS)
@@ -47,10 +47,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
 
   // tiles that some query of the workgroup sees
   const int last = off + min(w.tile * BM + BM, sq.nq) - 1;  // its last position
-  const int lo = max(0, off + w.tile * BM - a.window + 1);
-  const int first = lo / BN;
-  const int ns = min((a.sinks + BN - 1) / BN, first);
-  const int n = last < 0 ? 0 : ns + max(0, last / BN + 1 - first);
+  const AttnKeys<BN> keys(a, off + w.tile * BM, last);
+  const int n = keys.n;
 
   f32x4 o[MT][NT];
   float mx[MT], l[MT];
@@ -66,14 +64,13 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
 
   uint4 kr[VEC ? 1 : Tile::kPer], vr[VEC ? 1 : Tile::kPer];
   const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
-  const auto key = [&](int t) { return (t < ns ? t : t - ns + first) * BN; };  // first key of tile t
   const auto load = [&](int t) {
     if constexpr (VEC) {
-      Tile::load(lds_address(lds[t & 1]), ks, kb, a.k_stride, key(t), sq.nk, a.D);
-      Tile::load(lds_address(lds[t & 1]) + Tile::kBytes, vs, vb, a.v_stride, key(t), sq.nk, a.D);
+      Tile::load(lds_address(lds[t & 1]), ks, kb, a.k_stride, keys.key(t), keys.upto(t), a.D);
+      Tile::load(lds_address(lds[t & 1]) + Tile::kBytes, vs, vb, a.v_stride, keys.key(t), keys.upto(t), a.D);
     } else {
-      Tile::fetch(kb, a.k_stride, key(t), sq.nk, a.D, a.vec, kr);
-      Tile::fetch(vb, a.v_stride, key(t), sq.nk, a.D, a.vec, vr);
+      Tile::fetch(kb, a.k_stride, keys.key(t), keys.upto(t), a.D, a.vec, kr);
+      Tile::fetch(vb, a.v_stride, keys.key(t), keys.upto(t), a.D, a.vec, vr);
     }
   };
   const auto put = [&](int t) {
@@ -90,10 +87,10 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
     if constexpr (VEC) loads_done();
     lds_barrier();  // tile t is there, and nobody reads the tile before it any more
     if (t + 1 < n) load(t + 1);
-    const int j0 = key(t);
+    const int j0 = keys.key(t), window = keys.window(t, a.window);
     const unsigned char* const kl = lds[t & 1];
     const unsigned char* const vl = kl + Tile::kBytes;
-    const bool some = j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - a.window || j0 < a.sinks);
+    const bool some = j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - window || j0 < a.sinks);
     if (some) {
       f32x4 s[MT][KT];
 #pragma unroll
@@ -108,7 +105,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
 #pragma unroll
           for (int m = 0; m < MT; ++m) s[m][k] = attn_mma<T>(x, q[m][u], s[m][k]);
         }
-      const bool whole = j0 + BN - 1 <= p0 && (j0 > p1 - a.window || j0 + BN <= a.sinks);
+      const bool whole = j0 + BN - 1 <= p0 && (j0 > p1 - window || j0 + BN <= a.sinks);
       if (!whole) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -118,7 +115,7 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(const AttnArgs a, int 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int j = j0 + 16 * k + 4 * g + i;
-              s[m][k][i] = j <= p && (j > p - a.window || j < a.sinks) ? s[m][k][i] : -INFINITY;
+              s[m][k][i] = j <= p && (j > p - window || j < a.sinks) ? s[m][k][i] : -INFINITY;
             }
         }
       }
@@ -230,10 +227,8 @@ __global__ __launch_bounds__(256, 3) void attn_fwd_wide_kernel(const AttnArgs a,
 
   // tiles that some query of the workgroup sees
   const int last = off + min(w.tile * BM + BM, sq.nq) - 1;  // its last position
-  const int lo = max(0, off + w.tile * BM - a.window + 1);
-  const int first = lo / BN;
-  const int ns = min((a.sinks + BN - 1) / BN, first);
-  const int n = last < 0 ? 0 : ns + max(0, last / BN + 1 - first);
+  const AttnKeys<BN> keys(a, off + w.tile * BM, last);
+  const int n = keys.n;
 
   f32x16 o[NT];
 #pragma unroll
@@ -244,18 +239,17 @@ __global__ __launch_bounds__(256, 3) void attn_fwd_wide_kernel(const AttnArgs a,
 
   const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
   const uint32_t lds0 = lds_address(lds[0]), k0 = W::rows_at(lds[0], lane), v0 = W::cols_at(lds[2], lane);
-  const auto key = [&](int t) { return (t < ns ? t : t - ns + first) * BN; };  // first key of tile t
   const auto load = [&](int t) {
-    Tile::load(lds0 + (t & 1) * Tile::kBytes, ks, kb, a.k_stride, key(t), sq.nk, a.D);
-    Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, vs, vb, a.v_stride, key(t), sq.nk, a.D);
+    Tile::load(lds0 + (t & 1) * Tile::kBytes, ks, kb, a.k_stride, keys.key(t), keys.upto(t), a.D);
+    Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, vs, vb, a.v_stride, keys.key(t), keys.upto(t), a.D);
   };
   if (n > 0) load(0);
   for (int t = 0; t < n; ++t) {
     loads_done();
     lds_barrier();  // tile t is there, and nobody reads the tile before it any more
     if (t + 1 < n) load(t + 1);
-    const int j0 = key(t);
-    if (!(j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - a.window || j0 < a.sinks))) continue;
+    const int j0 = keys.key(t), window = keys.window(t, a.window);
+    if (!(j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - window || j0 < a.sinks))) continue;
     // The operands of a step of products are read during the step before it; the order is held, as the
     // compiler would read each right ahead of its use.
     const uint32_t kl = k0 + (t & 1) * Tile::kBytes, vl = v0 + (t & 1) * Tile::kBytes;
@@ -294,7 +288,7 @@ __global__ __launch_bounds__(256, 3) void attn_fwd_wide_kernel(const AttnArgs a,
         s[0] = mma32(kf[0][1], q[KS - 1], s[0]);
       }
     }
-    wide_hide<KT>(s, j0, p0, p0 + c, h, a.window, a.sinks);
+    wide_hide<KT>(s, j0, p0, p0 + c, h, window, a.sinks);
     float top = s[0][0];
 #pragma unroll
     for (int k = 0; k < KT; ++k)
@@ -388,12 +382,9 @@ __global__ __launch_bounds__(512, 2) void attn_fwd_long_kernel(const AttnArgs a,
 
   // tiles that some query of the workgroup sees
   const int last = off + min(w.tile * BM + BM, sq.nq) - 1;  // its last position
-  const int lo = max(0, off + w.tile * BM - a.window + 1);
-  const int first = lo / BN;
-  const int ns = min((a.sinks + BN - 1) / BN, first);
-  const int all = last < 0 ? 0 : ns + max(0, last / BN + 1 - first);
-  const int from = static_cast<int>(static_cast<long>(all) * blockIdx.y / a.nsplit);  // the part's tiles
-  const int n = static_cast<int>(static_cast<long>(all) * (blockIdx.y + 1) / a.nsplit) - from;
+  const AttnKeys<BN> keys(a, off + w.tile * BM, last);
+  const int from = static_cast<int>(static_cast<long>(keys.n) * blockIdx.y / a.nsplit);  // the part's tiles
+  const int n = static_cast<int>(static_cast<long>(keys.n) * (blockIdx.y + 1) / a.nsplit) - from;
 
   f32x16 o[NT], s[KT];
   Frag<NP> p[KT][2];
@@ -405,15 +396,14 @@ __global__ __launch_bounds__(512, 2) void attn_fwd_long_kernel(const AttnArgs a,
 
   const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
   unsigned char(&mine)[4][Tile::kBytes] = lds[half];
-  const auto key = [&](int t) { return (t + from < ns ? t + from : t + from - ns + first) * BN; };  // first key of tile t
   // the half's tile i (none: zeros, so that the number of loads in flight stays)
   const auto load_k = [&](int i) {
     const int t = 2 * i + half;
-    Tile::load(lds_address(mine[i & 1]), ks, kb, a.k_stride, t < n ? key(t) : 0, t < n ? sq.nk : 0, a.D);
+    Tile::load(lds_address(mine[i & 1]), ks, kb, a.k_stride, t < n ? keys.key(t + from) : 0, t < n ? keys.upto(t + from) : 0, a.D);
   };
   const auto load_v = [&](int i) {
     const int t = 2 * i + half;
-    Tile::load(lds_address(mine[2 + (i & 1)]), vs, vb, a.v_stride, t < n ? key(t) : 0, t < n ? sq.nk : 0, a.D);
+    Tile::load(lds_address(mine[2 + (i & 1)]), vs, vb, a.v_stride, t < n ? keys.key(t + from) : 0, t < n ? keys.upto(t + from) : 0, a.D);
   };
   // The operands of a step of products are read during the step before it; the order is held, as the
   // compiler would read each right ahead of its use.
@@ -460,8 +450,8 @@ __global__ __launch_bounds__(512, 2) void attn_fwd_long_kernel(const AttnArgs a,
     }
   };
   const auto softmax = [&](int i) {
-    const int t = 2 * i + half, j0 = t < n ? key(t) : kAttnAll;
-    wide_hide<KT>(s, j0, p0, p0 + c, h, a.window, a.sinks);
+    const int t = 2 * i + half, j0 = t < n ? keys.key(t + from) : kAttnAll;
+    wide_hide<KT>(s, j0, p0, p0 + c, h, keys.window(t + from, a.window), a.sinks);
     float top = s[0][0];
 #pragma unroll
     for (int k = 0; k < KT; ++k)

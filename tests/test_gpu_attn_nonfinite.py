@@ -1,0 +1,89 @@
+"""Where a NaN or an infinity in the window attention's inputs may reach (ssm_attn_fwd): a row of v only the queries of
+tiles (of 128 from the sequence's first query on) in which some query sees it, a row of k only the queries that see it.
+
+With v, everything else has to equal the result of clean inputs bit for bit: a hidden pair adds an exact zero.  With k,
+the scores of other queries may change when a row's running maximum moves: f32 1e-5 of the largest value, bf16 16 bits of
+P (1e-4) and the rounding of both results, 2^-8 of each value."""
+import pytest
+import torch
+
+import selective_state_space_03_amd as ssm
+from gpu_util import DEV
+from oracle import attn_oracle as A
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+NAN, INF = float("nan"), float("inf")
+
+
+def _case(seed, n, L, Lk, Hk, H, D, dtype):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV).to(dtype)  # noqa: E731
+    return rnd(n, L, H, D), rnd(n, Lk, Hk, D), rnd(n, Lk, Hk, D), rnd(n, L, H, D)
+
+
+def _visible(L, Lk, window, sinks):
+    return torch.from_numpy(A.visible(L, Lk, window or 0, sinks))
+
+
+# (sequences, queries, keys, key heads, heads, channels, types of q and o, window, sinks): the kernels for f32, for rows
+# that are not aligned, for results in f32, for many workgroups, for few queries of many keys, for keys in parts
+CASES = [
+    (1, 1, 100, 1, 2, 64, F32, None, 50, 0), (1, 1, 100, 1, 2, 64, BF, None, 50, 0), (1, 300, 300, 1, 2, 64, F32, None, 40, 4),
+    (1, 300, 305, 2, 4, 66, F32, None, 40, 4), (1, 300, 300, 1, 2, 40, BF, None, 40, 4), (1, 300, 331, 2, 4, 66, BF, None, 45, 70),
+    (1, 300, 303, 1, 2, 128, BF, F32, 70, 5), (2, 150, 161, 1, 1, 64, BF, None, None, 0), (1, 290, 290, 1, 2, 64, BF, None, 10, 9),
+    (8, 200, 207, 4, 32, 64, BF, None, 50, 3), (8, 200, 200, 4, 32, 128, BF, None, 33, 0), (4, 400, 433, 4, 32, 96, BF, None, 130, 65),
+    (8, 150, 170, 4, 32, 32, BF, None, None, 0), (8, 200, 220, 4, 32, 64, BF, None, 7, 5),
+    (1, 130, 1501, 1, 2, 64, BF, None, 1100, 3), (1, 300, 1707, 1, 2, 128, BF, None, 1024, 65), (1, 260, 1290, 1, 2, 96, BF, None, None, 0),
+    (1, 5, 3000, 2, 4, 64, BF, None, 2300, 5), (1, 130, 5000, 2, 2, 128, BF, None, 1950, 1),
+]
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
+def test_rows_of_v_that_no_query_of_a_tile_sees(case, bad):
+    n, L, Lk, Hk, H, D, dtype, o_dtype, window, sinks = case
+    q, k, v, _ = _case(L + Lk, n, L, Lk, Hk, H, D, dtype)
+    kw = dict(window=window, sinks=sinks, o_dtype=o_dtype)
+    lse = torch.empty(q.shape[:3], device=DEV)
+    want, see = ssm.attn_fwd(q, k, v, lse=lse, **kw), _visible(L, Lk, window, sinks)
+    assert torch.isfinite(want).all()
+    for i in range(0, L, 128):
+        hidden = (~see[i:i + 128].any(0)).to(DEV)
+        v2, l2 = v.clone(), torch.empty_like(lse)
+        v2[:, hidden] = bad
+        got = ssm.attn_fwd(q, k, v2, lse=l2, **kw)
+        assert torch.equal(got[:, i:i + 128], want[:, i:i + 128]), (i, int(hidden.sum()))
+        assert torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
+def test_rows_of_k_that_a_query_does_not_see(case, bad):
+    n, L, Lk, Hk, H, D, dtype, o_dtype, window, sinks = case
+    q, k, v, _ = _case(L + Lk, n, L, Lk, Hk, H, D, dtype)
+    kw = dict(window=window, sinks=sinks, o_dtype=o_dtype)
+    want, see = ssm.attn_fwd(q, k, v, **kw), _visible(L, Lk, window, sinks)
+    for i in {0, L // 3, L - 1}:
+        k2 = k.clone()
+        k2[:, (~see[i]).to(DEV)] = bad
+        got, ref = ssm.attn_fwd(q, k2, v, **kw)[:, i].double(), want[:, i].double()
+        bound = 1e-5 * ref.abs().max() if want.dtype == F32 else 1e-4 * ref.abs().max() + 2.0 ** -7 * ref.abs()
+        assert ((got - ref).abs() <= bound).all(), i
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rows_of_v_hidden_in_packed_sequences(dtype):
+    """Sequences that begin inside a tile of their neighbours, with keys of their own."""
+    cu, cu_k = [0, 140, 141, 300], [0, 150, 333, 500]
+    q, k, v, _ = _case(5, 1, 300, 500, 2, 4, 64, dtype)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    kw = dict(window=30, sinks=2, cu_seqlens=dev(cu), cu_seqlens_k=dev(cu_k))
+    want = ssm.attn_fwd(q, k, v, **kw)
+    for (a, b), (c, d) in zip(zip(cu, cu[1:]), zip(cu_k, cu_k[1:])):
+        see = _visible(b - a, d - c, 30, 2)
+        for i in range(0, b - a, 128):
+            v2, end = torch.full_like(v, NAN), min(b, a + i + 128)
+            seen = see[i:i + 128].any(0).to(DEV)
+            v2[:, c:d][:, seen] = v[:, c:d][:, seen]
+            assert torch.equal(ssm.attn_fwd(q, k, v2, **kw)[:, a + i:end], want[:, a + i:end]), (a, i)
