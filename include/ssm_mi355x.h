@@ -748,10 +748,12 @@ ssm_status_t ssm_attn_check(const ssm_attn_params_t *p);
  * it is given: an o in bf16 moves dS_pj by P_pj |dout_p||o_p| 2^-9 at most, which is as
  * much as the gradients' rounding to bf16 or, where dS is small, several times that; with
  * its o_rest, or in f32, it does not.  P and dS enter their products as they do in the
- * forward (grad_dtype in the place of o_dtype).  A NaN or infinity in a row of q, k
- * or dout may reach the gradients of rows of its tiles that do not see it, or that it does
- * not see, as one in v does in the forward; rows of other sequences never do.  Queries and
- * keys outside every sequence are not written.
+ * forward (grad_dtype in the place of o_dtype).  A NaN or infinity in a row of k may
+ * reach the dq of a query that does not see it where another query of its tile of 256 does,
+ * and one in a row of q or dout the dk and dv of a key that this query does not see where
+ * it sees another key of that key's tile of 64 (tiles from the sequence's first row on).
+ * One in a row of v reaches only the dq of queries that see it and its own dk; rows of other
+ * sequences never reach any.  Queries and keys outside every sequence are not written.
  * Workspace: ssm_attn_bwd_workspace_size() bytes, 256-byte aligned.
  * ---------------------------------------------------------------------- */
 typedef struct ssm_attn_bwd_params {

@@ -73,10 +73,8 @@ __device__ __forceinline__ void attn_dq(const AttnArgs& a, unsigned char* mem, u
   }
 
   const int last = off + min(w.tile * BM + BM, sq.nq) - 1;
-  const int lo = max(0, off + w.tile * BM - a.window + 1);
-  const int first = lo / BN;
-  const int ns = min((a.sinks + BN - 1) / BN, first);
-  const int n = last < 0 ? 0 : ns + max(0, last / BN + 1 - first);
+  const AttnKeys<BN> keys(a, off + w.tile * BM, last);
+  const int n = keys.n;
 
   f32x4 dq[MT][NT];
 #pragma unroll
@@ -89,14 +87,13 @@ __device__ __forceinline__ void attn_dq(const AttnArgs& a, unsigned char* mem, u
 
   uint4 kr[VEC ? 1 : Tile::kPer], vr[VEC ? 1 : Tile::kPer];
   const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
-  const auto key = [&](int t) { return (t < ns ? t : t - ns + first) * BN; };  // first key of tile t
   const auto load = [&](int t) {
     if constexpr (VEC) {
-      Tile::load(lds_address(lds[t & 1]), ks, kb, a.k_stride, key(t), sq.nk, a.D);
-      Tile::load(lds_address(lds[t & 1]) + Tile::kBytes, vs, vb, a.v_stride, key(t), sq.nk, a.D);
+      Tile::load(lds_address(lds[t & 1]), ks, kb, a.k_stride, keys.key(t), keys.upto(t), a.D);
+      Tile::load(lds_address(lds[t & 1]) + Tile::kBytes, vs, vb, a.v_stride, keys.key(t), keys.upto(t), a.D);
     } else {
-      Tile::fetch(kb, a.k_stride, key(t), sq.nk, a.D, a.vec, kr);
-      Tile::fetch(vb, a.v_stride, key(t), sq.nk, a.D, a.vec, vr);
+      Tile::fetch(kb, a.k_stride, keys.key(t), keys.upto(t), a.D, a.vec, kr);
+      Tile::fetch(vb, a.v_stride, keys.key(t), keys.upto(t), a.D, a.vec, vr);
     }
   };
   const auto put = [&](int t) {
@@ -113,12 +110,12 @@ __device__ __forceinline__ void attn_dq(const AttnArgs& a, unsigned char* mem, u
     if constexpr (VEC) loads_done();
     lds_barrier();  // tile t is there, and nobody reads the tile before it any more
     if (t + 1 < n) load(t + 1);
-    const int j0 = key(t);
+    const int j0 = keys.key(t), window = keys.window(t, a.window);
     const unsigned char* const kl = lds[t & 1];
     const unsigned char* const vl = kl + Tile::kBytes;
-    const bool some = j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - a.window || j0 < a.sinks);
+    const bool some = j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - window || j0 < a.sinks);
     if (some) {
-      const bool whole = j0 + BN - 1 <= p0 && (j0 > p1 - a.window || j0 + BN <= a.sinks);
+      const bool whole = j0 + BN - 1 <= p0 && (j0 > p1 - window || j0 + BN <= a.sinks);
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
         f32x4 s[MT][PU], dp[MT][PU];
@@ -153,7 +150,7 @@ __device__ __forceinline__ void attn_dq(const AttnArgs& a, unsigned char* mem, u
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int j = j0 + 16 * (PU * u + e) + 4 * g + i;
-                s[m][e][i] = j <= p && (j > p - a.window || j < a.sinks) && !lone ? s[m][e][i] : 0.0f;
+                s[m][e][i] = j <= p && (j > p - window || j < a.sinks) && !lone ? s[m][e][i] : 0.0f;
               }
           }
           f[m] = attn_operand<T, NP>(s[m]);
@@ -244,7 +241,7 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& a, unsigned char* mem, 
     }
   }
 
-  // queries that see some key of the workgroup
+  // queries that see some key of the workgroup: others, in whose rows a NaN would not vanish beside P = 0, are not loaded
   long lo = max(0, jt - off), hi = sq.nq - 1L;
   if (a.window != kAttnAll && jt >= a.sinks) hi = min(hi, static_cast<long>(min(jt + BM, sq.nk)) + a.window - 2 - off);
   if (sink) {
@@ -252,8 +249,8 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& a, unsigned char* mem, 
     hi = min(hi, static_cast<long>(piece) * a.span + a.span - 1);
   }
   if (jt >= sq.nk) hi = -1;
-  const int first = static_cast<int>(lo / BN);
-  const int per = hi < lo ? 0 : static_cast<int>(hi / BN) + 1 - first;  // tiles of a head
+  const int first = static_cast<int>(lo), upto = static_cast<int>(hi) + 1;  // (rows from upto on: zeros, and P = 0)
+  const int per = upto <= first ? 0 : (upto - first + BN - 1) / BN;         // tiles of a head
   const int n = per * heads, steps = (n + 1) / 2;  // of both halves, of one
 
   f32x4 dk[MT][NT], dv[MT][NT];
@@ -268,22 +265,27 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& a, unsigned char* mem, 
   float st = 0.0f;
   const long dstride = static_cast<long>(a.h) * a.D;
   const typename Tile::Source qs = Tile::source(a.q_stride, a.D), ds = Tile::source(dstride, a.D);
+  int head = kh * heads, row0 = first;  // of the tile asked for next
+  const int stop = first + per * BN;
+  const auto skip = [&](int by) {
+    for (row0 += by * BN; row0 >= stop && per > 0; row0 -= per * BN) ++head;
+  };
   const auto load = [&](int t) {
-    const int x = 2 * t + half, head = kh * heads + x / per, i0 = (first + x % per) * BN;
+    const int i0 = row0;
     const T* const qb = static_cast<const T*>(a.q) + sq.q0 * a.q_stride + static_cast<long>(head) * a.D;
     const T* const db = static_cast<const T*>(a.dout) + (sq.q0 * a.h + head) * a.D;
     if constexpr (VEC) {
-      Tile::load(lds_address(lds[t & 1]), qs, qb, a.q_stride, i0, sq.nq, a.D);
-      Tile::load(lds_address(lds[t & 1]) + Tile::kBytes, ds, db, dstride, i0, sq.nq, a.D);
+      Tile::load(lds_address(lds[t & 1]), qs, qb, a.q_stride, i0, upto, a.D);
+      Tile::load(lds_address(lds[t & 1]) + Tile::kBytes, ds, db, dstride, i0, upto, a.D);
     } else {
-      Tile::fetch(qb, a.q_stride, i0, sq.nq, a.D, a.vec, qr);
-      Tile::fetch(db, dstride, i0, sq.nq, a.D, a.vec, dr);
+      Tile::fetch(qb, a.q_stride, i0, upto, a.D, a.vec, qr);
+      Tile::fetch(db, dstride, i0, upto, a.D, a.vec, dr);
     }
     if (x256 < 2 * BN) {  // lse, then delta
       const int i = i0 + x256 % BN;
       const long row = (sq.q0 + i) * a.h + head;
       st = x256 < BN ? INFINITY : 0.0f;
-      if (i < sq.nq) st = x256 < BN ? attn_lse2(a.lse[row]) : a.delta[row];
+      if (i < upto) st = x256 < BN ? attn_lse2(a.lse[row]) : a.delta[row];
     }
   };
   const auto put = [&](int t) {
@@ -294,6 +296,8 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& a, unsigned char* mem, 
     }
     if (x256 < 2 * BN) reinterpret_cast<float*>(to + 2 * Tile::kBytes)[x256] = st;
   };
+  skip(half);
+  int now = row0;  // of the tile at hand
   if (half < n) {
     load(0);
     put(0);
@@ -302,14 +306,18 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& a, unsigned char* mem, 
     if constexpr (VEC) loads_done();
     lds_barrier();
     const bool more = 2 * (t + 1) + half < n;
-    if (more) load(t + 1);
+    const int i0 = now, p0 = off + i0, p1 = p0 + BN - 1;
+    if (more) {
+      skip(2);
+      now = row0;
+      load(t + 1);
+    }
     const unsigned char* const ql = lds[t & 1];
     const unsigned char* const dl = ql + Tile::kBytes;
     const float* const sl = reinterpret_cast<const float*>(ql + 2 * Tile::kBytes);
-    const int i0 = (first + (2 * t + half) % per) * BN, p0 = off + i0, p1 = p0 + BN - 1;
     const bool some = 2 * t + half < n && j0 <= p1 && j0 < sq.nk && (j1 > p0 - a.window || j0 < a.sinks);
     if (some) {
-      const bool whole = j1 <= p0 && (j0 > p1 - a.window || j1 < a.sinks) && i0 + BN <= sq.nq;
+      const bool whole = j1 <= p0 && (j0 > p1 - a.window || j1 < a.sinks) && i0 + BN <= upto;
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
         f32x4 s[MT][PU], dp[MT][PU];
@@ -345,7 +353,7 @@ __device__ __forceinline__ void attn_dkv(const AttnArgs& a, unsigned char* mem, 
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int r = i0 + 16 * (PU * u + e) + 4 * g + i, p = off + r;
-                const bool see = j <= p && (j > p - a.window || j < a.sinks) && r < sq.nq;
+                const bool see = j <= p && (j > p - a.window || j < a.sinks) && r < upto;
                 s[m][e][i] = see ? s[m][e][i] : 0.0f;
                 dp[m][e][i] = see && p != 0 && !lone_all ? dp[m][e][i] : 0.0f;
               }
@@ -479,10 +487,8 @@ __device__ __forceinline__ void attn_dq_wide(const AttnArgs& a, unsigned char* m
   }
 
   const int last = off + min(w.tile * BM + BM, sq.nq) - 1;
-  const int lo = max(0, off + w.tile * BM - a.window + 1);
-  const int first = lo / BN;
-  const int ns = min((a.sinks + BN - 1) / BN, first);
-  const int n = last < 0 ? 0 : ns + max(0, last / BN + 1 - first);
+  const AttnKeys<BN> keys(a, off + w.tile * BM, last);
+  const int n = keys.n;
 
   f32x16 dq[NT];
 #pragma unroll
@@ -493,18 +499,17 @@ __device__ __forceinline__ void attn_dq_wide(const AttnArgs& a, unsigned char* m
 
   const typename Tile::Source ks = Tile::source(a.k_stride, a.D), vs = Tile::source(a.v_stride, a.D);
   const uint32_t lds0 = lds_address(lds[0]), k0 = W::rows_at(lds[0], lane), v0 = W::rows_at(lds[2], lane), c0 = W::cols_at(lds[0], lane);
-  const auto key = [&](int t) { return (t < ns ? t : t - ns + first) * BN; };
   const auto load = [&](int t) {
-    Tile::load(lds0 + (t & 1) * Tile::kBytes, ks, kb, a.k_stride, key(t), sq.nk, a.D);
-    Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, vs, vb, a.v_stride, key(t), sq.nk, a.D);
+    Tile::load(lds0 + (t & 1) * Tile::kBytes, ks, kb, a.k_stride, keys.key(t), keys.upto(t), a.D);
+    Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, vs, vb, a.v_stride, keys.key(t), keys.upto(t), a.D);
   };
   if (n > 0) load(0);
   for (int t = 0; t < n; ++t) {
     loads_done();
     lds_barrier();
     if (t + 1 < n) load(t + 1);
-    const int j0 = key(t);
-    if (!(j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - a.window || j0 < a.sinks))) continue;
+    const int j0 = keys.key(t), window = keys.window(t, a.window);
+    if (!(j0 <= p1 && i0 < sq.nq && (j0 + BN - 1 > p0 - window || j0 < a.sinks))) continue;
     const uint32_t kl = k0 + (t & 1) * Tile::kBytes, vl = v0 + (t & 1) * Tile::kBytes, cl = c0 + (t & 1) * Tile::kBytes;
     f32x16 s = {}, dp = {};
     uint4 kf[3][2], cf[2][NT];
@@ -540,8 +545,8 @@ __device__ __forceinline__ void attn_dq_wide(const AttnArgs& a, unsigned char* m
       __builtin_amdgcn_sched_barrier(0);
     }
     products_done();
-    if (!(j0 + BN - 1 <= p0 && (j0 > p1 - a.window || j0 + BN <= a.sinks))) {
-      const int pos = p0 + c, d = pos - j0 - 4 * h, v = d - a.window, f = a.sinks - j0 - 4 * h;
+    if (!(j0 + BN - 1 <= p0 && (j0 > p1 - window || j0 + BN <= a.sinks))) {
+      const int pos = p0 + c, d = pos - j0 - 4 * h, v = d - window, f = a.sinks - j0 - 4 * h;
       const bool lone = pos == 0 || lone_all;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
@@ -641,7 +646,7 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
     for (int u = 0; u < KS; ++u) k[u] = load16_if(row + 16 * u + 8 * h, j < sq.nk && 16 * u + 8 * h < a.D);
   }
 
-  // queries that see some key of the workgroup
+  // queries that see some key of the workgroup: others, in whose rows a NaN would not vanish beside P = 0, are not loaded
   long lo = max(0, jt - off), hi = sq.nq - 1L;
   if (a.window != kAttnAll && jt >= a.sinks) hi = min(hi, static_cast<long>(min(jt + BM, sq.nk)) + a.window - 2 - off);
   if (sink) {
@@ -649,8 +654,8 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
     hi = min(hi, static_cast<long>(piece) * a.span + a.span - 1);
   }
   if (jt >= sq.nk) hi = -1;
-  const int first = static_cast<int>(lo / BN);
-  const int per = hi < lo ? 0 : static_cast<int>(hi / BN) + 1 - first;  // tiles of a head
+  const int first = static_cast<int>(lo), upto = static_cast<int>(hi) + 1;  // (rows from upto on: zeros, and P = 0)
+  const int per = upto <= first ? 0 : (upto - first + BN - 1) / BN;         // tiles of a head
   const int n = per * heads, steps = (n + G - 1) / G;
 
   f32x16 dk[NT], dv[NT];
@@ -666,24 +671,25 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
   const uint32_t vl = Wide<VTile>::rows_at(vlds + wave % 2 * 32 * VTile::kStride, lane);
   const bool stater = threadIdx.x % 128 < 2 * BN;
   float st = 0.0f;
-  int head = kh * heads, tile = first;  // of the tile asked for next
+  int head = kh * heads, row = first;  // of the tile asked for next
+  const int stop = first + per * BN;
   const auto skip = [&](int by) {
-    for (tile += by; tile >= first + per && per > 0; tile -= per) ++head;
+    for (row += by * BN; row >= stop && per > 0; row -= per * BN) ++head;
   };
   const auto load = [&](int t) {
-    const int i0 = tile * BN;
+    const int i0 = row;
     Tile::load(lds0 + (t & 1) * Tile::kBytes, qs, static_cast<const bf16s*>(a.q) + sq.q0 * a.q_stride + static_cast<long>(head) * a.D, a.q_stride,
-               i0, sq.nq, a.D);
-    Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, ds, static_cast<const bf16s*>(a.dout) + (sq.q0 * a.h + head) * a.D, dstride, i0, sq.nq, a.D);
+               i0, upto, a.D);
+    Tile::load(lds0 + (2 + (t & 1)) * Tile::kBytes, ds, static_cast<const bf16s*>(a.dout) + (sq.q0 * a.h + head) * a.D, dstride, i0, upto, a.D);
     if (stater) {
       const int x = threadIdx.x % (2 * BN), i = i0 + x % BN;
       const long row = (sq.q0 + i) * a.h + head;
       st = x < BN ? -INFINITY : 0.0f;
-      if (i < sq.nq) st = x < BN ? attn_lse2(a.lse[row]) * -inv : -a.delta[row];
+      if (i < upto) st = x < BN ? attn_lse2(a.lse[row]) * -inv : -a.delta[row];
     }
   };
   skip(g);
-  int now = tile;  // the tile at hand
+  int now = row;  // of the tile at hand
   if (g < n) {
     load(0);
     if (stater) stats[g][0][threadIdx.x % (2 * BN)] = st;
@@ -692,10 +698,10 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
     loads_done();
     lds_barrier();
     const bool more = G * (t + 1) + g < n;
-    const int i0 = now * BN, p0 = off + i0, p1 = p0 + BN - 1;
+    const int i0 = now, p0 = off + i0, p1 = p0 + BN - 1;
     if (more) {
       skip(G);
-      now = tile;
+      now = row;
       load(t + 1);
     }
     if (G * t + g < n && j0 <= p1 && j0 < sq.nk && (j1 > p0 - a.window || j0 < a.sinks)) {
@@ -749,14 +755,14 @@ __device__ __forceinline__ void attn_dkv_wide(const AttnArgs& a, unsigned char* 
         __builtin_amdgcn_sched_barrier(0);
       }
       products_done();
-      if (!(j1 <= p0 && (j0 > p1 - a.window || j1 < a.sinks) && i0 + BN <= sq.nq)) {
-        const int j = j0 + c, d = j - p0 - 4 * h, end = sq.nq - i0 - 4 * h;  // rows from d on, before d + window (or a sink), before end
+      if (!(j1 <= p0 && (j0 > p1 - a.window || j1 < a.sinks) && i0 + BN <= upto)) {
+        const int j = j0 + c, d = j - p0 - 4 * h, end = upto - i0 - 4 * h;  // rows from d on, before d + window (or a sink), before end
         const long far = j < a.sinks ? static_cast<long>(kAttnAll) * 2 : static_cast<long>(d) + a.window;
-        const int upto = static_cast<int>(min(static_cast<long>(end), far)), zero = -p0 - 4 * h;  // the row at position 0
+        const int past = static_cast<int>(min(static_cast<long>(end), far)), zero = -p0 - 4 * h;  // the row at position 0
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int r = 8 * (e / 4) + e % 4;
-          const bool see = r >= d && r < upto;
+          const bool see = r >= d && r < past;
           s[e] = see ? s[e] : 0.0f;
           dp[e] = see && r != zero && !lone_all ? dp[e] : 0.0f;
         }

@@ -398,20 +398,20 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int s) {
 // not in any product, where a NaN would not vanish beside P = 0.
 template <int BN>
 struct AttnKeys {
-  int sinks, first, end;  // sinks ahead of the window, its first key, past the last one
-  int ns, n;              // tiles of sinks, of all
+  int sinks, end;    // sinks ahead of the window, past the last key
+  int ns, n, shift;  // tiles of sinks, of all; from where tiles of the window would lie to where they do
   __device__ __forceinline__ AttnKeys(const AttnArgs& a, int p, int last) {
     const int lo = max(0, p - a.window + 1);
     const bool apart = lo > a.sinks;
     sinks = apart ? a.sinks : 0;
-    first = apart ? lo : 0;
     end = last + 1;
     ns = (sinks + BN - 1) / BN;
-    n = last < 0 ? 0 : ns + (end - first + BN - 1) / BN;
+    shift = (apart ? lo : 0) - ns * BN;
+    n = last < 0 ? 0 : (end - shift + BN - 1) / BN;
   }
-  __device__ __forceinline__ int key(int t) const { return t < ns ? t * BN : (t - ns) * BN + first; }  // first of tile t
-  __device__ __forceinline__ int upto(int t) const { return t < ns ? sinks : end; }                    // its rows end
-  __device__ __forceinline__ int window(int t, int w) const { return t < ns ? 0 : w; }                 // of its mask
+  __device__ __forceinline__ int key(int t) const { return t * BN + (t < ns ? 0 : shift); }  // first of tile t
+  __device__ __forceinline__ int upto(int t) const { return t < ns ? sinks : end; }           // its rows end
+  __device__ __forceinline__ int window(int t, int w) const { return t < ns ? 0 : w; }        // of its mask
 };
 
 // The tile of `rows` queries (keys) in slot x of a packed call: its sequence, and its number in it (-1: an

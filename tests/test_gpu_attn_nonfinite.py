@@ -1,4 +1,4 @@
-"""Where a NaN or an infinity in the window attention's inputs may reach (ssm_attn_fwd): a row of v only the queries of
+"""Where a NaN or an infinity in the window attention's inputs may reach (ssm_attn_fwd, ssm_attn_bwd): a row of v only the queries of
 tiles (of 128 from the sequence's first query on) in which some query sees it, a row of k only the queries that see it.
 
 With v, everything else has to equal the result of clean inputs bit for bit: a hidden pair adds an exact zero.  With k,
@@ -87,3 +87,49 @@ def test_rows_of_v_hidden_in_packed_sequences(dtype):
             seen = see[i:i + 128].any(0).to(DEV)
             v2[:, c:d][:, seen] = v[:, c:d][:, seen]
             assert torch.equal(ssm.attn_fwd(q, k, v2, **kw)[:, a + i:end], want[:, a + i:end]), (a, i)
+
+
+def _grads(c, o, lse, kw, **new):
+    q, k, v, do = (new.get(x, t) for x, t in zip(("q", "k", "v", "do"), c))
+    return ssm.attn_bwd(q, k, v, o, lse, do, **kw)
+
+
+# as above, with the type of the gradients: f32, rows that are not aligned, gradients in f32, aligned bf16 with sinks in
+# pieces and not, two heads a workgroup and one
+GRADS = [
+    (1, 300, 305, 1, 2, 64, F32, F32, 40, 4), (1, 300, 300, 2, 4, 66, F32, F32, None, 0), (1, 300, 331, 1, 3, 66, BF, BF, 45, 70),
+    (1, 300, 303, 1, 2, 128, BF, F32, 70, 5), (1, 600, 600, 1, 2, 64, BF, BF, 40, 4), (1, 600, 633, 1, 3, 128, BF, BF, 100, 65),
+    (2, 400, 410, 2, 4, 96, BF, BF, None, 0), (1, 500, 450, 1, 1, 32, BF, BF, 33, 300), (1, 400, 407, 1, 2, 64, BF, BF, 7, 5),
+]
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("case", GRADS, ids=[str(i) for i in range(len(GRADS))])
+def test_gradients(case, bad):
+    """A row of k reaches the dq of the queries of tiles of 256 in which some query sees it (and its own dk, dv); a row
+    of q or dout the dk and dv of the tiles of 64 keys of which it sees some (and its own dq); a row of v the dq of
+    the queries that see it and its own dk."""
+    n, L, Lk, Hk, H, D, dtype, gd, window, sinks = case
+    c = _case(L + Lk, n, L, Lk, Hk, H, D, dtype)
+    mask = dict(window=window, sinks=sinks)
+    lse = torch.empty(c[0].shape[:3], device=DEV)
+    o, see = ssm.attn_fwd(*c[:3], lse=lse, **mask), _visible(L, Lk, window, sinks)
+    kw = dict(mask, grad_dtype=gd)
+    want = _grads(c, o, lse, kw)
+    poisoned = lambda t, rows: t.masked_fill(rows.to(DEV)[None, :, None, None], bad)  # noqa: E731
+    for i in range(0, L, 256):
+        got = _grads(c, o, lse, kw, k=poisoned(c[1], ~see[i:i + 256].any(0)))
+        assert torch.equal(got["q"][:, i:i + 256], want["q"][:, i:i + 256]), i
+    for j in range(0, Lk, 64):
+        blind = ~see[:, j:j + 64].any(1)
+        for x, t in (("q", c[0]), ("do", c[3])):
+            got = _grads(c, o, lse, kw, **{x: poisoned(t, blind)})
+            for g in ("k", "v"):
+                assert torch.equal(got[g][:, j:j + 64], want[g][:, j:j + 64]), (x, g, j)
+            assert torch.equal(got["q"][:, ~blind], want["q"][:, ~blind]), (x, j)
+    for i in {0, L // 2, L - 1}:
+        got = _grads(c, o, lse, kw, v=poisoned(c[2], ~see[i]))
+        assert torch.equal(got["q"][:, i], want["q"][:, i]) and torch.equal(got["v"], want["v"])
+        assert torch.equal(got["k"][:, see[i]], want["k"][:, see[i]])
+        got = _grads(c, o, lse, kw, k=poisoned(c[1], ~see[i]))
+        assert torch.equal(got["k"][:, see[i]], want["k"][:, see[i]]) and torch.equal(got["v"][:, see[i]], want["v"][:, see[i]])
