@@ -830,6 +830,9 @@ ssm_status_t ssm_attn_cache_check(const ssm_attn_cache_params_t *p);
  * table counts as table_rows * page_size.  The result equals the last row of ssm_attn_fwd
  * over the values that the cache stands for.
  * cache_dtype: x_dtype, or SSM_E4M3, or bf16 beside an f32 x_dtype.
+ * A key with infinite channels whose score is -infinity vanishes, but not from a bf16 cache
+ * beside an f32 q, whose parts may be zero: there it may give NaN.  An infinity in a visible
+ * row of v gives an infinity or NaN.
  * Workspace: ssm_attn_decode_workspace_size() bytes, 256-byte aligned.
  * Supported: D <= 128; Bt * H below 2^24; page_size up to 65536, table_rows * page_size up
  * to 2^30.

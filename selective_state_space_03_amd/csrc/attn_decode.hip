@@ -112,6 +112,7 @@ __global__ __launch_bounds__(256, VEC && QP == 1 && sizeof(CT) < 4 ? 3 : 2) void
   constexpr int TK = sizeof(T) == 2 ? 32 : 16;             // keys of a tile: one unit
   constexpr int KT = TK / 16, KS = DQ / E::kUnit, NT = DQ / 16;
   constexpr int UW = C::kUnitBytes / 4;                    // words of K's units
+  constexpr int kRagged = (DQ - 32) / E::kUnit;            // units from here on may hold channels past D
   constexpr int W8 = sizeof(CT) == 1 ? DQ / 64 * 2 : 0;    // units loaded two at a time, 16 codes a lane
   constexpr int CH = 16 / static_cast<int>(sizeof(CT));    // elements of 16 bytes
   constexpr int CPR = DQ / CH, NV = TK * CPR / 64;         // those of a row, of a lane
@@ -207,7 +208,8 @@ __global__ __launch_bounds__(256, VEC && QP == 1 && sizeof(CT) < 4 ? 3 : 2) void
   uint32_t kn[KT][KS * UW];
   uint4 vn[NV];
   const auto fetch = [&](const Info& in, bool whole) {
-    // (channels past D: K's meet zeros of q, V's are not stored; in the aligned form they read channel 0 on)
+    // (channels past D: in the aligned form they read channel 0 on; V's are not stored, K's are put to zero where they
+    // are used, as an infinite one beside the zeros of q would not vanish; a code is never infinite)
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
       const CT* const row = kc + in.base[16 * k + c];
@@ -283,7 +285,8 @@ __global__ __launch_bounds__(256, VEC && QP == 1 && sizeof(CT) < 4 ? 3 : 2) void
       s[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
-        const uint4 kf = C::op(&kn[k][u * UW]);
+        uint4 kf = C::op(&kn[k][u * UW]);
+        if (VEC && sizeof(CT) > 1 && u >= kRagged && chan(u) >= a.D) kf = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int p = QP - 1; p >= 0; --p) s[k] = attn_mma<T>(kf, q[u].p[p], s[k]);
       }

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import selective_state_space_03_amd as ssm
-from gpu_util import DEV
+from gpu_util import DEV, check, np64
 from oracle import attn_oracle as A
 
 pytestmark = pytest.mark.gpu
@@ -133,3 +133,21 @@ def test_gradients(case, bad):
         assert torch.equal(got["k"][:, see[i]], want["k"][:, see[i]])
         got = _grads(c, o, lse, kw, k=poisoned(c[1], ~see[i]))
         assert torch.equal(got["k"][:, see[i]], want["k"][:, see[i]]) and torch.equal(got["v"][:, see[i]], want["v"][:, see[i]])
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 40), (BF, 80), (BF, 64), (BF, 66), (F32, 40), (F32, 36), (F32, 100), (F32, 64)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_a_step_over_infinite_keys(dtype, D, sign):
+    """A key whose score is -infinity vanishes from the step: infinite channels, the first and the last among them,
+    against queries of the other sign there.  Cache and queries of one type."""
+    lens, page, hk, h = [100, 33, 7], 16, 2, 4
+    gen = torch.Generator(device=DEV).manual_seed(D)
+    rnd = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731
+    table = torch.randperm(21, generator=gen, device=DEV).to(torch.int32).view(3, 7)
+    q, kc, vc = rnd(3, h, D).to(dtype), rnd(21, hk, page, D).to(dtype), rnd(21, hk, page, D).to(dtype)
+    for ch, pages in ((0, table[:, 0]), (D - 1, table[:, 1])):
+        q[..., ch] = -sign * (q[..., ch].abs() + 0.5)
+        kc[pages.long(), :, 3, ch] = sign * INF
+    o = ssm.attn_decode_step(q, kc, vc, table, torch.tensor(lens, dtype=torch.int32, device=DEV))
+    want = A.decode_step(np64(q), np64(kc), np64(vc), table.cpu().numpy(), lens)
+    check(np64(o), want, 1e-5, "o", out_bf16=dtype == BF)
