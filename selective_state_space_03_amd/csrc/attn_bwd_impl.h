@@ -546,7 +546,8 @@ __device__ __forceinline__ void attn_dq_wide(const AttnArgs& a, unsigned char* m
     }
     products_done();
     if (!(j0 + BN - 1 <= p0 && (j0 > p1 - window || j0 + BN <= a.sinks))) {
-      const int pos = p0 + c, d = pos - j0 - 4 * h, v = d - window, f = a.sinks - j0 - 4 * h;
+      const int pos = p0 + c;
+      const auto [d, v, f] = wide_mask(pos, j0, h, window, a.sinks);
       const bool lone = pos == 0 || lone_all;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {

@@ -248,11 +248,21 @@ __device__ __forceinline__ Frag<NP> wide_operand(const f32x16& x, int s) {
   for (int p = 0; p < NP; ++p) f.p[p] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
   return f;
 }
+// Of a lane in half h with the query at pos, and a tile of keys from j0 on: key j0 + 4 h + j is seen if j <= d
+// and (j > w or j < f).
+struct WideMask {
+  int d, w, f;
+};
+__host__ __device__ constexpr WideMask wide_mask(int pos, int j0, int h, int window, int sinks) {
+  return {pos - j0 - 4 * h, pos - j0 - 4 * h - window, sinks - j0 - 4 * h};
+}
+// A key that none of the 32 queries from position p0 on sees: where a tile that is not there lies
+__host__ __device__ constexpr int wide_none(int p0) { return p0 + 32; }
 // Scores of a tile from key j0 on, of queries from position p0 on (32 of them, the lane's at pos), of keys that
 // are not seen.  Tiles in which every query sees every key pass by; others mostly meet one border.
 template <int KT>
 __device__ __forceinline__ void wide_hide(f32x16 (&s)[KT], int j0, int p0, int pos, int h, int window, int sinks) {
-  const int d = pos - j0 - 4 * h, w = d - window, f = sinks - j0 - 4 * h;
+  const auto [d, w, f] = wide_mask(pos, j0, h, window, sinks);
   if (j0 + 32 * KT - 1 > p0) {
 #pragma unroll
     for (int k = 0; k < KT; ++k)

@@ -450,7 +450,7 @@ __global__ __launch_bounds__(512, 2) void attn_fwd_long_kernel(const AttnArgs a,
     }
   };
   const auto softmax = [&](int i) {
-    const int t = 2 * i + half, j0 = t < n ? keys.key(t + from) : kAttnAll;
+    const int t = 2 * i + half, j0 = t < n ? keys.key(t + from) : wide_none(p0);
     wide_hide<KT>(s, j0, p0, p0 + c, h, keys.window(t + from, a.window), a.sinks);
     float top = s[0][0];
 #pragma unroll
