@@ -117,10 +117,11 @@ __global__ __launch_bounds__(256, VEC && QP == 1 && sizeof(CT) < 4 ? 3 : 2) void
   constexpr int CH = 16 / static_cast<int>(sizeof(CT));    // elements of 16 bytes
   constexpr int CPR = DQ / CH, NV = TK * CPR / 64;         // those of a row, of a lane
   constexpr int VS = DQ * static_cast<int>(sizeof(CT)) + 16;
-  struct Info {  // of a tile's keys
+  struct __align__(16) Info {                              // of a tile's keys, read 16 bytes at a time
     long base[TK];                                         // first element of the row
     float add[TK], ks[TK], vs[TK];                         // 0, or -infinity: left out; scales
   };
+  static_assert(alignof(Info) == 16 && sizeof(long) * TK % 16 == 0 && sizeof(float) * TK % 16 == 0, "16-byte reads");
   constexpr int kRed = 4 * 16 * (DQ + 2) * 4, kTiles = 4 * TK * VS;
   __shared__ __align__(16) unsigned char tiles[kTiles > kRed ? kTiles : kRed];
   __shared__ Info infos[4][2];
