@@ -372,9 +372,20 @@ def _discretization(name):
     return codes[name]
 
 
+class _Handle(ctypes.c_void_p):
+    """A stream's handle with the index of its device, which a null handle does not tell."""
+
+    def __init__(self, value, device):
+        super().__init__(value)
+        self.device = device
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(device, stream):
     s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    return _Handle(s.cuda_stream, device.index)
 
 
 def _torch_stream(handle, device):
@@ -401,14 +412,20 @@ def _empty(shape, dtype, device, stream):
 
 class Call:
     """One marshalled entry-point call.  run() enqueues it (again) on the same
-    stream with the same buffers and returns the output tensor; the tensors
-    the call reads and writes are kept alive here."""
+    stream of the tensors' device, whichever is current, with the same buffers
+    and returns the output tensor; the tensors the call reads and writes are
+    kept alive here."""
 
     def __init__(self, fn, params, stream, out, keep):
         self._fn, self._p, self._stream, self.out, self._keep = fn, params, stream, out, keep
+        self._device = stream.device
 
     def run(self):
-        _raise(self._fn(ctypes.byref(self._p), self._stream))
+        if self._device == _current_device():
+            _raise(self._fn(ctypes.byref(self._p), self._stream))
+        else:  # (the null stream is the current device's, and so are launches)
+            with torch.cuda.device(self._device):
+                _raise(self._fn(ctypes.byref(self._p), self._stream))
         return self.out
 
 

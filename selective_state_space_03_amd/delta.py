@@ -15,6 +15,7 @@ from .binding import (
     DeltaChunkBwdParams,
     DeltaChunkParams,
     DeltaDecodeParams,
+    _Handle,
     _code,
     _empty,
     _ptr,
@@ -31,7 +32,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _on(device, stream):
     """The stream's handle, without building a Stream object for the current one."""
     if stream is None and _raw_stream is not None and device.index is not None:
-        return ctypes.c_void_p(_raw_stream(device.index))
+        return _Handle(_raw_stream(device.index), device.index)
     return _stream(device, stream)
 
 
