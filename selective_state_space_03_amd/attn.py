@@ -15,9 +15,9 @@ from .binding import (
     AttnDecodeParams,
     AttnParams,
     Call,
+    _clear,
     _code,
     _empty,
-    _torch_stream,
     lib,
 )
 from .delta import _arg, _dtype, _fits, _gpu, _on, _rows, _workspace
@@ -33,9 +33,7 @@ class _PackedGrads(Call):
     run clears the gradients first, on the call's stream (the offsets may have changed since the last)."""
 
     def run(self):
-        with torch.cuda.stream(_torch_stream(self._stream.value, self.out["q"].device)):
-            for t in self.out.values():
-                t.zero_()
+        _clear(list(self.out.values()), self._stream.value)
         return super().run()
 
 

@@ -16,11 +16,11 @@ from .binding import (
     DeltaChunkParams,
     DeltaDecodeParams,
     _Handle,
+    _clear,
     _code,
     _empty,
     _ptr,
     _stream,
-    _torch_stream,
     lib,
 )
 
@@ -107,10 +107,7 @@ class _PackedGrads(Call):
     each run clears their gradients first, on the call's stream (the offsets may have changed since the last)."""
 
     def run(self):
-        clear = [self.out[name] for name in ("q", "k", "v", "g", "beta")]
-        with torch.cuda.stream(_torch_stream(self._stream.value, clear[0].device)):
-            for t in clear:
-                t.zero_()
+        _clear([self.out[name] for name in ("q", "k", "v", "g", "beta")], self._stream.value)
         return super().run()
 
 

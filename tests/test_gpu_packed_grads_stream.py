@@ -90,3 +90,21 @@ def test_a_prepared_call_behind_queued_work(make):
         torch.cuda.synchronize()
         for x in want:
             assert torch.equal(got[x], want[x]) and torch.equal(copy[x], want[x]), x
+
+
+@pytest.mark.parametrize("grad_dtype", [F32, torch.bfloat16])
+def test_rows_of_no_sequence_in_both_types(grad_dtype):
+    """Gradients in bf16 beside ones that stay f32 (the delta rule's g and beta), and calls without any token."""
+    for make in (_attn, _delta):
+        got = make()(grad_dtype=grad_dtype)
+        torch.cuda.synchronize()
+        assert got["q"].dtype == grad_dtype
+        for x, t in got.items():
+            assert not t[:, :CU[0]].any() and not t[:, END:].any() and torch.isfinite(t).all() and t.any(), x
+    cu = torch.zeros(3, dtype=torch.int32, device=DEV)
+    q = torch.empty(1, 0, 2, 16, device=DEV)
+    g = ssm.attn_bwd(q, q, q, q, q[..., 0], q, cu_seqlens=cu, grad_dtype=grad_dtype)
+    assert all(t.shape == q.shape for t in g.values())
+    g = ssm.delta_chunk_bwd(q, q, q, q[..., 0], q[..., 0], q, cu_seqlens=cu, grad_dtype=grad_dtype)
+    assert g["k"].shape == q.shape and g["beta"].shape == q.shape[:3]
+    torch.cuda.synchronize()
