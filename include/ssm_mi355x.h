@@ -711,7 +711,8 @@ ssm_status_t ssm_block_norm_bwd_check(const ssm_block_norm_bwd_params_t *p);
  * A NaN or infinity in a row of v that a query does not see may reach it where another
  * query of its tile of 128 (from the sequence's first query on) sees that row; rows that
  * none of these sees, and rows of other sequences, never do.  One in a row of k reaches
- * only the queries that see it.
+ * only the queries that see it.  An infinity in a row of v that a query sees gives it an
+ * infinity or NaN.
  * Workspace: ssm_attn_workspace_size() bytes, 256-byte aligned.
  * Supported: D <= 128, x_dtype and o_dtype f32 or bf16, L and Lk up to 2^30; a launch's
  * 2^32 threads bound the tiles of 64 queries times H to below 2^24.
@@ -755,6 +756,9 @@ ssm_status_t ssm_attn_check(const ssm_attn_params_t *p);
  * One in a row of v reaches only the dq of queries that see it and its own dk; rows of other
  * sequences never reach any.  Queries and keys outside every sequence are not written.
  * Workspace: ssm_attn_bwd_workspace_size() bytes, 256-byte aligned.
+ * Supported: as in ssm_attn_fwd, and tiles of 64 keys (with the pieces of queries that the
+ * sinks' tiles are cut into) times Hk and tiles of 64 queries times half of H, together
+ * below 2^23.
  * ---------------------------------------------------------------------- */
 typedef struct ssm_attn_bwd_params {
   uint32_t struct_size; /* = sizeof(ssm_attn_bwd_params_t) */

@@ -12,7 +12,7 @@
 // gradients' own rounding), in three for f32 ones of bf16 inputs.
 //
 // Bound by the matrix cores, the vector instructions beside them and the reads from LDS: 4 x 2048 tokens, 16/4 heads
-// of 128, window 1024, bf16: 320-344 us, 129 GFLOP by the formulas, 258 with
+// of 128, window 1024, bf16: 320-350 us, 129 GFLOP by the formulas, 258 with
 // both walks and the parts (matrix cores busy 43 % of the time, vector instructions 31 %).
 #pragma once
 #include "attn_device.h"

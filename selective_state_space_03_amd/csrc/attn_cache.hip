@@ -3,10 +3,11 @@
 // A wave takes the keys (or values) of one head of one page that the call meets: the tokens that the page
 // holds already, and the new ones.  8 bits: the page's scale is the least power of two s = 2^e with
 // max |x| <= 448 s over the new ones, or the page's own where that is larger; products with 1 / s are exact.
-// A page of whole 16-byte groups is read at once into registers, up to 16 of them a lane, from which the maximum
-// and the codes are formed; others pass twice over the new rows, for the maximum and (from L2) for the codes.  A
-// page whose scale grows has its codes read and written again.  Bound by the reads and writes: 8192 tokens of 8 heads
-// of 128 in 8 bits 14.8 us, 3.4 TB/s (in two passes 24).
+// Aligned rows whose groups of 8 elements go evenly into the 64 lanes (heads of 8, 16, 32, 64 or 128) are read at once
+// into registers, up to 16 groups a lane (8 in f32), from which the maximum and the codes are formed; others, heads of
+// 40, 80 and 96 among them, pass twice over the new rows, for the maximum and (from L2) for the codes.  A page whose
+// scale grows has its codes read and written again.  Bound by the reads and writes: 8192 tokens of 8 heads of 128 in
+// 8 bits 14.7 us, 3.4 TB/s (in two passes 24).
 #include "attn.h"
 #include "delta_device.h"
 

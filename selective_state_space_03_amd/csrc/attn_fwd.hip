@@ -44,11 +44,12 @@ __global__ __launch_bounds__(256) void attn_fwd_join_kernel(const AttnArgs a) {
 hipError_t attn_fwd_bf16(const AttnLaunch& l, hipStream_t s) {
   const AttnArgs& a = l.a;
   const long blocks = attn_tiles(a, 128, false) * a.h;
-  // 128 queries a workgroup where that fills the CUs twice; where it does not, and the workgroups have 1024
+  // 128 queries a workgroup where that fills the CUs twice; where it does not, and the workgroups may have 1024
   // keys and more to go through, the kernel whose workgroup fills a CU by itself (500 queries behind 15000
   // tokens, 2 x 32 heads of 128: 320 us, with 64 queries a workgroup 486, with the wide kernel 697; 512 of 1024
-  // keys, 8 heads: 23.6 and 23.9 with 64 queries); else 64
-  // queries a workgroup.
+  // keys, 8 heads: 23.6 and 23.9 with 64 queries); else 64 queries a workgroup.  The host knows the keys of a packed
+  // call only in total: a pack of short prompts goes to the kernel for long ones too (32 of 40 tokens, 8 heads of
+  // 128: 20 us, with 64 queries a workgroup 7).
   if (a.vec == 2 && blocks >= 512) return attn_fwd_wide<2>(l, false, s);
   if (a.vec == 2 && a.lk >= 1024 && a.window >= 1024) {
     const hipError_t e = attn_fwd_wide<2>(l, true, s);
