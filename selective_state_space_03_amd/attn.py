@@ -187,7 +187,7 @@ def attn_decode_step(q, k_cache, v_cache, page_table, lens, *, k_scale=None, v_s
                      o=None, o_dtype=None, workspace=None, stream=None, prepare=False):
     """One query of each sequence over its pages (ssm_attn_decode_step): q (batch, H, D); the cache, its scales and
     page_table as in attn_cache_write; lens (batch,) int32 counts the query's own token, which has been written.
-    window, sinks and scale as in attn_fwd; pages that no visible key lies in are not touched.  Returns o
+    window, sinks and scale as in attn_fwd; what pages hold in which no visible key lies does not matter.  Returns o
     (batch, H, D), or with prepare=True a Call that enqueues this same step again on each run()."""
     L_ = lib()
     dev = _gpu(q, "q")
