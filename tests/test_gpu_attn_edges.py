@@ -1,0 +1,112 @@
+"""Window attention at the edges of its calls: packed training recorded in a graph, strides and offsets past 31 bits.
+
+Bounds as for its other tests: f32 1e-5 of the largest value; bf16 results 1e-4 of it, and their own rounding, 2^-8."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_03_amd as ssm
+from gpu_util import DEV, check, np64
+from oracle import attn_oracle as A
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _rnd(seed, dtype, *shapes):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    return [torch.randn(s, generator=gen, device=DEV).to(dtype) for s in shapes]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_packed_training_in_a_graph(dtype):
+    """Forward and backward of packed sequences, captured once; offsets and inputs change between the replays, and every
+    replay equals the eager call bit for bit, zeros in rows of no sequence among it."""
+    q, k, v, do = _rnd(1, dtype, (1, 700, 4, 64), (1, 700, 2, 64), (1, 700, 2, 64), (1, 700, 4, 64))
+    cu = torch.tensor([0, 300, 700], dtype=torch.int32, device=DEV)
+    kw = dict(window=90, sinks=3, cu_seqlens=cu)
+    lse, o = torch.zeros(q.shape[:3], device=DEV), torch.zeros_like(q)
+
+    def step(lse, o):
+        ssm.attn_fwd(q, k, v, lse=lse, o=o, **kw)
+        return ssm.attn_bwd(q, k, v, o, lse, do, grad_dtype=dtype, **kw)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(lse, o)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        rec = step(lse, o)
+    for i, off in enumerate(([0, 300, 700], [50, 51, 400], [0, 0, 64], [699, 700, 700], [0, 650, 690])):
+        cu.copy_(torch.tensor(off, dtype=torch.int32))
+        for t in (q, k, v, do):
+            t.mul_(-0.9)
+        o.zero_()
+        lse.zero_()
+        graph.replay()
+        le, e = torch.zeros_like(lse), torch.zeros_like(o)
+        want = step(le, e)
+        torch.cuda.synchronize()
+        assert torch.equal(o, e) and torch.equal(lse, le), i
+        for x in want:
+            assert torch.equal(rec[x], want[x]), (i, x)
+            assert not rec[x][:, :off[0]].any() and not rec[x][:, off[-1]:].any(), (i, x)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("stride", [1 << 22, (1 << 22) + 8, (1 << 24) + 24, (1 << 24) + 1])
+def test_wide_strides(dtype, stride):
+    """Rows of q, k and v far apart: a tile's rows span more than 31 bits of bytes from some stride on."""
+    L, H, Hk, D = 70, 2, 1, 64
+    whole = torch.full((L * stride + 1024,), float("nan"), dtype=dtype, device=DEV)
+    out = []
+    for at, t in zip((0, 256, 512), _rnd(stride % 1000, dtype, (1, L, H, D), (1, L, Hk, D), (1, L, Hk, D))):
+        view = whole.as_strided(t.shape, (L * stride, stride, D, 1), at)
+        view.copy_(t)
+        out.append(view)
+    q, k, v = out
+    (do,) = _rnd(5, dtype, (1, L, H, D))
+    kw = dict(window=33, sinks=2)
+    lse = torch.empty(q.shape[:3], device=DEV)
+    o = ssm.attn_fwd(q, k, v, lse=lse, **kw)
+    g = ssm.attn_bwd(q, k, v, o, lse, do, grad_dtype=dtype, **kw)
+    torch.cuda.synchronize()
+    ins = [np64(t) for t in (q, k, v)]
+    ro, rl = A.attention(*ins, **kw)
+    rg = A.attention_backward(*ins, np64(do), o=np64(o), **kw)
+    bf, tol = dtype == BF, 1e-4 if dtype == BF else 1e-5
+    check(np64(o), ro, tol, "o", out_bf16=bf)
+    check(np64(lse), rl, 1e-5, "lse")
+    for x in g:
+        check(np64(g[x]), rg[x], tol, "d" + x, out_bf16=bf)
+
+
+def test_tensors_past_31_bits():
+    """More than 2^31 elements in q, o, dout and dq: the last tokens' rows are where they belong."""
+    L, H, Hk, D, n = 270000, 64, 1, 128, 200
+    assert L * H * D > 2 ** 31
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    q, do = torch.zeros(1, L, H, D, dtype=BF, device=DEV), torch.zeros(1, L, H, D, dtype=BF, device=DEV)
+    k, v = (torch.randn(1, L, Hk, D, generator=gen, device=DEV).to(BF) for _ in range(2))
+    for t in (q, do):
+        t[:, -n:] = torch.randn(1, n, H, D, generator=gen, device=DEV).to(BF)
+    lse = torch.empty(q.shape[:3], device=DEV)
+    kw = dict(window=100, sinks=2)
+    o = ssm.attn_fwd(q, k, v, lse=lse, **kw)
+    g = ssm.attn_bwd(q, k, v, o, lse, do, grad_dtype=BF, **kw)
+    torch.cuda.synchronize()
+    # the same queries behind the sinks and the keys that they see alone
+    m = n + 100
+    see = lambda t: torch.cat([t[:, :2], t[:, -m:]], 1)  # noqa: E731
+    ins = [np64(q[:, -n:]), np64(see(k)), np64(see(v))]
+    ro, _ = A.attention(*ins, **kw)
+    rg = A.attention_backward(*ins, np64(do[:, -n:]), o=np64(o[:, -n:]), **kw)
+    check(np64(o[:, -n:]), ro, 1e-4, "o", out_bf16=True)
+    check(np64(g["q"][:, -n:]), rg["q"], 1e-4, "dq", out_bf16=True)
+    assert not g["q"][:, :-n].any()
+    # (earlier queries have dout = 0: no gradient from them)
+    check(np64(g["k"][:, -m:]), rg["k"][:, 2:], 1e-4, "dk", out_bf16=True)
+    check(np64(g["v"][:, -m:]), rg["v"][:, 2:], 1e-4, "dv", out_bf16=True)
+    assert np.isfinite(np64(lse[:, -1])).all()
