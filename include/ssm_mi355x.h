@@ -746,7 +746,7 @@ ssm_status_t ssm_attn_check(const ssm_attn_params_t *p);
  *   dq_p = scale sum_j dS_pj k_j,  dk_j = scale sum_p dS_pj q_p,  dv_j = sum_p P_pj dout_p
  * Key heads shared by several heads receive the sum over them.  Sums are taken in a
  * fixed order, without atomics: results repeat bit for bit.  dout_p.o_p comes from o as
- * it is given: an o in bf16 moves dS_pj by P_pj |dout_p||o_p| 2^-9 at most, which is as
+ * it is given: an o in bf16 moves dS_pj by P_pj |dout_p||o_p| 2^-8 at most, which is as
  * much as the gradients' rounding to bf16 or, where dS is small, several times that; with
  * its o_rest, or in f32, it does not.  P and dS enter their products as they do in the
  * forward (grad_dtype in the place of o_dtype).  A NaN or infinity in a row of k may
