@@ -804,6 +804,9 @@ ssm_status_t ssm_attn_bwd_check(const ssm_attn_bwd_params_t *p);
  * scale or takes a larger one, and its codes are put to that (exactly, but for codes that
  * become subnormal, which are rounded again).  Values are rounded to nearest even;
  * infinities and NaN become NaN.  Rows that no token is put to keep their contents.
+ * A page whose first token here is not its row 0 is taken to hold the rows before, with its
+ * scales: one that is new to the sequence there (its entry was out of range before) wants
+ * scales of 0.
  * Pages that the call writes to belong to one sequence.
  * Supported: D <= 128; page_size up to 65536, table_rows * page_size up to 2^30; the pages
  * met (at most tokens / page_size + 2 num_seqs) times Hk below 2^24.

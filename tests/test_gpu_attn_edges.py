@@ -110,3 +110,23 @@ def test_tensors_past_31_bits():
     check(np64(g["k"][:, -m:]), rg["k"][:, 2:], 1e-4, "dk", out_bf16=True)
     check(np64(g["v"][:, -m:]), rg["v"][:, 2:], 1e-4, "dv", out_bf16=True)
     assert np.isfinite(np64(lse[:, -1])).all()
+
+
+def test_a_page_given_to_a_sequence_in_the_middle():
+    """Rows of a page were not kept when they came; the page that is given later starts with scales of 0, and the tokens
+    from then on are as exact as in a page of their own."""
+    hk, page, D, E4 = 2, 16, 64, torch.float8_e4m3fn
+    (k, v) = _rnd(7, BF, (1, 20, hk, D), (1, 20, hk, D))
+    kc, vc = (torch.zeros(3, hk, page, D, device=DEV).to(E4) for _ in range(2))
+    ks, vs = (torch.full((3, hk), float("nan"), device=DEV) for _ in range(2))
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    ssm.attn_cache_write(k[:, :5].contiguous(), v[:, :5].contiguous(), kc, vc, dev([[-1, 2]]), dev([0]), k_scale=ks, v_scale=vs)
+    ks[1], vs[1] = 0.0, 0.0
+    ssm.attn_cache_write(k[:, 5:].contiguous(), v[:, 5:].contiguous(), kc, vc, dev([[1, 2]]), dev([5]), k_scale=ks, v_scale=vs)
+    torch.cuda.synchronize()
+    for c, s, x in ((kc, ks, k), (vc, vs, v)):
+        got = c[1].float()[:, 5:] * s[1][:, None, None]
+        new = np64(x[0, 5:page].transpose(0, 1))
+        for h in range(hk):
+            want = A.page_scale(new[h])
+            assert s[1, h].item() == want and np.array_equal(np64(got[h]), A.e4m3(new[h] / want) * want)
